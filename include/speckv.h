@@ -338,6 +338,173 @@ spk_status decode_attention(int batch, int layers, int hq, int hkv, int head_dim
                             const void* q_bf16, const void* k_bf16, const void* v_bf16, float* out,
                             void* stream);
 
+/* ------------------------------------------------------------------------
+ * A paged KV cache (section 整体框架: the target model goes on decoding over
+ * the reduced cache; the paper does not say how the cache is kept)
+ *
+ *   k_pages, v_pages [layers][n_pages][hkv][page_rows][head_dim], elements of
+ *                    elem_bytes bytes; a page holds page_rows rows of every
+ *                    layer and KV head
+ *   page_table       int32 [n_seqs][max_pages]: row t of sequence s is row
+ *                    t % page_rows of page page_table[s][t / page_rows]; -1
+ *                    where the sequence has no page
+ *   seq_lens         int32 [n_seqs]: the rows of each sequence
+ *   page_refs        int32 [n_pages]: how many sequences hold the page (0: free)
+ * An empty cache has page_table = -1, seq_lens = 0 and page_refs = 0.  All of
+ * it is on the device and is changed there, in stream order.  Sequences may
+ * hold pages together (kv_pages_fork); rows are only ever written into pages
+ * that one sequence holds.
+ *
+ * Lists of sequences (seqs, src, dst) are int32 device arrays of n <= 1024
+ * entries.  *result (int32, device) tells what became of a call: 0 done; > 0
+ * that many free pages were missing; -1 an argument was wrong (a sequence or a
+ * count out of range, a destination listed twice), recorded as SPK_ERR_ARG in
+ * the device error word too.  Unless it is 0 the call changed nothing.  Free
+ * pages are taken lowest number first, for the sequences in the list's order.
+ * page_table, seq_lens and page_refs need 4-byte alignment, the pages 16.
+ * Calls that change the same cache must not overlap on different streams.
+ *
+ * Supported: head_dim * elem_bytes a multiple of 16; max_pages * page_rows,
+ * n * max_pages, layers * n_pages * hkv < 2^31.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int layers, n_pages, hkv, page_rows, head_dim, elem_bytes;
+  int n_seqs, max_pages;
+} spk_pages_shape;
+
+/* Workspace of kv_pages_reserve, kv_pages_compact and kv_pages_fork over n
+ * sequences: 4 * (n * max_pages + 4 n) bytes (rounded up to 256); 16-byte
+ * aligned. */
+size_t kv_pages_workspace_size(const spk_pages_shape* shape, int n);
+
+/* Sequence seqs[i] grows by n_new[i] >= 0 rows: seq_lens, and pages for the
+ * rows that have none (the rows themselves are left to kv_pages_write).  A
+ * partially filled last page that other sequences hold too is replaced by a
+ * copy of its rows, unless n_new[i] is 0.  No sequence may be listed twice. */
+spk_status kv_pages_reserve(const spk_pages_shape* shape, void* k_pages, void* v_pages, int32_t* page_refs,
+                            int32_t* page_table, int32_t* seq_lens, const int32_t* seqs, const int32_t* n_new, int n,
+                            int32_t* result, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The newest rows of each sequence: for unit u = (i * layers + l) * hkv + h and
+ * t < counts[i],
+ *   row seq_lens[seqs[i]] - counts[i] + t of sequence seqs[i] = k[u][idx[u / units_per_idx][t]],  same for v
+ *   k, v    [n][layers][hkv][n_src][head_dim]
+ *   idx     int32 [n * layers * hkv / units_per_idx][n_idx], each in [0, n_src);
+ *           NULL: row t is row t of k (n_idx <= n_src)
+ *   counts  int32 [n], each in [0, n_idx]; NULL: n_idx
+ * e.g. a prompt's rows (idx NULL), the rows topk_select kept (units_per_idx 1),
+ * or the accepted nodes of a token tree (units_per_idx layers * hkv).  A row
+ * whose index or position is out of range, or whose page is held by another
+ * sequence too, is left unwritten and recorded as SPK_ERR_ARG in the device
+ * error word; so are all rows of a sequence that stands earlier in the list. */
+spk_status kv_pages_write(const spk_pages_shape* shape, const void* k, const void* v, int n_src, const int32_t* idx,
+                          int n_idx, int units_per_idx, const int32_t* counts, const int32_t* page_refs,
+                          const int32_t* page_table, const int32_t* seq_lens, const int32_t* seqs, int n,
+                          void* k_pages, void* v_pages, void* stream);
+
+/* Sequence dst[i] becomes the n_idx rows of sequence src[i] that idx selects,
+ * in pages of its own (kv_compact for a paged cache):
+ *   row t of dst[i] = row idx[u / units_per_idx][t] of src[i], for u = (i * layers + l) * hkv + h
+ *   idx  int32 [n * layers * hkv / units_per_idx][n_idx], each in [0, seq_lens[src[i]])
+ * What dst[i] held is released; src[i] keeps its rows unless it is a
+ * destination of the call (dst[i] == src[i] compacts in place).  The sources
+ * are read as they were before the call; no destination may be listed twice.
+ * An index out of range leaves that row unwritten and is recorded as
+ * SPK_ERR_ARG in the device error word. */
+spk_status kv_pages_compact(const spk_pages_shape* shape, void* k_pages, void* v_pages, int32_t* page_refs,
+                            int32_t* page_table, int32_t* seq_lens, const int32_t* src, const int32_t* dst, int n,
+                            const int32_t* idx, int n_idx, int units_per_idx, int32_t* result, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* Sequence dst[i] becomes the rows of sequence src[i] as it was before the call
+ * (its first n_rows[i] rows where n_rows is given and that is fewer), by
+ * holding their pages: no row is copied.  What dst[i] held is released.  No
+ * destination may be listed twice; a source may, and may be a destination (a
+ * beam search's reordering).  Of the shape, head_dim, elem_bytes, layers and
+ * hkv are not used. */
+spk_status kv_pages_fork(const spk_pages_shape* shape, int32_t* page_refs, int32_t* page_table, int32_t* seq_lens,
+                         const int32_t* src, const int32_t* dst, const int32_t* n_rows, int n, int32_t* result,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* Sequence seqs[i] keeps its first keep_rows[i] rows (none where keep_rows is
+ * NULL); pages behind them are released.  A sequence listed twice keeps the
+ * fewer; an entry out of range is skipped and recorded as SPK_ERR_ARG in the
+ * device error word.  Of the shape, head_dim, elem_bytes, layers and hkv are
+ * not used. */
+spk_status kv_pages_free(const spk_pages_shape* shape, int32_t* page_refs, int32_t* page_table, int32_t* seq_lens,
+                         const int32_t* seqs, const int32_t* keep_rows, int n, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Attention for a tree of drafted tokens over a paged cache (section 整体框架:
+ * a draft model runs ahead of the target; here the target checks its tokens
+ * together)
+ *
+ * Batch element b has T = n_nodes drafted tokens (nodes) behind sequence
+ * s = seqs[b], of which the first n_live[b] count.  Node i of query head qh
+ * attends to the seq_lens[s] rows of the cache and to the nodes j < n_live[b]
+ * with bit j % 32 of mask[b][i][j / 32] set:
+ *   out[b][l][qh][i]  = softmax(scale * q . k) . v over those keys
+ *   lse2[b][l][qh][i] = log2 sum 2^(scale * log2(e) * q . k)   (optional)
+ * A node that sees no key gets out = 0 and lse2 = -inf.  Rows of nodes
+ * i >= n_live[b] are left as they were.  T = 1 is single-token decoding.
+ *
+ *   q               [batch][layers][hq][T][head_dim]
+ *   k_pages, v_pages [layers][n_pages][hkv][page_rows][head_dim]
+ *   page_table      int32 [n_seqs][max_pages], seq_lens int32 [n_seqs]
+ *   seqs            int32 [batch] or NULL (element b is sequence b)
+ *   k_tree, v_tree  [batch][layers][hkv][T][head_dim]; both NULL: the nodes see
+ *                   the cache only
+ *   mask            32-bit words [batch][T][ceil(T / 32)] (tree_mask), or NULL:
+ *                   node i sees the nodes 0 .. i (a chain)
+ *   n_live          int32 [batch] or NULL (T)
+ *   out             like q; lse2 fp32 [batch][layers][hq][T] or NULL
+ *   workspace       tree_attention_workspace_size(shape) bytes, 16-byte
+ *                   aligned, for the shape's device (query it with that device
+ *                   current): the partial results of units that several CTAs
+ *                   share.  It needs no clearing.
+ * q, pages, tree and out are bf16 or fp16 (dtype).  Rows behind a sequence's
+ * length or among the nodes that do not count are never read into a result,
+ * whatever they hold.  An element whose sequence, length or node count is out
+ * of range keeps its output rows and is recorded as SPK_ERR_ARG in the device
+ * error word; a page number out of range is recorded and its rows are read as
+ * zeros.  Weights enter the V product rounded to dtype (fp32 accumulation);
+ * the normaliser and lse2 are formed from the fp32 weights.
+ * Supported: head_dim in {64, 128}; hq % hkv == 0; T <= 1024; batch <= 1024;
+ * page_rows a multiple of 8; layers * n_pages * hkv and the key tiles (of 64)
+ * of all units < 2^31; scale > 0 and finite.
+ * ------------------------------------------------------------------------ */
+typedef enum {
+  SPK_BF16 = 0,
+  SPK_FP16 = 1
+} spk_dtype;
+
+typedef struct {
+  int batch, layers, hq, hkv, head_dim, n_nodes;
+  int n_pages, page_rows, n_seqs, max_pages;
+  int dtype; /* spk_dtype */
+  float scale;
+} spk_tree_shape;
+
+size_t tree_attention_workspace_size(const spk_tree_shape* shape);
+
+spk_status tree_attention(const spk_tree_shape* shape, const void* q, const void* k_pages, const void* v_pages,
+                          const int32_t* page_table, const int32_t* seq_lens, const int32_t* seqs,
+                          const void* k_tree, const void* v_tree, const uint32_t* mask, const int32_t* n_live,
+                          void* out, float* lse2, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The visibility words of trees given by their nodes' parents:
+ *   parents int32 [batch][n_nodes]: the node before node i, in [-1, i); -1:
+ *           node i follows the cache's last row
+ *   mask    words [batch][n_nodes][ceil(n_nodes / 32)]: bit j of node i is set
+ *           where j is i or one of its ancestors; 0 for nodes >= n_live[b]
+ *   depth   int32 [batch][n_nodes] or NULL: how many ancestors a node has (its
+ *           position is seq_lens + depth); 0 for nodes >= n_live[b]
+ * A parent outside [-1, i) counts as -1, an n_live outside [0, n_nodes] as the
+ * nearer end; both are recorded as SPK_ERR_ARG in the device error word.
+ * Supported: n_nodes <= 1024; batch <= 65535. */
+spk_status tree_mask(int batch, int n_nodes, const int32_t* parents, const int32_t* n_live, uint32_t* mask,
+                     int32_t* depth, void* stream);
+
 /* Device address of page-locked, device-mapped host memory (a deployment
  * helper; the paper has no counterpart).  k and v of kv_compact may point
  * into such memory: the gather then reads only the selected rows over the
@@ -358,7 +525,8 @@ const char* spk_last_error(void);
 /* Synchronises the current device, then reports an error recorded by a
  * kernel since the last clear: *status = SPK_OK, SPK_ERR_TIMEOUT (a bounded
  * device wait ran out; *site says where) or SPK_ERR_ARG (an index out of
- * range in kv_compact or vs_sparse_attention).  Each source file of the
+ * range in kv_compact, vs_sparse_attention, the kv_pages operators,
+ * tree_attention or tree_mask).  Each source file of the
  * library keeps its own first-error word; the first set one, in a fixed
  * order of the files, is reported.  clear != 0 resets them all.  Returns
  * SPK_ERR_CUDA if the device could not be read. */

@@ -21,6 +21,8 @@ from .binding import (  # noqa: F401
     topk_workspace_size, topk_select, kv_compact, decode_attention,
     spk_device_error, spk_selftest_wait_timeout, spk_exp2_fma, mapped_host_pointer,
     SPK_POOL_MAX, SPK_POOL_AVG, vs_workspace_size, vs_sparse_attention,
+    pages_shape, kv_pages_workspace_size, kv_pages_reserve, kv_pages_write, kv_pages_compact, kv_pages_fork,
+    kv_pages_free, tree_shape, tree_attention_workspace_size, tree_attention, tree_mask,
 )
 from .pipeline import speckv_compress, specpc_select, cascade_compress  # noqa: F401
 
@@ -30,5 +32,8 @@ __all__ = [
     "speckv_prefill_attention", "specpc_workspace_size", "specpc_score", "specpc_row_offsets", "specpc_colsum",
     "topk_workspace_size", "topk_select", "kv_compact", "decode_attention",
     "spk_device_error", "spk_selftest_wait_timeout", "spk_exp2_fma", "mapped_host_pointer",
-    "SPK_POOL_MAX", "SPK_POOL_AVG", "vs_workspace_size", "vs_sparse_attention", "speckv_compress", "specpc_select", "cascade_compress",
+    "SPK_POOL_MAX", "SPK_POOL_AVG", "vs_workspace_size", "vs_sparse_attention",
+    "pages_shape", "kv_pages_workspace_size", "kv_pages_reserve", "kv_pages_write", "kv_pages_compact",
+    "kv_pages_fork", "kv_pages_free", "tree_shape", "tree_attention_workspace_size", "tree_attention", "tree_mask",
+    "speckv_compress", "specpc_select", "cascade_compress",
 ]

@@ -50,6 +50,19 @@ class VsShape(ctypes.Structure):
                 ("n_vertical", ctypes.c_int), ("n_slash", ctypes.c_int), ("scale", ctypes.c_float)]
 
 
+class PagesShape(ctypes.Structure):
+    _fields_ = [("layers", ctypes.c_int), ("n_pages", ctypes.c_int), ("hkv", ctypes.c_int),
+                ("page_rows", ctypes.c_int), ("head_dim", ctypes.c_int), ("elem_bytes", ctypes.c_int),
+                ("n_seqs", ctypes.c_int), ("max_pages", ctypes.c_int)]
+
+
+class TreeShape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("layers", ctypes.c_int), ("hq", ctypes.c_int),
+                ("hkv", ctypes.c_int), ("head_dim", ctypes.c_int), ("n_nodes", ctypes.c_int),
+                ("n_pages", ctypes.c_int), ("page_rows", ctypes.c_int), ("n_seqs", ctypes.c_int),
+                ("max_pages", ctypes.c_int), ("dtype", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
 def library_path() -> str:
     return _LIB_PATH
 
@@ -66,6 +79,8 @@ def load_library():
     sk = ctypes.POINTER(SpeckvShape)
     sp = ctypes.POINTER(SpecpcShape)
     vsp = ctypes.POINTER(VsShape)
+    pg = ctypes.POINTER(PagesShape)
+    tr = ctypes.POINTER(TreeShape)
     sig = {
         "speckv_workspace_size": (sz, [sk]),
         "speckv_score": (I, [sk, vp, vp, vp, vp, vp, sz, vp]),
@@ -89,6 +104,15 @@ def load_library():
         "decode_attention": (I, [I, I, I, I, I, I, F, vp, vp, vp, vp, vp]),
         "vs_workspace_size": (sz, [vsp]),
         "vs_sparse_attention": (I, [vsp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "kv_pages_workspace_size": (sz, [pg, I]),
+        "kv_pages_reserve": (I, [pg, vp, vp, vp, vp, vp, vp, vp, I, vp, vp, sz, vp]),
+        "kv_pages_write": (I, [pg, vp, vp, I, vp, I, I, vp, vp, vp, vp, vp, I, vp, vp, vp]),
+        "kv_pages_compact": (I, [pg, vp, vp, vp, vp, vp, vp, vp, I, vp, I, I, vp, vp, sz, vp]),
+        "kv_pages_fork": (I, [pg, vp, vp, vp, vp, vp, vp, I, vp, vp, sz, vp]),
+        "kv_pages_free": (I, [pg, vp, vp, vp, vp, vp, I, vp]),
+        "tree_attention_workspace_size": (sz, [tr]),
+        "tree_attention": (I, [tr, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "tree_mask": (I, [I, I, vp, vp, vp, vp, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -453,6 +477,271 @@ def vs_sparse_attention(q, k, v, vertical, slash, out=None, lse2=None, workspace
                                    _dev(lse2, "lse2", torch.float32), _dev(ws, "workspace"),
                                    ws.numel() * ws.element_size() if ws is not None else 0, _stream(stream)))
     return out
+
+
+# --------------------------------------------------------------------- paged cache, tree attention
+# These entry points launch on the device of their tensors, whichever device
+# is current, and refuse tensors of several devices.
+def _cuda_device(t: torch.Tensor, name: str) -> torch.device:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _ptr(t: Optional[torch.Tensor], name: str, dtype, dev, numel: Optional[int] = None) -> Optional[int]:
+    """Data pointer of a contiguous tensor of `dtype` (None: any) on `dev`; None for None."""
+    if t is None:
+        return None
+    if t.device != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on {dev}, got one on {t.device}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if numel is not None and t.numel() != numel:
+        raise ValueError(f"{name} has {t.numel()} elements, the call needs {numel}")
+    return t.data_ptr()
+
+
+def _launch(dev, stream, fn, *args):
+    """fn(*args, stream) with `dev` current."""
+    if isinstance(stream, torch.cuda.Stream) and stream.device != dev:
+        raise ValueError(f"the stream is one of {stream.device}, the tensors are on {dev}")
+    if torch.cuda.current_device() == dev.index:
+        _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(stream)))
+
+
+def _new(shape, dtype, dev, stream) -> torch.Tensor:
+    """An output of a call on `stream`: allocated there, and known to the
+    caller's stream too, so that its memory is not given away while either uses it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(_stream_object(stream, dev)):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    t.record_stream(torch.cuda.current_stream(dev))
+    return t
+
+
+def _scratch(ws: Optional[torch.Tensor], nbytes: int, dev, stream) -> torch.Tensor:
+    """The caller's workspace, or a temporary one on the launch stream."""
+    if ws is None:
+        ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev) if stream is None else \
+            _workspace(None, nbytes, dev, stream)
+    return ws
+
+
+def pages_shape(k_pages, v_pages, page_refs, page_table, seq_lens) -> PagesShape:
+    if k_pages.dim() != 5 or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype:
+        raise ValueError("k_pages and v_pages are [L, n_pages, Hkv, page_rows, d], of the same dtype")
+    L, n_pages, hkv, rows, d = k_pages.shape
+    return _table_shape(page_refs, page_table, seq_lens, rows, (L, hkv, d, k_pages.element_size()), n_pages)
+
+
+def _table_shape(page_refs, page_table, seq_lens, page_rows, lhde=(1, 1, 16, 1), n_pages=None) -> PagesShape:
+    if page_table.dim() != 2:
+        raise ValueError("page_table is [n_seqs, max_pages]")
+    n_seqs, max_pages = page_table.shape
+    if n_pages is None:
+        n_pages = page_refs.numel()
+    if page_refs.numel() != n_pages:
+        raise ValueError(f"page_refs has {page_refs.numel()} elements, the call needs {n_pages}")
+    if seq_lens.numel() != n_seqs:
+        raise ValueError(f"seq_lens has {seq_lens.numel()} elements, the call needs {n_seqs}")
+    return PagesShape(lhde[0], n_pages, lhde[1], int(page_rows), lhde[2], lhde[3], n_seqs, max_pages)
+
+
+def kv_pages_workspace_size(shape: PagesShape, n: int) -> int:
+    return int(load_library().kv_pages_workspace_size(ctypes.byref(shape), n))
+
+
+def _book(page_refs, page_table, seq_lens, dev):
+    i32 = torch.int32
+    return (_ptr(page_refs, "page_refs", i32, dev), _ptr(page_table, "page_table", i32, dev),
+            _ptr(seq_lens, "seq_lens", i32, dev))
+
+
+def _result(result, dev, stream):
+    if result is None:
+        result = _new((1,), torch.int32, dev, stream)
+    return result, _ptr(result, "result", torch.int32, dev, 1)
+
+
+def kv_pages_reserve(k_pages, v_pages, page_refs, page_table, seq_lens, seqs, n_new, result=None, workspace=None,
+                     stream=None):
+    """Sequences seqs int32 [n] grow by n_new int32 [n] rows: their lengths, pages
+    for the new rows, and a copy of a partially filled last page that other
+    sequences hold too.  Returns result int32 [1] (on the device): 0 done, > 0
+    that many pages were missing, -1 a wrong argument; nothing changed unless 0."""
+    lib = load_library()
+    dev = _cuda_device(k_pages, "k_pages")
+    shape = pages_shape(k_pages, v_pages, page_refs, page_table, seq_lens)
+    n = seqs.numel()
+    result, res = _result(result, dev, stream)
+    ws = _scratch(workspace, kv_pages_workspace_size(shape, n), dev, stream)
+    _launch(dev, stream, lib.kv_pages_reserve, ctypes.byref(shape), _ptr(k_pages, "k_pages", None, dev),
+            _ptr(v_pages, "v_pages", None, dev), *_book(page_refs, page_table, seq_lens, dev),
+            _ptr(seqs, "seqs", torch.int32, dev), _ptr(n_new, "n_new", torch.int32, dev, n), n, res,
+            _ptr(ws, "workspace", None, dev), ws.numel() * ws.element_size())
+    return result
+
+
+def kv_pages_write(k, v, k_pages, v_pages, page_refs, page_table, seq_lens, seqs, idx=None, counts=None,
+                   units_per_idx: int = 1, stream=None):
+    """The newest rows of sequences seqs int32 [n] from k, v [n, L, Hkv, n_src, d]:
+    the rows idx int32 [n * L * Hkv / units_per_idx, n_idx] selects (None: all),
+    of which the first counts int32 [n] are written (None: all)."""
+    lib = load_library()
+    dev = _cuda_device(k_pages, "k_pages")
+    shape = pages_shape(k_pages, v_pages, page_refs, page_table, seq_lens)
+    n = seqs.numel()
+    if k.dim() != 5 or k.shape != v.shape or tuple(k.shape[:3]) != (n, shape.layers, shape.hkv) \
+            or k.shape[4] != shape.head_dim:
+        raise ValueError("k and v are [n, L, Hkv, n_src, d] with the pages' L, Hkv and d")
+    if k.dtype != k_pages.dtype or v.dtype != k_pages.dtype:
+        raise ValueError(f"k and v must be {k_pages.dtype} like the pages")
+    n_src, units = k.shape[3], n * shape.layers * shape.hkv
+    n_idx = n_src if idx is None else idx.shape[-1]
+    if units_per_idx < 1 or units % units_per_idx:
+        raise ValueError(f"units ({units}) must be a multiple of units_per_idx ({units_per_idx})")
+    _launch(dev, stream, lib.kv_pages_write, ctypes.byref(shape), _ptr(k, "k", None, dev), _ptr(v, "v", None, dev),
+            n_src, _ptr(idx, "idx", torch.int32, dev, units // units_per_idx * n_idx), n_idx, units_per_idx,
+            _ptr(counts, "counts", torch.int32, dev, n), *_book(page_refs, page_table, seq_lens, dev),
+            _ptr(seqs, "seqs", torch.int32, dev), n, _ptr(k_pages, "k_pages", None, dev),
+            _ptr(v_pages, "v_pages", None, dev))
+
+
+def kv_pages_compact(k_pages, v_pages, page_refs, page_table, seq_lens, src, dst, idx, units_per_idx: int = 1,
+                     result=None, workspace=None, stream=None):
+    """Sequences dst int32 [n] become the rows idx int32 [n * L * Hkv /
+    units_per_idx, n_idx] of sequences src int32 [n], in pages of their own
+    (dst = src: in place).  Returns result as kv_pages_reserve does."""
+    lib = load_library()
+    dev = _cuda_device(k_pages, "k_pages")
+    shape = pages_shape(k_pages, v_pages, page_refs, page_table, seq_lens)
+    n, n_idx = src.numel(), idx.shape[-1]
+    units = n * shape.layers * shape.hkv
+    if units_per_idx < 1 or units % units_per_idx:
+        raise ValueError(f"units ({units}) must be a multiple of units_per_idx ({units_per_idx})")
+    result, res = _result(result, dev, stream)
+    ws = _scratch(workspace, kv_pages_workspace_size(shape, n), dev, stream)
+    _launch(dev, stream, lib.kv_pages_compact, ctypes.byref(shape), _ptr(k_pages, "k_pages", None, dev),
+            _ptr(v_pages, "v_pages", None, dev), *_book(page_refs, page_table, seq_lens, dev),
+            _ptr(src, "src", torch.int32, dev), _ptr(dst, "dst", torch.int32, dev, n), n,
+            _ptr(idx, "idx", torch.int32, dev, units // units_per_idx * n_idx), n_idx, units_per_idx, res,
+            _ptr(ws, "workspace", None, dev), ws.numel() * ws.element_size())
+    return result
+
+
+def kv_pages_fork(page_refs, page_table, seq_lens, src, dst, page_rows: int, n_rows=None, result=None, workspace=None,
+                  stream=None):
+    """Sequences dst int32 [n] become sequences src int32 [n] as they were before
+    the call (their first n_rows int32 [n] rows where given), by holding their
+    pages.  Returns result as kv_pages_reserve does."""
+    lib = load_library()
+    dev = _cuda_device(page_table, "page_table")
+    shape = _table_shape(page_refs, page_table, seq_lens, page_rows)
+    n = src.numel()
+    result, res = _result(result, dev, stream)
+    ws = _scratch(workspace, kv_pages_workspace_size(shape, n), dev, stream)
+    _launch(dev, stream, lib.kv_pages_fork, ctypes.byref(shape), *_book(page_refs, page_table, seq_lens, dev),
+            _ptr(src, "src", torch.int32, dev), _ptr(dst, "dst", torch.int32, dev, n),
+            _ptr(n_rows, "n_rows", torch.int32, dev, n), n, res, _ptr(ws, "workspace", None, dev),
+            ws.numel() * ws.element_size())
+    return result
+
+
+def kv_pages_free(page_refs, page_table, seq_lens, seqs, page_rows: int, keep_rows=None, stream=None):
+    """Sequences seqs int32 [n] keep their first keep_rows int32 [n] rows (None:
+    none); the pages behind them are released."""
+    lib = load_library()
+    dev = _cuda_device(page_table, "page_table")
+    shape = _table_shape(page_refs, page_table, seq_lens, page_rows)
+    n = seqs.numel()
+    _launch(dev, stream, lib.kv_pages_free, ctypes.byref(shape), *_book(page_refs, page_table, seq_lens, dev),
+            _ptr(seqs, "seqs", torch.int32, dev), _ptr(keep_rows, "keep_rows", torch.int32, dev, n), n)
+
+
+SPK_BF16, SPK_FP16 = 0, 1
+_TREE_DTYPES = {torch.bfloat16: SPK_BF16, torch.float16: SPK_FP16}
+
+
+def tree_shape(q, k_pages, page_table, scale: float = 1.0) -> TreeShape:
+    if q.dim() != 5 or k_pages.dim() != 5 or page_table.dim() != 2:
+        raise ValueError("q is [B, L, Hq, T, d], k_pages [L, n_pages, Hkv, page_rows, d], page_table [n_seqs, max_pages]")
+    Bsz, L, hq, T, d = q.shape
+    Lk, n_pages, hkv, rows, dk = k_pages.shape
+    if (L, d) != (Lk, dk):
+        raise ValueError("q and k_pages disagree on layers or head_dim")
+    if q.dtype not in _TREE_DTYPES:
+        raise ValueError(f"q must be bfloat16 or float16, got {q.dtype}")
+    n_seqs, max_pages = page_table.shape
+    return TreeShape(Bsz, L, hq, hkv, d, T, n_pages, rows, n_seqs, max_pages, _TREE_DTYPES[q.dtype], float(scale))
+
+
+def tree_attention_workspace_size(shape: TreeShape) -> int:
+    return int(load_library().tree_attention_workspace_size(ctypes.byref(shape)))
+
+
+def tree_attention(q, k_pages, v_pages, page_table, seq_lens, k_tree=None, v_tree=None, mask=None, n_live=None,
+                   seqs=None, out=None, lse2=None, workspace=None, scale: float = 1.0, stream=None):
+    """Attention of T drafted tokens a batch element, q [B, L, Hq, T, d], over
+    their sequence's cached rows and the tokens k_tree, v_tree [B, L, Hkv, T, d]
+    that mask int32 [B, T, ceil(T/32)] lets each see (None: a chain).  seqs
+    int32 [B]: the elements' sequences (None: 0 .. B-1); n_live int32 [B]: how
+    many of the tokens count (None: T).  Returns out [B, L, Hq, T, d]; fills
+    lse2 fp32 [B, L, Hq, T] when given."""
+    lib = load_library()
+    dev = _cuda_device(q, "q")
+    shape = tree_shape(q, k_pages, page_table, scale)
+    Bsz, L, hq, T, d = q.shape
+    if v_pages.shape != k_pages.shape:
+        raise ValueError("v_pages must have k_pages' shape")
+    if (k_tree is None) != (v_tree is None):
+        raise ValueError("k_tree and v_tree are given together or not at all")
+    if k_tree is not None:
+        tree = (Bsz, L, shape.hkv, T, d)
+        if tuple(k_tree.shape) != tree or tuple(v_tree.shape) != tree:
+            raise ValueError(f"k_tree and v_tree must be {list(tree)}")
+    if out is None:
+        out = _new(q.shape, q.dtype, dev, stream)
+    i32 = torch.int32
+    if torch.cuda.current_device() == dev.index:
+        need = tree_attention_workspace_size(shape)
+    else:
+        with torch.cuda.device(dev):
+            need = tree_attention_workspace_size(shape)
+    ws = _scratch(workspace, need, dev, stream)
+    _launch(dev, stream, lib.tree_attention, ctypes.byref(shape), _ptr(q, "q", None, dev),
+            _ptr(k_pages, "k_pages", q.dtype, dev), _ptr(v_pages, "v_pages", q.dtype, dev),
+            _ptr(page_table, "page_table", i32, dev), _ptr(seq_lens, "seq_lens", i32, dev, shape.n_seqs),
+            _ptr(seqs, "seqs", i32, dev, Bsz), _ptr(k_tree, "k_tree", q.dtype, dev),
+            _ptr(v_tree, "v_tree", q.dtype, dev), _ptr(mask, "mask", i32, dev, Bsz * T * ((T + 31) // 32)),
+            _ptr(n_live, "n_live", i32, dev, Bsz), _ptr(out, "out", q.dtype, dev, q.numel()),
+            _ptr(lse2, "lse2", torch.float32, dev, Bsz * L * hq * T), _ptr(ws, "workspace", None, dev),
+            ws.numel() * ws.element_size())
+    return out
+
+
+def tree_mask(parents, n_live=None, mask=None, depth=None, stream=None):
+    """Visibility words int32 [B, T, ceil(T/32)] and depths int32 [B, T] of trees
+    given by parents int32 [B, T] (the node before node i, in [-1, i))."""
+    lib = load_library()
+    if parents.dim() != 2:
+        raise ValueError("parents is [B, T]")
+    dev = _cuda_device(parents, "parents")
+    Bsz, T = parents.shape
+    words = (T + 31) // 32
+    if mask is None:
+        mask = _new((Bsz, T, words), torch.int32, dev, stream)
+    if depth is None:
+        depth = _new((Bsz, T), torch.int32, dev, stream)
+    i32 = torch.int32
+    _launch(dev, stream, lib.tree_mask, Bsz, T, _ptr(parents, "parents", i32, dev), _ptr(n_live, "n_live", i32, dev, Bsz),
+            _ptr(mask, "mask", i32, dev, Bsz * T * words), _ptr(depth, "depth", i32, dev, Bsz * T))
+    return mask, depth
 
 
 # --------------------------------------------------------------------- errors

@@ -12,6 +12,7 @@
 #include "../../include/speckv.h"
 #include "common.cuh"
 #include "exp2_poly.cuh"
+#include "paged.cuh"
 #include "score.cuh"
 
 namespace spk {
@@ -617,6 +618,276 @@ spk_status decode_attention(int batch, int layers, int hq, int hkv, int head_dim
   return ok();
 }
 
+// --------------------------------------------------------------------- paged cache
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// The table's part of a shape, and the list's length.
+static spk_status check_pages_table(const spk_pages_shape* s, int n) {
+  if (s == nullptr) return fail(SPK_ERR_ARG, "shape is NULL");
+  if (s->n_pages < 1 || s->page_rows < 1 || s->n_seqs < 1 || s->max_pages < 1)
+    return fail(SPK_ERR_ARG, "n_pages, page_rows, n_seqs and max_pages must be >= 1");
+  if (n < 0) return fail(SPK_ERR_ARG, "n must be >= 0");
+  if (n > kPagesMaxCall) return fail(SPK_ERR_UNSUPPORTED, "%d sequences in a call: at most %d", n, kPagesMaxCall);
+  if (static_cast<long long>(s->max_pages) * s->page_rows > 0x7fffffffLL ||
+      static_cast<long long>(n) * s->max_pages > 0x7fffffffLL)
+    return fail(SPK_ERR_UNSUPPORTED, "max_pages * page_rows or n * max_pages is too large");
+  return SPK_OK;
+}
+
+static spk_status check_pages(const spk_pages_shape* s, int n) {
+  spk_status st = check_pages_table(s, n);
+  if (st != SPK_OK) return st;
+  if (s->layers < 1 || s->hkv < 1 || s->head_dim < 1 || s->elem_bytes < 1)
+    return fail(SPK_ERR_ARG, "layers, hkv, head_dim and elem_bytes must be >= 1");
+  if (static_cast<long long>(s->head_dim) * s->elem_bytes % 16 != 0 ||
+      static_cast<long long>(s->head_dim) * s->elem_bytes > (1 << 20))
+    return fail(SPK_ERR_UNSUPPORTED, "head_dim * elem_bytes = %lld must be a multiple of 16 (at most 1 MiB)",
+                static_cast<long long>(s->head_dim) * s->elem_bytes);
+  if (static_cast<long long>(s->layers) * s->n_pages > 0x7fffffffLL / s->hkv)
+    return fail(SPK_ERR_UNSUPPORTED, "layers * n_pages * hkv is too large");
+  return SPK_OK;
+}
+
+static PagesShape pages_shape(const spk_pages_shape* s) {
+  return {s->layers, s->n_pages, s->hkv, s->page_rows, static_cast<int>(static_cast<long long>(s->head_dim) * s->elem_bytes / 16),
+          s->n_seqs, s->max_pages};
+}
+
+static spk_status check_book(const int32_t* refs, const int32_t* table, const int32_t* lens) {
+  if (refs == nullptr || table == nullptr || lens == nullptr)
+    return fail(SPK_ERR_ARG, "page_refs, page_table and seq_lens must be non-NULL device pointers");
+  if (!aligned4(refs) || !aligned4(table) || !aligned4(lens))
+    return fail(SPK_ERR_ARG, "page_refs, page_table and seq_lens must be 4-byte aligned");
+  return SPK_OK;
+}
+
+static spk_status check_pool(const void* k, const void* v) {
+  if (k == nullptr || v == nullptr) return fail(SPK_ERR_ARG, "k_pages and v_pages must be non-NULL device pointers");
+  if (!aligned16(k) || !aligned16(v)) return fail(SPK_ERR_ARG, "k_pages and v_pages must be 16-byte aligned");
+  return SPK_OK;
+}
+
+static spk_status check_pages_ws(const void* ws, size_t bytes, size_t need) {
+  if (ws == nullptr || bytes < need)
+    return fail(SPK_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu needed", ws ? bytes : size_t(0), need);
+  if (!aligned16(ws)) return fail(SPK_ERR_ARG, "workspace must be 16-byte aligned");
+  return SPK_OK;
+}
+
+size_t kv_pages_workspace_size(const spk_pages_shape* s, int n) {
+  if (check_pages_table(s, n) != SPK_OK) return 0;
+  return round_up(pages_ws_bytes(n, s->max_pages), 256);
+}
+
+spk_status kv_pages_reserve(const spk_pages_shape* s, void* k_pages, void* v_pages, int32_t* refs, int32_t* table,
+                            int32_t* lens, const int32_t* seqs, const int32_t* n_new, int n, int32_t* result, void* ws,
+                            size_t ws_bytes, void* stream) {
+  spk_status st = check_pages(s, n);
+  if (st == SPK_OK) st = check_book(refs, table, lens);
+  if (st == SPK_OK) st = check_pool(k_pages, v_pages);
+  if (st != SPK_OK) return st;
+  if (result == nullptr || (n > 0 && (seqs == nullptr || n_new == nullptr)))
+    return fail(SPK_ERR_ARG, "seqs, n_new and result must be non-NULL device pointers");
+  if ((st = check_pages_ws(ws, ws_bytes, pages_ws_bytes(n, s->max_pages))) != SPK_OK) return st;
+  cudaError_t e = launch_pages_reserve(pages_shape(s), {refs, table, lens}, k_pages, v_pages, seqs, n_new, n, result,
+                                       ws, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ok() : cuda_fail(e, "kv_pages_reserve launch");
+}
+
+spk_status kv_pages_write(const spk_pages_shape* s, const void* k, const void* v, int n_src, const int32_t* idx,
+                          int n_idx, int units_per_idx, const int32_t* counts, const int32_t* refs,
+                          const int32_t* table, const int32_t* lens, const int32_t* seqs, int n, void* k_pages,
+                          void* v_pages, void* stream) {
+  spk_status st = check_pages(s, n);
+  if (st == SPK_OK) st = check_book(refs, table, lens);
+  if (st == SPK_OK) st = check_pool(k_pages, v_pages);
+  if (st != SPK_OK) return st;
+  if (n_src < 0 || n_idx < 0) return fail(SPK_ERR_ARG, "n_src and n_idx must be >= 0");
+  const long long units = static_cast<long long>(n) * s->layers * s->hkv;
+  if (units > 0x7fffffffLL) return fail(SPK_ERR_UNSUPPORTED, "n * layers * hkv is too large");
+  if (units_per_idx < 1 || units % units_per_idx != 0)
+    return fail(SPK_ERR_ARG, "n * layers * hkv (%lld) must be a multiple of units_per_idx (%d)", units, units_per_idx);
+  if (n == 0 || n_idx == 0) return ok();
+  if (k == nullptr || v == nullptr || seqs == nullptr)
+    return fail(SPK_ERR_ARG, "k, v and seqs must be non-NULL device pointers");
+  if (!aligned16(k) || !aligned16(v)) return fail(SPK_ERR_ARG, "k and v must be 16-byte aligned");
+  if (idx == nullptr && n_idx > n_src) return fail(SPK_ERR_ARG, "without idx, n_idx (%d) is at most n_src (%d)", n_idx, n_src);
+  cudaError_t e = launch_pages_write(pages_shape(s), {const_cast<int*>(refs), const_cast<int*>(table), const_cast<int*>(lens)},
+                                     k, v, n_src, idx, n_idx, units_per_idx, counts, seqs, n, k_pages, v_pages,
+                                     static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ok() : cuda_fail(e, "kv_pages_write launch");
+}
+
+spk_status kv_pages_compact(const spk_pages_shape* s, void* k_pages, void* v_pages, int32_t* refs, int32_t* table,
+                            int32_t* lens, const int32_t* src, const int32_t* dst, int n, const int32_t* idx, int n_idx,
+                            int units_per_idx, int32_t* result, void* ws, size_t ws_bytes, void* stream) {
+  spk_status st = check_pages(s, n);
+  if (st == SPK_OK) st = check_book(refs, table, lens);
+  if (st == SPK_OK) st = check_pool(k_pages, v_pages);
+  if (st != SPK_OK) return st;
+  if (n_idx < 0 || n_idx > static_cast<long long>(s->max_pages) * s->page_rows)
+    return fail(SPK_ERR_ARG, "need 0 <= n_idx <= max_pages * page_rows");
+  const long long units = static_cast<long long>(n) * s->layers * s->hkv;
+  if (units > 0x7fffffffLL) return fail(SPK_ERR_UNSUPPORTED, "n * layers * hkv is too large");
+  if (units_per_idx < 1 || units % units_per_idx != 0)
+    return fail(SPK_ERR_ARG, "n * layers * hkv (%lld) must be a multiple of units_per_idx (%d)", units, units_per_idx);
+  if (result == nullptr || (n > 0 && (src == nullptr || dst == nullptr || (n_idx > 0 && idx == nullptr))))
+    return fail(SPK_ERR_ARG, "src, dst, idx and result must be non-NULL device pointers");
+  if ((st = check_pages_ws(ws, ws_bytes, pages_ws_bytes(n, s->max_pages))) != SPK_OK) return st;
+  cudaError_t e = launch_pages_compact(pages_shape(s), {refs, table, lens}, k_pages, v_pages, src, dst, n, idx, n_idx,
+                                       units_per_idx, result, ws, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ok() : cuda_fail(e, "kv_pages_compact launch");
+}
+
+spk_status kv_pages_fork(const spk_pages_shape* s, int32_t* refs, int32_t* table, int32_t* lens, const int32_t* src,
+                         const int32_t* dst, const int32_t* n_rows, int n, int32_t* result, void* ws, size_t ws_bytes,
+                         void* stream) {
+  spk_status st = check_pages_table(s, n);
+  if (st == SPK_OK) st = check_book(refs, table, lens);
+  if (st != SPK_OK) return st;
+  if (result == nullptr || (n > 0 && (src == nullptr || dst == nullptr)))
+    return fail(SPK_ERR_ARG, "src, dst and result must be non-NULL device pointers");
+  if ((st = check_pages_ws(ws, ws_bytes, pages_ws_bytes(n, s->max_pages))) != SPK_OK) return st;
+  PagesShape g{1, s->n_pages, 1, s->page_rows, 1, s->n_seqs, s->max_pages};
+  cudaError_t e = launch_pages_fork(g, {refs, table, lens}, src, dst, n_rows, n, result, ws,
+                                    static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ok() : cuda_fail(e, "kv_pages_fork launch");
+}
+
+spk_status kv_pages_free(const spk_pages_shape* s, int32_t* refs, int32_t* table, int32_t* lens, const int32_t* seqs,
+                         const int32_t* keep_rows, int n, void* stream) {
+  spk_status st = check_pages_table(s, n);
+  if (st == SPK_OK) st = check_book(refs, table, lens);
+  if (st != SPK_OK) return st;
+  if (n == 0) return ok();
+  if (seqs == nullptr) return fail(SPK_ERR_ARG, "seqs must be a non-NULL device pointer");
+  PagesShape g{1, s->n_pages, 1, s->page_rows, 1, s->n_seqs, s->max_pages};
+  cudaError_t e = launch_pages_free(g, {refs, table, lens}, seqs, keep_rows, n, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ok() : cuda_fail(e, "kv_pages_free launch");
+}
+
+// --------------------------------------------------------------------- tree attention
+static spk_status check_tree(const spk_tree_shape* s) {
+  if (s == nullptr) return fail(SPK_ERR_ARG, "shape is NULL");
+  if (s->batch < 1 || s->layers < 1 || s->hq < 1 || s->hkv < 1 || s->n_nodes < 1 || s->n_pages < 1 ||
+      s->page_rows < 1 || s->n_seqs < 1 || s->max_pages < 1)
+    return fail(SPK_ERR_ARG, "batch, layers, hq, hkv, n_nodes, n_pages, page_rows, n_seqs and max_pages must be >= 1");
+  if (s->hq % s->hkv != 0) return fail(SPK_ERR_ARG, "hq (%d) must be a multiple of hkv (%d)", s->hq, s->hkv);
+  if (s->dtype != SPK_BF16 && s->dtype != SPK_FP16) return fail(SPK_ERR_ARG, "dtype must be SPK_BF16 or SPK_FP16");
+  if (!(s->scale > 0.f) || !std::isfinite(s->scale)) return fail(SPK_ERR_ARG, "scale must be finite and > 0");
+  if (s->head_dim != 64 && s->head_dim != 128)
+    return fail(SPK_ERR_UNSUPPORTED, "head_dim %d not supported (64 or 128)", s->head_dim);
+  if (s->n_nodes > kTreeMaxNodes) return fail(SPK_ERR_UNSUPPORTED, "n_nodes %d exceeds %d", s->n_nodes, kTreeMaxNodes);
+  if (s->batch > kTreeMaxBatch) return fail(SPK_ERR_UNSUPPORTED, "batch %d exceeds %d", s->batch, kTreeMaxBatch);
+  if (s->page_rows % 8 != 0) return fail(SPK_ERR_UNSUPPORTED, "page_rows (%d) must be a multiple of 8", s->page_rows);
+  const long long rows = static_cast<long long>(s->hq / s->hkv) * s->n_nodes;
+  const long long most = static_cast<long long>(s->max_pages) * s->page_rows;
+  const long long units = static_cast<long long>(s->layers) * s->hkv;      // of a batch element
+  if (most > 0x7fffffffLL || rows > 0x7fffffffLL / 2 || units > 0x7fffffffLL / s->batch ||
+      static_cast<long long>(s->n_pages) > 0x7fffffffLL / units)
+    return fail(SPK_ERR_UNSUPPORTED, "too many units, rows or pages");
+  // tiles of all units (in double: only the order of magnitude matters near the limit)
+  const double tiles = static_cast<double>(s->batch) * units * ((rows + 7) / 8) * (most / kTreeKeys + 1 + s->n_nodes / kTreeKeys + 1);
+  const TreePlan plan = tree_plan(static_cast<int>(rows), s->head_dim, num_sms());
+  if (tiles / (static_cast<double>((rows + 7) / 8)) * plan.row_tiles > 2.0e9)
+    return fail(SPK_ERR_UNSUPPORTED, "too many key tiles over all units");
+  return SPK_OK;
+}
+
+static int box_rows_of(int page_rows, int tile) {
+  int a = page_rows, b = tile;
+  while (b != 0) { const int t = a % b; a = b; b = t; }
+  return a;
+}
+
+// 3-D view [n_units][n_rows][head_dim] of 16-bit elements in boxes of
+// box_rows x 64 with the 128-byte swizzle; rows past n_rows read as zero.
+static spk_status make_map16(CUtensorMap* map, bool fp16, const void* base, int head_dim, long long n_rows,
+                             long long n_units, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return fail(SPK_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(n_rows),
+                              static_cast<cuuint64_t>(n_units)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim) * 2, static_cast<cuuint64_t>(n_rows) * head_dim * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(map, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                  const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(SPK_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
+  return SPK_OK;
+}
+
+size_t tree_attention_workspace_size(const spk_tree_shape* s) {
+  if (check_tree(s) != SPK_OK) return 0;
+  return round_up(tree_ws_bytes(tree_plan(s->hq / s->hkv * s->n_nodes, s->head_dim, num_sms()), s->head_dim), 256);
+}
+
+spk_status tree_attention(const spk_tree_shape* s, const void* q, const void* k_pages, const void* v_pages,
+                          const int32_t* table, const int32_t* lens, const int32_t* seqs, const void* k_tree,
+                          const void* v_tree, const uint32_t* mask, const int32_t* n_live, void* out, float* lse2,
+                          void* ws, size_t ws_bytes, void* stream) {
+  spk_status st = check_tree(s);
+  if (st != SPK_OK) return st;
+  if (q == nullptr || k_pages == nullptr || v_pages == nullptr || out == nullptr || table == nullptr || lens == nullptr)
+    return fail(SPK_ERR_ARG, "q, k_pages, v_pages, page_table, seq_lens and out must be non-NULL device pointers");
+  if ((k_tree == nullptr) != (v_tree == nullptr)) return fail(SPK_ERR_ARG, "k_tree and v_tree are given together or not at all");
+  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) || !aligned16(k_tree) ||
+      !aligned16(v_tree))
+    return fail(SPK_ERR_ARG, "q, pages, tree and out must be 16-byte aligned");
+  if (!aligned4(table) || !aligned4(lens) || !aligned4(seqs) || !aligned4(mask) || !aligned4(n_live) || !aligned4(lse2))
+    return fail(SPK_ERR_ARG, "page_table, seq_lens, seqs, mask, n_live and lse2 must be 4-byte aligned");
+  if (seqs == nullptr && s->batch > s->n_seqs)
+    return fail(SPK_ERR_ARG, "without seqs, batch (%d) is at most n_seqs (%d)", s->batch, s->n_seqs);
+  const int g = s->hq / s->hkv;
+  const TreePlan plan = tree_plan(g * s->n_nodes, s->head_dim, num_sms());
+  if ((st = check_pages_ws(ws, ws_bytes, tree_ws_bytes(plan, s->head_dim))) != SPK_OK) return st;
+  TreeParams p;
+  memset(&p, 0, sizeof p);
+  p.q = q; p.out = out; p.lse2 = lse2;
+  p.table = table; p.lens = lens; p.seqs = seqs; p.n_live = n_live;
+  p.mask = mask; p.words = (s->n_nodes + 31) / 32;
+  p.batch = s->batch; p.layers = s->layers; p.hkv = s->hkv; p.g = g; p.T = s->n_nodes;
+  p.rows = g * s->n_nodes;
+  p.row_tiles = plan.row_tiles;
+  p.has_tree = k_tree != nullptr;
+  p.n_seqs = s->n_seqs; p.max_pages = s->max_pages; p.n_pages = s->n_pages; p.page_rows = s->page_rows;
+  p.box_rows = box_rows_of(s->page_rows, kTreeKeys);
+  p.c2 = s->scale * 1.4426950408889634f;
+  p.ctas = plan.ctas;
+  p.min_chunk = 1;
+  p.part_o = static_cast<float*>(ws);
+  p.part_ml = p.part_o + static_cast<size_t>(plan.ctas) * 2 * plan.tile_rows * s->head_dim;
+  const bool fp16 = s->dtype == SPK_FP16;
+  const long long pool = static_cast<long long>(s->layers) * s->n_pages * s->hkv;
+  const long long units = static_cast<long long>(s->batch) * s->layers * s->hkv;
+  CUtensorMap maps[4];
+  st = make_map16(&maps[0], fp16, k_pages, s->head_dim, s->page_rows, pool, p.box_rows);
+  if (st == SPK_OK) st = make_map16(&maps[1], fp16, v_pages, s->head_dim, s->page_rows, pool, p.box_rows);
+  if (st == SPK_OK && k_tree != nullptr) {
+    st = make_map16(&maps[2], fp16, k_tree, s->head_dim, s->n_nodes, units, kTreeKeys);
+    if (st == SPK_OK) st = make_map16(&maps[3], fp16, v_tree, s->head_dim, s->n_nodes, units, kTreeKeys);
+  } else {
+    maps[2] = maps[0];
+    maps[3] = maps[1];
+  }
+  if (st != SPK_OK) return st;
+  cudaError_t e = launch_tree_attention(fp16, s->head_dim, maps, p, plan, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ok() : cuda_fail(e, "tree attention launch");
+}
+
+spk_status tree_mask(int batch, int n_nodes, const int32_t* parents, const int32_t* n_live, uint32_t* mask,
+                     int32_t* depth, void* stream) {
+  if (batch < 1 || n_nodes < 1) return fail(SPK_ERR_ARG, "batch and n_nodes must be >= 1");
+  if (n_nodes > kTreeMaxNodes) return fail(SPK_ERR_UNSUPPORTED, "n_nodes %d exceeds %d", n_nodes, kTreeMaxNodes);
+  if (batch > 65535) return fail(SPK_ERR_UNSUPPORTED, "batch %d exceeds 65535", batch);
+  if (parents == nullptr || mask == nullptr) return fail(SPK_ERR_ARG, "parents and mask must be non-NULL device pointers");
+  if (!aligned4(parents) || !aligned4(mask) || !aligned4(n_live) || !aligned4(depth))
+    return fail(SPK_ERR_ARG, "parents, n_live, mask and depth must be 4-byte aligned");
+  cudaError_t e = launch_tree_mask(parents, n_live, batch, n_nodes, mask, depth, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ok() : cuda_fail(e, "tree mask launch");
+}
+
 spk_status spk_mapped_host_pointer(const void* host, void** dev) {
   if (host == nullptr || dev == nullptr) return fail(SPK_ERR_ARG, "host and dev must be non-NULL");
   void* d = nullptr;
@@ -635,7 +906,8 @@ spk_status spk_device_error(int* status, int* site, int clear) {
   // every translation unit's error word, the first set one in this order
   // reported (the others are cleared with it)
   cudaError_t (*const readers[])(int*, int*, bool) = {device_errors_api, device_errors_score, device_errors_attn,
-                                                       device_errors_vs, device_errors_compact};
+                                                       device_errors_vs, device_errors_compact, device_errors_pages,
+                                                       device_errors_tree};
   int code = 0, where = 0;
   for (auto rd : readers) {
     int c = 0, w = 0;

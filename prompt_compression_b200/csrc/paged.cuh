@@ -1,0 +1,93 @@
+// paged.cuh -- parameters of the paged-cache operators (pages.cu, tree.cu)
+// and their host launchers.
+//
+// The cache: k_pages, v_pages [layers][n_pages][hkv][page_rows][head_dim];
+// row t of sequence s is row t % page_rows of page
+// page_table[s][t / page_rows], for every layer and KV head; seq_lens[s] rows
+// are valid; page_refs[p] sequences hold page p (0: free).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace spk {
+
+// ---------------------------------------------------------------- pages.cu
+constexpr int kPagesMaxCall = 1024;   // sequences in one call
+
+struct PagesShape {
+  int layers, n_pages, hkv, page_rows;
+  int row_vecs;            // 16-byte vectors of a row
+  int n_seqs, max_pages;
+};
+
+struct PagesBook {         // the bookkeeping arrays
+  int* refs;               // [n_pages]
+  int* table;              // [n_seqs][max_pages]
+  int* lens;               // [n_seqs]
+};
+
+size_t pages_ws_bytes(int n, int max_pages);
+
+cudaError_t launch_pages_reserve(const PagesShape& s, const PagesBook& b, void* k_pages, void* v_pages,
+                                 const int* seqs, const int* n_new, int n, int* result, void* ws,
+                                 cudaStream_t stream);
+cudaError_t launch_pages_fork(const PagesShape& s, const PagesBook& b, const int* src, const int* dst,
+                              const int* n_rows, int n, int* result, void* ws, cudaStream_t stream);
+cudaError_t launch_pages_free(const PagesShape& s, const PagesBook& b, const int* seqs, const int* keep_rows, int n,
+                              cudaStream_t stream);
+cudaError_t launch_pages_write(const PagesShape& s, const PagesBook& b, const void* k, const void* v, int n_src,
+                               const int* idx, int n_idx, int units_per_idx, const int* counts, const int* seqs,
+                               int n, void* k_pages, void* v_pages, cudaStream_t stream);
+cudaError_t launch_pages_compact(const PagesShape& s, const PagesBook& b, void* k_pages, void* v_pages,
+                                 const int* src, const int* dst, int n, const int* idx, int n_idx,
+                                 int units_per_idx, int* result, void* ws, cudaStream_t stream);
+cudaError_t device_errors_pages(int* code, int* site, bool clear);
+
+// ----------------------------------------------------------------- tree.cu
+constexpr int kTreeMaxBatch = 1024;
+constexpr int kTreeMaxNodes = 1024;
+constexpr int kTreeKeys = 64;         // keys of a tile
+
+struct TreeParams {
+  const void* q;           // [batch][layers][hq][T][d]
+  void* out;               // like q
+  float* lse2;             // [batch][layers][hq][T] or null
+  const int* table;        // [n_seqs][max_pages]
+  const int* lens;         // [n_seqs]
+  const int* seqs;         // [batch] or null (batch element b is sequence b)
+  const int* n_live;       // [batch] or null (every node is live)
+  const uint32_t* mask;    // [batch][T][words] or null (node i sees the nodes 0 .. i)
+  int words;
+  int batch, layers, hkv, g, T;
+  int rows;                // query rows per unit = g * T, ordered [query head][node]
+  int row_tiles;           // row tiles per unit
+  int has_tree;            // k_tree and v_tree are given
+  int n_seqs, max_pages, n_pages, page_rows;
+  int box_rows;            // rows of one page copy: divides page_rows and the tile
+  float c2;                // scale * log2(e)
+  int ctas;                // CTAs of the main kernel
+  int min_chunk;           // key tiles a CTA takes at least
+  float* part_o;           // [ctas * 2][tile rows][d] partial outputs
+  float* part_ml;          // [ctas * 2][tile rows][2] their row maxima and sums
+};
+
+struct TreePlan {
+  int tile_rows;           // query rows of a tile
+  int row_tiles;
+  int ctas;
+};
+TreePlan tree_plan(int rows, int head_dim, int sms);
+size_t tree_ws_bytes(const TreePlan& plan, int head_dim);
+
+// maps: k_pages, v_pages [layers * n_pages * hkv][page_rows][d] in boxes of
+// box_rows x 64; k_tree, v_tree [batch * layers * hkv][T][d] in boxes of
+// kTreeKeys x 64
+cudaError_t launch_tree_attention(bool fp16, int head_dim, const CUtensorMap (&maps)[4], const TreeParams& p,
+                                  const TreePlan& plan, cudaStream_t stream);
+cudaError_t launch_tree_mask(const int* parents, const int* n_live, int batch, int T, uint32_t* mask, int* depth,
+                             cudaStream_t stream);
+cudaError_t device_errors_tree(int* code, int* site, bool clear);
+
+}  // namespace spk

@@ -1,0 +1,673 @@
+// tree.cu -- attention for a tree of drafted tokens over a paged KV cache.
+//
+// Row r = (query head, node i) of a unit (batch element, layer, KV head):
+//   z_j  = scale * q_r . k_j   over the n cached rows and the tree's nodes j
+//                              with bit j of the visibility words of node i
+//   out  = sum_j 2^(c2 s_j - m) v_j / sum_j 2^(c2 s_j - m),  lse2 = m + log2 sum,
+// in one pass with the running maximum m and sum (log2 domain, fp32).
+//
+// Work split: the key tiles (64 keys: first the cached rows, then the nodes)
+// of all units, in the order (batch element, layer, KV head, row tile, tile),
+// form one sequence that the CTAs take in equal consecutive shares, so ragged
+// lengths balance and a few long sequences still fill the GPU.  The shares
+// follow from seq_lens on the device.  A unit inside one share is finished
+// there; the others leave (m, sum, unnormalised output) of each share in the
+// workspace, and tree_join_kernel adds them in the order of the shares: the
+// results do not depend on timing.
+#include "common.cuh"
+#include "mma.cuh"
+#include "paged.cuh"
+
+namespace spk {
+
+SPK_ERROR_READER(device_errors_tree)
+
+namespace {
+
+constexpr int kWarps = 4;                       // consumer warps
+constexpr int kThreads = (kWarps + 1) * 32;     // and the producer warp
+constexpr int kSmemPerCta = 113 * 1024;         // two CTAs share an SM
+
+__device__ __forceinline__ int site(int which) { return 600 + which; }
+
+// --------------------------------------------------------------------------
+// the shares
+// --------------------------------------------------------------------------
+struct Element {           // a batch element
+  int seq, len, live, tiles;
+};
+
+// Length and live nodes of batch element b; an element whose sequence, length
+// or node count is out of range has no rows (its outputs stay unwritten).
+__device__ __forceinline__ Element element_of(const TreeParams& p, int b, bool record) {
+  Element e;
+  e.seq = p.seqs != nullptr ? __ldg(p.seqs + b) : b;
+  e.live = p.n_live != nullptr ? __ldg(p.n_live + b) : p.T;
+  bool ok = e.seq >= 0 && e.seq < p.n_seqs && e.live >= 0 && e.live <= p.T;
+  e.len = ok ? __ldg(p.lens + e.seq) : 0;
+  ok = ok && e.len >= 0 && e.len <= static_cast<long long>(p.max_pages) * p.page_rows;
+  if (!ok) {
+    if (record) record_error(SPK_DEVERR_INDEX, b);
+    e.seq = 0;
+    e.len = 0;
+    e.live = 0;
+  }
+  const int nodes = p.has_tree ? (e.live + kTreeKeys - 1) / kTreeKeys : 0;
+  const int t = (e.len + kTreeKeys - 1) / kTreeKeys + nodes;
+  e.tiles = e.live == 0 ? 0 : (t > 0 ? t : 1);   // rows without any key still get their zeros
+  return e;
+}
+
+// prefix[b] = tiles of the batch elements before b, by the calling warp.
+__device__ __forceinline__ void tree_prefix(const TreeParams& p, int* prefix, bool record) {
+  const int lane = threadIdx.x & 31;
+  const int units = p.layers * p.hkv * p.row_tiles;
+  int base = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += 32) {
+    const int b = b0 + lane;
+    const int x = b < p.batch ? element_of(p, b, record).tiles * units : 0;
+    int s = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += y;
+    }
+    if (b < p.batch) prefix[b] = base + s - x;
+    base += __shfl_sync(0xffffffffu, s, 31);
+  }
+  if (lane == 0) prefix[p.batch] = base;
+}
+
+__device__ __forceinline__ int share_of(const TreeParams& p, int total) {
+  const int even = (total + p.ctas - 1) / p.ctas;
+  return even > p.min_chunk ? even : p.min_chunk;
+}
+
+// The part of a share that lies in one unit: tiles [t0, t1) of its `e.tiles`.
+struct Run {
+  int b, unit, row0, t0, t1;   // unit = (b * layers + l) * hkv + h; row0 = first row of the row tile
+  Element e;
+};
+
+struct Walker {
+  int x, end, b;
+  __device__ __forceinline__ bool next(const TreeParams& p, const int* prefix, int tile_rows, Run& r) {
+    if (x >= end) return false;
+    while (x >= prefix[b + 1]) ++b;
+    r.b = b;
+    r.e = element_of(p, b, false);
+    const int y = x - prefix[b];
+    const int w = y / r.e.tiles;
+    r.t0 = y - w * r.e.tiles;
+    r.t1 = min(r.e.tiles, r.t0 + (end - x));
+    const int lh = w / p.row_tiles;
+    r.unit = b * p.layers * p.hkv + lh;
+    r.row0 = (w - lh * p.row_tiles) * tile_rows;
+    x += r.t1 - r.t0;
+    return true;
+  }
+};
+
+// Keys of tile t of a batch element: [0, n) of the tile are there.
+struct Tile {
+  bool cached;
+  int first;      // first cached row or first node
+  int n;
+};
+__device__ __forceinline__ Tile tile_of(const TreeParams& p, const Element& e, int t) {
+  Tile k;
+  const int cached = (e.len + kTreeKeys - 1) / kTreeKeys;
+  k.cached = t < cached;
+  k.first = (k.cached ? t : t - cached) * kTreeKeys;
+  k.n = k.cached ? min(kTreeKeys, e.len - k.first) : (p.has_tree ? min(kTreeKeys, e.live - k.first) : 0);
+  return k;
+}
+
+// --------------------------------------------------------------------------
+// main kernel
+// --------------------------------------------------------------------------
+template <int D, int NT>
+struct TreeCfg {
+  static constexpr int kRows = 8 * NT;                  // query rows of a tile
+  static constexpr int kHalf = kTreeKeys * 128;         // 64 keys x 64 columns
+  static constexpr int kAtoms = D / 64;
+  static constexpr int kStageBytes = 2 * kAtoms * kHalf;
+  static constexpr int kQBytes = kRows * D * 2;
+  static constexpr int kPBytes = kRows * kTreeKeys * 2;
+  static constexpr int kStages = (kSmemPerCta - 2048 - 1024 - kTreeMaxBatch * 4 - 4 * kRows * 8 - kQBytes - kPBytes) /
+                                 kStageBytes;
+  static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kQBytes + kPBytes;
+  static_assert(kStages >= 2, "a tile is loaded while another is used");
+};
+
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// Four consumer warps.  Per tile, warp w takes 16 of its keys for the logits
+//   S^T[key][row] = K Q^T               (A = K by ldmatrix, B = Q)
+// the four warps exchange their column maxima, leave P = 2^(c2 s - m) in shared
+// memory as 16-bit values, and then each takes a quarter of head_dim for
+//   O^T[d][row] = alpha O^T + V^T P^T   (A = V^T by ldmatrix.trans, B = P^T),
+// so no state is merged at the end of a unit.  P is rounded to the element
+// type for the product (the largest weight is 1 exactly, the others are off by
+// half a step at most, and the errors average over the keys); the sum is
+// formed from the fp32 values, so lse2 keeps 32 bits.
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kThreads, 2)
+    tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                const __grid_constant__ CUtensorMap ktmap, const __grid_constant__ CUtensorMap vtmap,
+                const __grid_constant__ TreeParams p) {
+  using C = TreeCfg<D, NT>;
+  constexpr int KS = D / 16;              // k-steps of the logits
+  constexpr int DW = D / kWarps;          // head_dim columns of a warp
+  constexpr int MT = DW / 16;             // their m-tiles
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t stage_s = smem_u32(smem);
+  uint8_t* const q_p = smem + C::kStages * C::kStageBytes;
+  const uint32_t q_s = smem_u32(q_p), p_s = q_s + C::kQBytes;
+
+  __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages];
+  __shared__ int prefix[kTreeMaxBatch + 1];
+  __shared__ __align__(16) float wmax[kWarps][C::kRows];   // read and written in pairs
+  __shared__ int abort_flag;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], kWarps);
+    }
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) tree_prefix(p, prefix, blockIdx.x == 0);
+  if (warp == kWarps && lane == 0) {
+    tma_prefetch_map(&kmap);
+    tma_prefetch_map(&vmap);
+  }
+  __syncthreads();
+  volatile int* const abort_v = &abort_flag;
+  const int total = prefix[p.batch];
+  const int share = share_of(p, total);
+  const int begin = static_cast<int>(min(static_cast<long long>(total), static_cast<long long>(share) * blockIdx.x));
+  Walker walk{begin, min(total - begin, share) + begin, 0};
+  Run run;
+
+  if (warp == kWarps) {
+    // ---------------------------------------------------------------- producer
+    uint32_t count = 0;
+    bool ok = true;
+    int last[C::kStages];
+#pragma unroll
+    for (int s = 0; s < C::kStages; ++s) last[s] = -1;
+    while (ok && walk.next(p, prefix, C::kRows, run)) {
+      const int* row = p.table + static_cast<size_t>(run.e.seq) * p.max_pages;
+      const int lh = run.unit - run.b * p.layers * p.hkv;
+      const int layer = lh / p.hkv, head = lh - layer * p.hkv;
+      for (int t = run.t0; t < run.t1; ++t, ++count) {
+        const Tile tile = tile_of(p, run.e, t);
+        const int st = count % C::kStages;
+        const uint32_t ph = (count / C::kStages) & 1;
+        // lane i: the page of box i of the tile
+        const int boxes = tile.cached ? (tile.n + p.box_rows - 1) / p.box_rows : 0;
+        int unit = 0, in_page = 0;
+        if (lane < boxes) {
+          const int t_row = tile.first + lane * p.box_rows;
+          const int slot = t_row / p.page_rows;
+          in_page = t_row - slot * p.page_rows;
+          int page = __ldg(row + slot);
+          if (page < 0 || page >= p.n_pages) {
+            record_error(SPK_DEVERR_INDEX, run.b);
+            unit = p.layers * p.n_pages * p.hkv;     // outside the map: the box reads as zeros
+          } else {
+            unit = (layer * p.n_pages + page) * p.hkv + head;
+          }
+        }
+        ok = mbar_wait(&empty[st], ph ^ 1, abort_v, site(0));
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) {
+          if (tile.cached)
+            mbar_arrive_expect_tx(&full[st], boxes * p.box_rows * 128 * 2 * C::kAtoms);
+          else if (tile.n > 0)
+            mbar_arrive_expect_tx(&full[st], C::kStageBytes);
+          else
+            mbar_arrive(&full[st]);
+        }
+        __syncwarp();
+        uint8_t* const kp = smem + st * C::kStageBytes;
+        if (lane < boxes) {
+          uint8_t* const dst = kp + lane * p.box_rows * 128;
+#pragma unroll
+          for (int a = 0; a < C::kAtoms; ++a) {
+            tma_load_3d(dst + a * C::kHalf, &kmap, &full[st], a * 64, in_page, unit);
+            tma_load_3d(dst + (C::kAtoms + a) * C::kHalf, &vmap, &full[st], a * 64, in_page, unit);
+          }
+        } else if (!tile.cached && tile.n > 0 && lane == 0) {
+#pragma unroll
+          for (int a = 0; a < C::kAtoms; ++a) {
+            tma_load_3d(kp + a * C::kHalf, &ktmap, &full[st], a * 64, tile.first, run.unit);
+            tma_load_3d(kp + (C::kAtoms + a) * C::kHalf, &vtmap, &full[st], a * 64, tile.first, run.unit);
+          }
+        }
+#pragma unroll
+        for (int s = 0; s < C::kStages; ++s)
+          if (s == st) last[s] = static_cast<int>(ph);
+      }
+    }
+    if (!ok && lane == 0) {   // let the copies in flight land before the block ends
+      volatile int never = 0;
+#pragma unroll
+      for (int s = 0; s < C::kStages; ++s)
+        if (last[s] >= 0) mbar_wait(&full[s], last[s], &never, site(1), 100000000ull);
+    }
+  } else {
+    // --------------------------------------------------------------- consumers
+    // A wait that runs out raises the abort flag; the warps go on through their
+    // barriers (every later wait returns at once) and the error word says so.
+    const int gr = lane >> 2, gc = lane & 3;
+    uint32_t count = 0;
+    int runs = 0;
+    while (walk.next(p, prefix, C::kRows, run)) {
+      const int rows = min(C::kRows, p.rows - run.row0);     // rows of this tile that exist
+      // Q rows of the tile (they lie together: a unit's heads and nodes), zeros behind them
+      {
+        const uint4* src = reinterpret_cast<const uint4*>(p.q) +
+                           (static_cast<size_t>(run.unit) * p.rows + run.row0) * (D / 8);
+        for (int x = threadIdx.x; x < C::kRows * (D / 8); x += kWarps * 32) {
+          const int row = x / (D / 8), ch = x % (D / 8);
+          const uint4 w = row < rows ? __ldg(src + x) : make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(q_p + row * (D * 2) + ((ch ^ (row & 7)) << 4)) = w;
+        }
+      }
+      consumers_sync();
+      float o[MT][NT][4];
+      float m[NT][2], l[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        m[n][0] = m[n][1] = -INFINITY;
+        l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+        for (int j = 0; j < MT; ++j) o[j][n][0] = o[j][n][1] = o[j][n][2] = o[j][n][3] = 0.f;
+      }
+      for (int t = run.t0; t < run.t1; ++t, ++count) {
+        const Tile tile = tile_of(p, run.e, t);
+        const int st = count % C::kStages;
+        const uint32_t ks = stage_s + st * C::kStageBytes, vs = ks + C::kAtoms * C::kHalf;
+        const int key0 = warp * 16;
+        // which of keys gr, gr + 8 each row sees
+        uint32_t sees[NT][2];
+        if (tile.cached) {
+          const uint32_t bits = (key0 + gr < tile.n ? 1u : 0u) | (key0 + gr + 8 < tile.n ? 2u : 0u);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) sees[n][0] = sees[n][1] = bits;
+        } else {
+          const int node0 = tile.first + key0;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int r = run.row0 + 8 * n + 2 * gc + c;
+              uint32_t w = 0;
+              if (r < p.rows && key0 < tile.n) {
+                const int i = r % p.T;
+                if (p.mask != nullptr)
+                  w = __ldg(p.mask + (static_cast<size_t>(run.b) * p.T + i) * p.words + (node0 >> 5)) >> (node0 & 31);
+                else
+                  w = i >= node0 ? (i - node0 >= 31 ? 0xffffffffu : (2u << (i - node0)) - 1u) : 0u;
+              }
+              sees[n][c] = ((w >> gr) & (key0 + gr < tile.n ? 1u : 0u)) |
+                           (((w >> (gr + 8)) & (key0 + gr + 8 < tile.n ? 1u : 0u)) << 1);
+            }
+          }
+        }
+        mbar_wait(&full[st], (count / C::kStages) & 1, abort_v, site(2));
+
+        float s[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+        if (key0 < tile.n) {
+          const int arow = key0 + (lane & 15);
+#pragma unroll
+          for (int k = 0; k < KS; k += 2) {
+            uint32_t a[4], b[4];
+            const int ch = 2 * k + (lane >> 4);
+            ldsm_x4(ks + (ch >> 3) * C::kHalf + arow * 128 + (((ch & 7) ^ (arow & 7)) << 4), a);
+            const int ch2 = ch + 2;
+            ldsm_x4(ks + (ch2 >> 3) * C::kHalf + arow * 128 + (((ch2 & 7) ^ (arow & 7)) << 4), b);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              uint32_t q[4];
+              const int row = 8 * n + (lane & 7);
+              ldsm_x4(q_s + row * (D * 2) + (((2 * k + (lane >> 3)) ^ (row & 7)) << 4), q);
+              Half16<T>::mma(s[n], a, q[0], q[1]);
+              Half16<T>::mma(s[n], b, q[2], q[3]);
+            }
+          }
+        }
+        // this warp's maximum of each row, then all four warps'
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float mx[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            s[n][c] = (sees[n][c] & 1u) ? s[n][c] * p.c2 : -INFINITY;
+            s[n][2 + c] = (sees[n][c] & 2u) ? s[n][2 + c] * p.c2 : -INFINITY;
+            mx[c] = fmaxf(s[n][c], s[n][2 + c]);
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], x));
+          }
+          if (gr == 0) *reinterpret_cast<float2*>(&wmax[warp][8 * n + 2 * gc]) = make_float2(mx[0], mx[1]);
+        }
+        consumers_sync();
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float mx[2] = {m[n][0], m[n][1]};
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            const float2 y = *reinterpret_cast<const float2*>(&wmax[w][8 * n + 2 * gc]);
+            mx[0] = fmaxf(mx[0], y.x);
+            mx[1] = fmaxf(mx[1], y.y);
+          }
+          float ref[2], alpha[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            ref[c] = mx[c] == -INFINITY ? 0.f : mx[c];     // no key yet: every weight is 2^-inf = 0
+            alpha[c] = ex2_approx(m[n][c] - ref[c]);
+            m[n][c] = mx[c];
+          }
+          float e[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) e[x] = ex2_approx(s[n][x] - ref[x & 1]);
+          const uint32_t lo = Half16<T>::pack(e[0], e[1]), hi = Half16<T>::pack(e[2], e[3]);
+          l[n][0] = fmaf(l[n][0], alpha[0], e[0] + e[2]);
+          l[n][1] = fmaf(l[n][1], alpha[1], e[1] + e[3]);
+          const int row = 8 * n + (lane & 7);
+          stsm_x2_t(p_s + row * 128 + (((2 * warp + ((lane >> 3) & 1)) ^ (row & 7)) << 4), lo, hi);
+#pragma unroll
+          for (int j = 0; j < MT; ++j) {
+            o[j][n][0] *= alpha[0];
+            o[j][n][1] *= alpha[1];
+            o[j][n][2] *= alpha[0];
+            o[j][n][3] *= alpha[1];
+          }
+        }
+        // V rows behind the tile's last key: whatever the slot holds (it may be
+        // NaN) must not meet the zeros of P, so the rest of the last k-step is cleared
+        const int steps = (tile.n + 15) / 16;
+        if (tile.n < steps * 16) {
+          constexpr int kCh = DW / 8;            // this warp's 16-byte columns
+          const int bad = steps * 16 - tile.n;
+          for (int x = lane; x < bad * kCh; x += 32) {
+            const int row = tile.n + x / kCh, ch = warp * kCh + x % kCh;
+            uint8_t* at = smem + st * C::kStageBytes + C::kAtoms * C::kHalf + (ch >> 3) * C::kHalf + row * 128 +
+                          (((ch & 7) ^ (row & 7)) << 4);
+            *reinterpret_cast<uint4*>(at) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();              // before the slot's next copy
+        }
+        consumers_sync();
+#pragma unroll
+        for (int k = 0; k < kTreeKeys / 16; k += 2) {
+          if (k >= steps) break;
+          uint32_t b[NT][4];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const int row = 8 * n + (lane & 7);
+            ldsm_x4(p_s + row * 128 + (((2 * k + (lane >> 3)) ^ (row & 7)) << 4), b[n]);
+          }
+#pragma unroll
+          for (int kk = 0; kk < 2; ++kk) {
+            if (k + kk >= steps) break;
+            const int vrow = (k + kk) * 16 + (lane & 7) + (lane >> 4) * 8;
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+              uint32_t a[4];
+              const int ch = warp * (DW / 8) + 2 * j + ((lane >> 3) & 1);
+              ldsm_x4_t(vs + (ch >> 3) * C::kHalf + vrow * 128 + (((ch & 7) ^ (vrow & 7)) << 4), a);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) Half16<T>::mma(o[j][n], a, b[n][2 * kk], b[n][2 * kk + 1]);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[st]);
+      }
+
+      // row sums over the keys of all warps (wmax is free: every warp is past the last tile's maxima)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], x);
+        if (gr == 0) *reinterpret_cast<float2*>(&wmax[warp][8 * n + 2 * gc]) = make_float2(l[n][0], l[n][1]);
+      }
+      consumers_sync();
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float2 y = *reinterpret_cast<const float2*>(&wmax[w][8 * n + 2 * gc]);
+          l[n][0] += y.x;
+          l[n][1] += y.y;
+        }
+      }
+      if (run.t0 == 0 && run.t1 == run.e.tiles) {
+        // the whole unit: outputs through shared memory (over Q), 16 bytes a store
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float i0 = l[n][0] > 0.f ? 1.f / l[n][0] : (l[n][0] == 0.f ? 0.f : l[n][0]);
+          const float i1 = l[n][1] > 0.f ? 1.f / l[n][1] : (l[n][1] == 0.f ? 0.f : l[n][1]);
+          const int row = 8 * n + (lane & 7);
+#pragma unroll
+          for (int j = 0; j < MT; ++j) {
+            const int ch = warp * (DW / 8) + 2 * j + ((lane >> 3) & 1);
+            stsm_x2_t(q_s + row * (D * 2) + ((ch ^ (row & 7)) << 4), Half16<T>::pack(o[j][n][0] * i0, o[j][n][1] * i1),
+                      Half16<T>::pack(o[j][n][2] * i0, o[j][n][3] * i1));
+          }
+          if (warp == 0 && gr == 0 && p.lse2 != nullptr) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int r = run.row0 + 8 * n + 2 * gc + c;
+              if (r < p.rows && r % p.T < run.e.live)
+                p.lse2[static_cast<size_t>(run.unit) * p.rows + r] =
+                    l[n][c] == 0.f ? -INFINITY : m[n][c] + lg2_approx(l[n][c]);
+            }
+          }
+        }
+        consumers_sync();
+        uint4* dst = reinterpret_cast<uint4*>(p.out) + (static_cast<size_t>(run.unit) * p.rows + run.row0) * (D / 8);
+        for (int x = threadIdx.x; x < rows * (D / 8); x += kWarps * 32) {
+          const int row = x / (D / 8), ch = x % (D / 8);
+          if ((run.row0 + row) % p.T < run.e.live)
+            dst[x] = *reinterpret_cast<const uint4*>(q_p + row * (D * 2) + ((ch ^ (row & 7)) << 4));
+        }
+      } else {
+        const size_t part = (static_cast<size_t>(blockIdx.x) * 2 + (runs > 0 ? 1 : 0)) * C::kRows;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const size_t row = part + 8 * n + 2 * gc + c;
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+              const int d = warp * DW + 16 * j + gr;
+              p.part_o[row * D + d] = o[j][n][c];
+              p.part_o[row * D + d + 8] = o[j][n][2 + c];
+            }
+            if (warp == 0 && gr == 0) *reinterpret_cast<float2*>(p.part_ml + row * 2) = make_float2(m[n][c], l[n][c]);
+          }
+        }
+      }
+      consumers_sync();                          // Q, the staged outputs and the sums are free
+      ++runs;
+    }
+  }
+}
+
+// --------------------------------------------------------------------------
+// the units that several shares hold
+// --------------------------------------------------------------------------
+// Block (c, y): the unit that the border between shares c - 1 and c cuts, if
+// this is the first border inside it; rows y * 4 .. of its row tile, a warp a
+// row.  A row's shares are added in their order:
+//   M = max m_c,  out = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) tree_join_kernel(const __grid_constant__ TreeParams p, int tile_rows) {
+  __shared__ int prefix[kTreeMaxBatch + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 0) tree_prefix(p, prefix, false);
+  __syncthreads();
+  const int total = prefix[p.batch];
+  const int share = share_of(p, total);
+  const int c = blockIdx.x + 1;
+  if (static_cast<long long>(c) * share >= total) return;
+  const int x = c * share;
+  int b = 0;
+  while (x >= prefix[b + 1]) ++b;
+  const Element e = element_of(p, b, false);
+  const int w = (x - prefix[b]) / e.tiles;
+  const int u0 = prefix[b] + w * e.tiles, u1 = u0 + e.tiles;
+  const int c0 = u0 / share, c1 = (u1 - 1) / share;
+  if (u0 == x || c0 != c - 1) return;
+  const int lh = w / p.row_tiles;
+  const size_t unit = static_cast<size_t>(b) * p.layers * p.hkv + lh;
+  const int row = blockIdx.y * 4 + warp;                     // in the row tile
+  const int r = (w - lh * p.row_tiles) * tile_rows + row;    // in the unit
+  if (row >= tile_rows || r >= p.rows || r % p.T >= e.live) return;
+
+  auto slot = [&](int i) { return (static_cast<size_t>(i) * 2 + (i == c0 && u0 > c0 * share ? 1 : 0)) * tile_rows + row; };
+  float M = -INFINITY;
+  for (int i = c0 + lane; i <= c1; i += 32) M = fmaxf(M, p.part_ml[slot(i) * 2]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float ref = M == -INFINITY ? 0.f : M;
+  constexpr int V = D / 32;
+  float acc[V], L = 0.f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] = 0.f;
+  for (int i = c0; i <= c1; ++i) {
+    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + slot(i) * 2);
+    const float f = ex2_approx(ml.x - ref);
+    L = fmaf(ml.y, f, L);
+    const float* src = p.part_o + slot(i) * D + lane * V;
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = fmaf(src[v], f, acc[v]);
+  }
+  const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.out) + (unit * p.rows + r) * (D / 2) + lane * (V / 2);
+#pragma unroll
+  for (int v = 0; v < V; v += 2) dst[v / 2] = Half16<T>::pack(acc[v] * inv, acc[v + 1] * inv);
+  if (lane == 0 && p.lse2 != nullptr) p.lse2[unit * p.rows + r] = L == 0.f ? -INFINITY : M + lg2_approx(L);
+}
+
+template <typename T, int D, int NT>
+cudaError_t launch_nt(const CUtensorMap (&maps)[4], const TreeParams& p, const TreePlan& plan, cudaStream_t stream) {
+  using C = TreeCfg<D, NT>;
+  static thread_local int configured_device = -1;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (configured_device != dev) {
+    e = cudaFuncSetAttribute(tree_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    configured_device = dev;
+  }
+  tree_kernel<T, D, NT><<<plan.ctas, kThreads, C::kSmemBytes, stream>>>(maps[0], maps[1], maps[2], maps[3], p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || plan.ctas == 1) return e;
+  tree_join_kernel<T, D><<<dim3(plan.ctas - 1, (C::kRows + 3) / 4), 128, 0, stream>>>(p, C::kRows);
+  return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_d(const CUtensorMap (&maps)[4], const TreeParams& p, const TreePlan& plan, cudaStream_t stream) {
+  switch (plan.tile_rows) {
+    case 8: return launch_nt<T, D, 1>(maps, p, plan, stream);
+    case 16: return launch_nt<T, D, 2>(maps, p, plan, stream);
+    case 32: return launch_nt<T, D, 4>(maps, p, plan, stream);
+    default: return launch_nt<T, D, 8>(maps, p, plan, stream);
+  }
+}
+
+// --------------------------------------------------------------------------
+// visibility words
+// --------------------------------------------------------------------------
+// Thread = node: walk the parents up to the root, one bit a step.  A parent
+// stands before its child, so the words are met from the last to the first
+// and each is written once.  Latency bound: one shared-memory load a step.
+__global__ void __launch_bounds__(128) tree_mask_kernel(const int* __restrict__ parents, const int* __restrict__ n_live,
+                                                        int T, int words, uint32_t* __restrict__ mask,
+                                                        int* __restrict__ depth) {
+  __shared__ int parent_s[kTreeMaxNodes];
+  const int b = blockIdx.x;
+  int live = n_live != nullptr ? __ldg(n_live + b) : T;
+  if (live < 0 || live > T) {
+    if (threadIdx.x == 0 && blockIdx.y == 0) record_error(SPK_DEVERR_INDEX, b);
+    live = live < 0 ? 0 : T;
+  }
+  const int i = blockIdx.y * blockDim.x + threadIdx.x;
+  const int upto = min(live, static_cast<int>((blockIdx.y + 1) * blockDim.x));
+  for (int x = threadIdx.x; x < upto; x += blockDim.x) {
+    int q = __ldg(parents + static_cast<size_t>(b) * T + x);
+    if (q < -1 || q >= x) {
+      record_error(SPK_DEVERR_INDEX, b);
+      q = -1;
+    }
+    parent_s[x] = q;
+  }
+  __syncthreads();
+  if (i >= T) return;
+  uint32_t* row = mask + (static_cast<size_t>(b) * T + i) * words;
+  int steps = 0, at = words - 1;
+  if (i < live) {
+    uint32_t w = 0;
+    int q = i;
+    while (q >= 0) {
+      while ((q >> 5) < at) {
+        row[at--] = w;
+        w = 0;
+      }
+      w |= 1u << (q & 31);
+      q = parent_s[q];
+      ++steps;
+    }
+    row[at--] = w;
+    --steps;
+  }
+  while (at >= 0) row[at--] = 0;
+  if (depth != nullptr) depth[static_cast<size_t>(b) * T + i] = steps;
+}
+
+}  // namespace
+
+TreePlan tree_plan(int rows, int head_dim, int sms) {
+  TreePlan plan;
+  plan.tile_rows = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  plan.row_tiles = (rows + plan.tile_rows - 1) / plan.tile_rows;
+  plan.ctas = 2 * sms;
+  return plan;
+}
+
+size_t tree_ws_bytes(const TreePlan& plan, int head_dim) {
+  return static_cast<size_t>(plan.ctas) * 2 * plan.tile_rows * (head_dim + 2) * sizeof(float);
+}
+
+cudaError_t launch_tree_attention(bool fp16, int head_dim, const CUtensorMap (&maps)[4], const TreeParams& p,
+                                  const TreePlan& plan, cudaStream_t stream) {
+  if (head_dim == 128)
+    return fp16 ? launch_d<__half, 128>(maps, p, plan, stream) : launch_d<__nv_bfloat16, 128>(maps, p, plan, stream);
+  if (head_dim == 64)
+    return fp16 ? launch_d<__half, 64>(maps, p, plan, stream) : launch_d<__nv_bfloat16, 64>(maps, p, plan, stream);
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_tree_mask(const int* parents, const int* n_live, int batch, int T, uint32_t* mask, int* depth,
+                             cudaStream_t stream) {
+  tree_mask_kernel<<<dim3(batch, (T + 127) / 128), 128, 0, stream>>>(parents, n_live, T, (T + 31) / 32, mask, depth);
+  return cudaGetLastError();
+}
+
+}  // namespace spk

@@ -150,3 +150,112 @@ def test_binding_signatures_match_the_header(lib):
         assert len(fn.argtypes) == n, f"{name}: header has {n} parameters, binding {len(fn.argtypes)}"
         checked += 1
     assert checked >= 10
+
+
+def _pages(**change):
+    from prompt_compression_b200 import binding as B
+    f = dict(layers=2, n_pages=10, hkv=2, page_rows=16, head_dim=64, elem_bytes=2, n_seqs=4, max_pages=5)
+    f.update(change)
+    return B.PagesShape(*f.values())
+
+
+@pytest.mark.parametrize("change,n,status,needle", [
+    (dict(n_pages=0), 2, 1, ">= 1"),
+    (dict(page_rows=0), 2, 1, ">= 1"),
+    (dict(max_pages=0), 2, 1, ">= 1"),
+    (dict(layers=0), 2, 1, ">= 1"),
+    (dict(), -1, 1, "n must be"),
+    (dict(), 1025, 2, "1025 sequences"),
+    (dict(head_dim=7), 2, 2, "multiple of 16"),
+    (dict(max_pages=1 << 20, page_rows=1 << 12), 2, 2, "too large"),
+    (dict(layers=1 << 12, n_pages=1 << 20), 2, 2, "too large"),
+])
+def test_pages_shape_errors(lib, change, n, status, needle):
+    s = _pages(**change)
+    assert lib.kv_pages_reserve(ctypes.byref(s), 16, 16, 16, 16, 16, 16, 16, n, 16, 16, 1 << 30, None) == status
+    assert needle in lib.spk_last_error().decode()
+    assert lib.kv_pages_write(ctypes.byref(s), 16, 16, 4, None, 4, 1, None, 16, 16, 16, 16, n, 16, 16, None) == status
+    assert lib.kv_pages_compact(ctypes.byref(s), 16, 16, 16, 16, 16, 16, 16, n, 16, 3, 1, 16, 16, 1 << 30, None) == status
+
+
+def test_pages_pointer_and_workspace_errors(lib):
+    from prompt_compression_b200 import binding as B
+    s = ctypes.byref(_pages())
+    need = 4 * (2 * 5 + 2 + 4 * 2)                   # two table rows (rounded up to 4 words) and 4 words a sequence
+    assert lib.kv_pages_workspace_size(s, 2) == 256
+    assert lib.kv_pages_workspace_size(ctypes.byref(_pages(max_pages=0)), 2) == 0
+    assert lib.kv_pages_reserve(s, 16, 16, 16, 16, 16, 16, 16, 2, 16, 16, need - 1, None) == B.SPK_ERR_WORKSPACE
+    assert lib.kv_pages_fork(s, 16, 16, 16, 16, 16, None, 2, 16, None, 1 << 20, None) == B.SPK_ERR_WORKSPACE
+    assert lib.kv_pages_fork(s, 16, 16, 16, 16, 16, None, 2, 16, 24, 1 << 20, None) == B.SPK_ERR_ARG     # workspace alignment
+    assert lib.kv_pages_reserve(s, 16, 24, 16, 16, 16, 16, 16, 2, 16, 16, 1 << 20, None) == B.SPK_ERR_ARG
+    assert lib.kv_pages_reserve(s, 16, 16, 18, 16, 16, 16, 16, 2, 16, 16, 1 << 20, None) == B.SPK_ERR_ARG
+    assert lib.kv_pages_reserve(s, 16, 16, 16, 16, 16, 16, 16, 2, None, 16, 1 << 20, None) == B.SPK_ERR_ARG
+    assert lib.kv_pages_reserve(s, 16, 16, 16, 16, 16, None, 16, 2, 16, 16, 1 << 20, None) == B.SPK_ERR_ARG
+    assert lib.kv_pages_free(s, 16, None, 16, 16, None, 2, None) == B.SPK_ERR_ARG
+    assert lib.kv_pages_free(s, 16, 16, 16, None, None, 2, None) == B.SPK_ERR_ARG
+    assert lib.kv_pages_free(s, 16, 16, 16, None, None, 0, None) == B.SPK_OK                             # nothing to do
+    w = lambda **k: lib.kv_pages_write(s, k.get("k", 16), 16, k.get("n_src", 4), k.get("idx"), k.get("n_idx", 4),  # noqa: E731
+                                       k.get("per", 1), None, 16, 16, 16, 16, 2, 16, 16, None)
+    assert w(per=3) == B.SPK_ERR_ARG and w(per=0) == B.SPK_ERR_ARG and w(n_idx=5) == B.SPK_ERR_ARG
+    assert w(k=None) == B.SPK_ERR_ARG and w(k=8) == B.SPK_ERR_ARG and w(n_src=-1) == B.SPK_ERR_ARG
+    assert w(n_idx=0) == B.SPK_OK
+    c = lambda n_idx, per=1, idx=16: lib.kv_pages_compact(s, 16, 16, 16, 16, 16, 16, 16, 2, idx, n_idx, per, 16, 16,  # noqa: E731
+                                                          1 << 20, None)
+    assert c(81) == B.SPK_ERR_ARG and c(-1) == B.SPK_ERR_ARG and c(3, per=5) == B.SPK_ERR_ARG
+    assert c(3, idx=None) == B.SPK_ERR_ARG
+
+
+def _tree(**change):
+    from prompt_compression_b200 import binding as B
+    f = dict(batch=2, layers=1, hq=8, hkv=2, head_dim=128, n_nodes=4, n_pages=10, page_rows=16, n_seqs=2, max_pages=5,
+             dtype=0, scale=1.0)
+    f.update(change)
+    return B.TreeShape(*f.values())
+
+
+@pytest.mark.parametrize("change,status,needle", [
+    (dict(n_nodes=0), 1, ">= 1"),
+    (dict(max_pages=0), 1, ">= 1"),
+    (dict(hq=7), 1, "multiple"),
+    (dict(dtype=2), 1, "dtype"),
+    (dict(scale=0.0), 1, "scale"),
+    (dict(scale=float("inf")), 1, "scale"),
+    (dict(head_dim=96), 2, "head_dim"),
+    (dict(n_nodes=1025), 2, "exceeds 1024"),
+    (dict(batch=1025, n_seqs=1025), 2, "exceeds 1024"),
+    (dict(page_rows=12), 2, "multiple of 8"),
+    (dict(layers=1 << 20, n_pages=1 << 20), 2, "too many"),
+    (dict(layers=1 << 16, max_pages=1 << 16, n_pages=1 << 13), 2, "too many"),
+])
+def test_tree_shape_errors(lib, change, status, needle):
+    s = _tree(**change)
+    assert lib.tree_attention(ctypes.byref(s), 16, 16, 16, 16, 16, None, 16, 16, None, None, 16, None, 16, 1 << 40,
+                              None) == status
+    assert needle in lib.spk_last_error().decode()
+    assert lib.tree_attention_workspace_size(ctypes.byref(s)) == 0
+
+
+def test_tree_pointer_and_workspace_errors(lib):
+    from prompt_compression_b200 import binding as B
+    s = _tree()
+    base = dict(q=16, kp=16, vp=16, table=16, lens=16, seqs=None, kt=16, vt=16, mask=None, live=None, out=16, lse=None,
+                ws=16, n=1 << 40)
+
+    def call(shape=s, **k):
+        a = dict(base, **k)
+        return lib.tree_attention(ctypes.byref(shape), a["q"], a["kp"], a["vp"], a["table"], a["lens"], a["seqs"],
+                                  a["kt"], a["vt"], a["mask"], a["live"], a["out"], a["lse"], a["ws"], a["n"], None)
+
+    assert lib.tree_attention_workspace_size(ctypes.byref(s)) > 0
+    for k in (dict(q=None), dict(kp=None), dict(vp=None), dict(table=None), dict(lens=None), dict(out=None),
+              dict(kt=None), dict(vt=None), dict(q=24), dict(kt=8), dict(out=8), dict(table=18), dict(seqs=2),
+              dict(mask=6), dict(live=1), dict(lse=2), dict(ws=24)):
+        assert call(**k) == B.SPK_ERR_ARG, k
+    assert call(ws=None) == B.SPK_ERR_WORKSPACE
+    assert call(n=lib.tree_attention_workspace_size(ctypes.byref(s)) - 256) == B.SPK_ERR_WORKSPACE
+    assert call(shape=_tree(batch=3)) == B.SPK_ERR_ARG and "n_seqs" in lib.spk_last_error().decode()
+    assert lib.tree_mask(0, 4, 16, None, 16, None, None) == B.SPK_ERR_ARG
+    assert lib.tree_mask(1, 1025, 16, None, 16, None, None) == B.SPK_ERR_UNSUPPORTED
+    assert lib.tree_mask(65536, 4, 16, None, 16, None, None) == B.SPK_ERR_UNSUPPORTED
+    assert lib.tree_mask(1, 4, None, None, 16, None, None) == B.SPK_ERR_ARG
+    assert lib.tree_mask(1, 4, 16, None, 18, None, None) == B.SPK_ERR_ARG

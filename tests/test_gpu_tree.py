@@ -1,0 +1,284 @@
+"""Tree attention over a paged cache and the trees' visibility words, through
+the C ABI, against plain 64-bit implementations: both element types and head
+sizes, groups of 1 to 8 heads, one node to many, empty sequences, rows that see
+nothing, nodes that do not count, pages that end inside a tile, NaN wherever
+no row may look.
+
+Tolerance of out, per element, with e = half a step of the element type and
+A = the weights' sum of |v|: the result's rounding e |out|; the weights'
+rounding e A; the logits, fp32 sums of up to 128 products (at most 2^-24 * 128
+of the sum of |q||k|, below 4e-5 at the tests' scales) and the exponential's
+2^-22: together below 2e-4 of A + |out|, the |out| through the normaliser.
+Weights below the smallest normal number of fp16 keep 2^-25 of the largest:
+n * 2^-25 * max|v|.  lse2: fp32 sums, 2e-4 by the same bound."""
+import numpy as np
+import pytest
+
+from tests import paged_reference as R
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def P():
+    from prompt_compression_b200 import build
+    build.build_library()
+    import prompt_compression_b200 as P
+    P.spk_device_error(clear=True)
+    return P
+
+
+def build_case(seed, dtype, B, L, hq, hkv, d, T, page, lens, live=None, mask="tree", tree=True, spare=1, scale=None,
+               seqs=None, n_seqs=None):
+    """Tensors on the GPU, with NaN in every row that no result may look at,
+    and their fp64 copies by sequence."""
+    import torch
+    rng = np.random.default_rng(seed)
+    live = [T] * B if live is None else live
+    seqs_l = list(range(B)) if seqs is None else seqs
+    n_seqs = max(seqs_l) + 1 if n_seqs is None else n_seqs
+    max_pages = max(1, max(-(-n // page) for n in lens)) + spare
+    need = sum(-(-n // page) for n in lens)
+    n_pages = need + 2
+    order = rng.permutation(n_pages)[:need]
+    table = np.full((n_seqs, max_pages), -1, np.int32)
+    seq_lens = np.zeros(n_seqs, np.int32)
+
+    def half(x):
+        return torch.from_numpy(np.ascontiguousarray(x, np.float32)).to(dtype)
+
+    kp = torch.full((L, n_pages, hkv, page, d), float("nan"), dtype=dtype)
+    vp = torch.full_like(kp, float("nan"))
+    at = 0
+    for b, n in zip(seqs_l, lens):
+        seq_lens[b] = n
+        for x in range(-(-n // page)):
+            pg = int(order[at])
+            at += 1
+            table[b, x] = pg
+            r = min(page, n - x * page)
+            kp[:, pg, :, :r] = half(rng.standard_normal((L, hkv, r, d)))
+            vp[:, pg, :, :r] = half(rng.standard_normal((L, hkv, r, d)))
+    q = half(rng.standard_normal((B, L, hq, T, d)))
+    kt = vt = None
+    if tree:
+        kt, vt = half(rng.standard_normal((B, L, hkv, T, d))), half(rng.standard_normal((B, L, hkv, T, d)))
+        for b in range(B):
+            kt[b, :, :, live[b]:] = float("nan")
+            vt[b, :, :, live[b]:] = float("nan")
+    sees = np.zeros((B, T, T), bool)
+    words = np.zeros((B, T, (T + 31) // 32), np.int32)
+    parents = np.array([[int(rng.integers(-1, i)) for i in range(T)] for _ in range(B)], np.int32)
+    for b in range(B):
+        if mask == "tree":
+            words[b], _ = R.mask_words(parents[b], live[b])
+        elif mask == "random":                       # any bits, some rows empty, some beyond the live nodes
+            w = rng.integers(0, 1 << 32, size=words[b].shape, dtype=np.uint64).astype(np.uint32)
+            w[rng.random(T) < 0.3] = 0
+            words[b] = w.view(np.int32)
+        else:
+            for i in range(T):
+                sees[b, i, :i + 1] = True
+        if mask != "chain":
+            for i in range(T):
+                for j in range(T):
+                    sees[b, i, j] = (int(words[b, i, j // 32]) >> (j % 32)) & 1
+        sees[b, :, live[b]:] = False
+    t = dict(q=q.cuda(), k_pages=kp.cuda(), v_pages=vp.cuda(), page_table=torch.from_numpy(table).cuda(),
+             seq_lens=torch.from_numpy(seq_lens).cuda(), k_tree=None if kt is None else kt.cuda(),
+             v_tree=None if vt is None else vt.cuda(),
+             mask=None if mask == "chain" else torch.from_numpy(words).cuda(),
+             n_live=torch.tensor(live, dtype=torch.int32, device="cuda"), scale=d ** -0.5 if scale is None else scale,
+             seqs=None if seqs is None else torch.tensor(seqs, dtype=torch.int32, device="cuda"))
+    host = dict(q=q.double().numpy(), kp=kp.double().numpy(), vp=vp.double().numpy(), table=table, lens=lens, live=live,
+                kt=None if kt is None else kt.double().numpy(), vt=None if vt is None else vt.double().numpy(),
+                sees=sees, page=page, seqs=seqs_l, scale=t["scale"])
+    return t, host
+
+
+def reference(h, units=None):
+    B, L, hq, T, d = h["q"].shape
+    hkv = h["kp"].shape[2]
+    g = hq // hkv
+    out, lse2, mag = np.zeros(h["q"].shape), np.zeros((B, L, hq, T)), np.zeros(h["q"].shape)
+    for b in range(B):
+        n, lv = h["lens"][b], h["live"][b]
+        pages = h["table"][h["seqs"][b], :-(-n // h["page"])]
+        for l in range(L):
+            for x in range(hkv):
+                k = h["kp"][l, pages, x].reshape(-1, d)[:n]
+                v = h["vp"][l, pages, x].reshape(-1, d)[:n]
+                s = slice(x * g, (x + 1) * g)
+                kt = None if h["kt"] is None else h["kt"][b, l, x, :lv]
+                vt = None if h["vt"] is None else h["vt"][b, l, x, :lv]
+                o, ls, a = R.tree_rows(h["q"][b, l, s, :lv], k, v, kt, vt, h["sees"][b][:lv, :lv], h["scale"])
+                out[b, l, s, :lv], lse2[b, l, s, :lv], mag[b, l, s, :lv] = o, ls, a
+    return out, lse2, mag
+
+
+def check(P, t, h, dtype, **more):
+    import torch
+    out = torch.full_like(t["q"], 7.0)
+    lse2 = torch.full(t["q"].shape[:-1], 7.0, dtype=torch.float32, device="cuda")
+    got = P.tree_attention(**t, out=out, lse2=lse2, **more)
+    torch.cuda.synchronize()
+    assert got is out
+    assert P.spk_device_error() == (0, 0)
+    compare(out, lse2, h, dtype)
+    return out, lse2
+
+
+def compare(out, lse2, h, dtype):
+    import torch
+    ref, ref_lse, mag = reference(h)
+    o, ls = out.double().cpu().numpy(), lse2.double().cpu().numpy()
+    e = torch.finfo(dtype).eps / 2
+    vmax = 6.0
+    n = max(h["lens"]) + h["q"].shape[3]
+    tol = e * (np.abs(ref) + mag) + 2e-4 * (mag + np.abs(ref))
+    if dtype == torch.float16:
+        tol = tol + n * 2.0 ** -25 * vmax
+    for b, lv in enumerate(h["live"]):
+        assert (o[b, :, :, lv:] == 7.0).all() and (ls[b, :, :, lv:] == 7.0).all(), "rows of dead nodes were written"
+        err, ok = np.abs(o[b] - ref[b])[:, :, :lv], tol[b][:, :, :lv]
+        assert (err <= ok).all(), f"element {b}: worst {np.nanmax(err / np.maximum(ok, 1e-30)):.2f} of the tolerance, " \
+            f"{np.isnan(err).sum()} NaN"
+        a, r = ls[b, :, :, :lv], ref_lse[b, :, :, :lv]
+        assert np.array_equal(np.isneginf(a), np.isneginf(r))
+        fin = np.isfinite(r)
+        assert (np.abs(a[fin] - r[fin]) <= 2e-4).all()
+
+
+CASES = [
+    # seed, dtype, B, L, hq, hkv, d, T, page, lens, live, mask, tree
+    (1, "bf16", 1, 1, 8, 8, 128, 1, 16, [1], None, "tree", True),              # one row, one token
+    (2, "bf16", 1, 1, 8, 2, 128, 1, 64, [300], None, "chain", True),           # single-token decoding
+    (3, "bf16", 2, 1, 4, 2, 64, 1, 32, [0, 65], None, "tree", False),          # an empty cache and no tree: zeros
+    (4, "bf16", 1, 2, 10, 2, 128, 7, 64, [320], None, "tree", True),           # g = 5, 35 rows: a 64-row tile
+    (5, "fp16", 3, 1, 8, 2, 128, 4, 16, [129, 64, 3], [4, 2, 1], "tree", True),
+    (6, "bf16", 2, 1, 14, 2, 64, 8, 48, [500, 47], [8, 5], "tree", True),      # g = 7, pages across tiles
+    (7, "fp16", 1, 1, 8, 1, 64, 33, 128, [257], None, "tree", True),           # 264 rows: five row tiles
+    (8, "bf16", 2, 2, 4, 4, 128, 64, 24, [63, 200], [64, 1], "random", True),  # rows that see only the cache
+    (9, "bf16", 2, 1, 4, 4, 128, 16, 8, [0, 0], [16, 9], "random", True),      # no cache: some rows see nothing
+    (10, "bf16", 1, 1, 2, 1, 128, 130, 64, [100], None, "chain", True),        # three node tiles, words 0 .. 4
+    (11, "bf16", 3, 1, 16, 2, 128, 2, 16, [2500, 1, 900], [2, 2, 0], "tree", True),  # split over shares; no live node
+    (12, "fp16", 1, 1, 5, 1, 128, 13, 64, [4097], [12], "random", True),       # 65 rows
+    (13, "bf16", 1, 1, 8, 8, 64, 5, 40, [511], None, "chain", True),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=[str(c[0]) for c in CASES])
+def test_tree_attention_parity(P, case):
+    import torch
+    seed, dt, B, L, hq, hkv, d, T, page, lens, live, mask, tree = case
+    dtype = torch.bfloat16 if dt == "bf16" else torch.float16
+    t, h = build_case(seed, dtype, B, L, hq, hkv, d, T, page, lens, live, mask, tree)
+    check(P, t, h, dtype)
+
+
+def test_sequences_of_a_larger_table_and_peaked_rows(P):
+    import torch
+    t, h = build_case(20, torch.bfloat16, 3, 1, 8, 2, 128, 6, 32, [70, 1000, 31], [6, 3, 6], seqs=[5, 0, 2], n_seqs=9,
+                      scale=1.0)
+    check(P, t, h, torch.bfloat16)
+
+
+def test_the_same_sequence_twice(P):
+    # two trees over one sequence: the batch elements read the same pages
+    import torch
+    t, h = build_case(21, torch.bfloat16, 2, 1, 4, 2, 64, 3, 16, [90, 90], seqs=[0, 1])
+    t["seqs"] = torch.tensor([1, 1], dtype=torch.int32, device="cuda")
+    h["seqs"] = [1, 1]
+    check(P, t, h, torch.bfloat16)
+
+
+def test_results_do_not_depend_on_the_workspace(P):
+    import torch
+    t, h = build_case(22, torch.bfloat16, 1, 1, 8, 2, 128, 9, 64, [3000])
+    shape = P.tree_shape(t["q"], t["k_pages"], t["page_table"], t["scale"])
+    ws = torch.full((P.tree_attention_workspace_size(shape),), 255, dtype=torch.uint8, device="cuda")
+    a, la = check(P, t, h, torch.bfloat16, workspace=ws)
+    b, lb = check(P, t, h, torch.bfloat16)
+    assert torch.equal(a, b) and torch.equal(la, lb)
+
+
+def test_captured_and_replayed_with_a_longer_sequence(P):
+    # the lengths are read when the graph runs: a captured call serves every step
+    import torch
+    t, h = build_case(23, torch.bfloat16, 2, 1, 8, 2, 128, 3, 16, [700, 40], spare=2)
+    full = t["seq_lens"].clone()
+    shape = P.tree_shape(t["q"], t["k_pages"], t["page_table"], t["scale"])
+    ws = torch.empty(P.tree_attention_workspace_size(shape), dtype=torch.uint8, device="cuda")
+    out, lse2 = torch.full_like(t["q"], 7.0), torch.full(t["q"].shape[:-1], 7.0, device="cuda")
+    t["seq_lens"].copy_(torch.tensor([1, 40], dtype=torch.int32))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        P.tree_attention(**t, out=out, lse2=lse2, workspace=ws)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        P.tree_attention(**t, out=out, lse2=lse2, workspace=ws)
+    for lens in ([1, 40], full.tolist()):
+        t["seq_lens"].copy_(torch.tensor(lens, dtype=torch.int32))
+        h["lens"] = lens
+        graph.replay()
+        torch.cuda.synchronize()
+        compare(out, lse2, h, torch.bfloat16)
+    assert P.spk_device_error() == (0, 0)
+
+
+def test_on_another_stream(P):
+    import torch
+    t, h = build_case(24, torch.bfloat16, 1, 1, 8, 2, 128, 5, 16, [400])
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    out = P.tree_attention(**t, stream=side)
+    side.synchronize()
+    ref = P.tree_attention(**t)
+    torch.cuda.synchronize()
+    assert torch.equal(out, ref)
+
+
+def test_bad_elements_keep_their_rows_and_are_recorded(P):
+    import torch
+    t, h = build_case(25, torch.bfloat16, 3, 1, 4, 2, 64, 2, 16, [60, 60, 60], seqs=[0, 1, 2])
+    t["seqs"] = torch.tensor([0, 7, 2], dtype=torch.int32, device="cuda")
+    out = torch.full_like(t["q"], 7.0)
+    P.tree_attention(**t, out=out)
+    st, _ = P.spk_device_error(clear=True)
+    assert st == P.binding.SPK_ERR_ARG
+    assert (out[1] == 7.0).all() and not (out[0] == 7.0).any() and not (out[2] == 7.0).any()
+    t["seqs"] = None
+    t["n_live"] = torch.tensor([2, 2, 3], dtype=torch.int32, device="cuda")
+    out = torch.full_like(t["q"], 7.0)
+    P.tree_attention(**t, out=out)
+    st, _ = P.spk_device_error(clear=True)
+    assert st == P.binding.SPK_ERR_ARG
+    assert (out[2] == 7.0).all() and not (out[0] == 7.0).any()
+
+
+@pytest.mark.parametrize("T", [1, 2, 31, 32, 33, 64, 200, 1024])
+def test_tree_mask(P, T):
+    import torch
+    rng = np.random.default_rng(T)
+    B = 3
+    parents = np.array([[int(rng.integers(-1, i)) for i in range(T)] for _ in range(B)], np.int32)
+    parents[1] = np.arange(T) - 1                                   # a chain
+    live = [T, max(0, T - 3), (T + 1) // 2]
+    mask, depth = P.tree_mask(torch.from_numpy(parents).cuda(), torch.tensor(live, dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    assert P.spk_device_error() == (0, 0)
+    for b in range(B):
+        w, dp = R.mask_words(parents[b], live[b])
+        assert np.array_equal(mask[b].cpu().numpy(), w)
+        assert np.array_equal(depth[b].cpu().numpy(), dp)
+
+
+def test_tree_mask_of_wrong_parents(P):
+    import torch
+    parents = torch.tensor([[-1, 1, 0, 7, -2]], dtype=torch.int32, device="cuda")
+    mask, depth = P.tree_mask(parents)
+    st, _ = P.spk_device_error(clear=True)
+    assert st == P.binding.SPK_ERR_ARG
+    assert mask[0, :, 0].tolist() == [1, 2, 5, 8, 16] and depth[0].tolist() == [0, 0, 1, 0, 0]
