@@ -786,10 +786,10 @@ static spk_status check_tree(const spk_tree_shape* s) {
   if (most > 0x7fffffffLL || rows > 0x7fffffffLL / 2 || units > 0x7fffffffLL / s->batch ||
       static_cast<long long>(s->n_pages) > 0x7fffffffLL / units)
     return fail(SPK_ERR_UNSUPPORTED, "too many units, rows or pages");
-  // tiles of all units (in double: only the order of magnitude matters near the limit)
-  const double tiles = static_cast<double>(s->batch) * units * ((rows + 7) / 8) * (most / kTreeKeys + 1 + s->n_nodes / kTreeKeys + 1);
+  // jobs of all units: 32-bit on the device
   const TreePlan plan = tree_plan(static_cast<int>(rows), s->head_dim, num_sms());
-  if (tiles / (static_cast<double>((rows + 7) / 8)) * plan.row_tiles > 2.0e9)
+  const double tiles = static_cast<double>(most / plan.keys + 1 + s->n_nodes / plan.keys + 1);
+  if (static_cast<double>(s->batch) * units * plan.row_tiles * tiles > 2.0e9)
     return fail(SPK_ERR_UNSUPPORTED, "too many key tiles over all units");
   return SPK_OK;
 }
@@ -847,30 +847,32 @@ spk_status tree_attention(const spk_tree_shape* s, const void* q, const void* k_
   p.q = q; p.out = out; p.lse2 = lse2;
   p.table = table; p.lens = lens; p.seqs = seqs; p.n_live = n_live;
   p.mask = mask; p.words = (s->n_nodes + 31) / 32;
-  p.batch = s->batch; p.layers = s->layers; p.hkv = s->hkv; p.g = g; p.T = s->n_nodes;
+  p.batch = s->batch; p.layers = s->layers; p.hkv = s->hkv; p.T = s->n_nodes;
   p.rows = g * s->n_nodes;
+  p.tile_rows = plan.tile_rows;
   p.row_tiles = plan.row_tiles;
   p.has_tree = k_tree != nullptr;
   p.n_seqs = s->n_seqs; p.max_pages = s->max_pages; p.n_pages = s->n_pages; p.page_rows = s->page_rows;
-  p.box_rows = box_rows_of(s->page_rows, kTreeKeys);
+  p.box_rows = box_rows_of(s->page_rows, plan.keys);
   p.c2 = s->scale * 1.4426950408889634f;
   p.ctas = plan.ctas;
-  p.min_chunk = 1;
+  p.min_share = 1;
   p.part_o = static_cast<float*>(ws);
-  p.part_ml = p.part_o + static_cast<size_t>(plan.ctas) * 2 * plan.tile_rows * s->head_dim;
+  p.part_ml = p.part_o + static_cast<size_t>(plan.ctas) * 2 * plan.item_rows * s->head_dim;
   const bool fp16 = s->dtype == SPK_FP16;
   const long long pool = static_cast<long long>(s->layers) * s->n_pages * s->hkv;
   const long long units = static_cast<long long>(s->batch) * s->layers * s->hkv;
-  CUtensorMap maps[4];
+  CUtensorMap maps[5];
   st = make_map16(&maps[0], fp16, k_pages, s->head_dim, s->page_rows, pool, p.box_rows);
   if (st == SPK_OK) st = make_map16(&maps[1], fp16, v_pages, s->head_dim, s->page_rows, pool, p.box_rows);
   if (st == SPK_OK && k_tree != nullptr) {
-    st = make_map16(&maps[2], fp16, k_tree, s->head_dim, s->n_nodes, units, kTreeKeys);
-    if (st == SPK_OK) st = make_map16(&maps[3], fp16, v_tree, s->head_dim, s->n_nodes, units, kTreeKeys);
+    st = make_map16(&maps[2], fp16, k_tree, s->head_dim, s->n_nodes, units, plan.keys);
+    if (st == SPK_OK) st = make_map16(&maps[3], fp16, v_tree, s->head_dim, s->n_nodes, units, plan.keys);
   } else {
     maps[2] = maps[0];
     maps[3] = maps[1];
   }
+  if (st == SPK_OK && plan.wide) st = make_map16(&maps[4], fp16, q, s->head_dim, p.rows, units, 128);
   if (st != SPK_OK) return st;
   cudaError_t e = launch_tree_attention(fp16, s->head_dim, maps, p, plan, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ok() : cuda_fail(e, "tree attention launch");
@@ -907,7 +909,7 @@ spk_status spk_device_error(int* status, int* site, int clear) {
   // reported (the others are cleared with it)
   cudaError_t (*const readers[])(int*, int*, bool) = {device_errors_api, device_errors_score, device_errors_attn,
                                                        device_errors_vs, device_errors_compact, device_errors_pages,
-                                                       device_errors_tree};
+                                                       device_errors_tree, device_errors_tree_umma};
   int code = 0, where = 0;
   for (auto rd : readers) {
     int c = 0, w = 0;

@@ -45,10 +45,9 @@ cudaError_t launch_pages_compact(const PagesShape& s, const PagesBook& b, void* 
                                  int units_per_idx, int* result, void* ws, cudaStream_t stream);
 cudaError_t device_errors_pages(int* code, int* site, bool clear);
 
-// ----------------------------------------------------------------- tree.cu
+// ---------------------------------------------------- tree.cu, tree_umma.cu
 constexpr int kTreeMaxBatch = 1024;
 constexpr int kTreeMaxNodes = 1024;
-constexpr int kTreeKeys = 64;         // keys of a tile
 
 struct TreeParams {
   const void* q;           // [batch][layers][hq][T][d]
@@ -60,22 +59,26 @@ struct TreeParams {
   const int* n_live;       // [batch] or null (every node is live)
   const uint32_t* mask;    // [batch][T][words] or null (node i sees the nodes 0 .. i)
   int words;
-  int batch, layers, hkv, g, T;
+  int batch, layers, hkv, T;
   int rows;                // query rows per unit = g * T, ordered [query head][node]
+  int tile_rows;           // query rows of a row tile (wide kernel: 128)
   int row_tiles;           // row tiles per unit
   int has_tree;            // k_tree and v_tree are given
   int n_seqs, max_pages, n_pages, page_rows;
-  int box_rows;            // rows of one page copy: divides page_rows and the tile
+  int box_rows;            // rows of one page copy: divides page_rows and the key tile
   float c2;                // scale * log2(e)
   int ctas;                // CTAs of the main kernel
-  int min_chunk;           // key tiles a CTA takes at least
-  float* part_o;           // [ctas * 2][tile rows][d] partial outputs
-  float* part_ml;          // [ctas * 2][tile rows][2] their row maxima and sums
+  int min_share;           // jobs a CTA takes at least
+  float* part_o;           // [ctas * 2][rows of an item][d] partial outputs
+  float* part_ml;          // [ctas * 2][rows of an item][2] their row maxima and sums
 };
 
 struct TreePlan {
-  int tile_rows;           // query rows of a tile
-  int row_tiles;
+  bool wide;               // tree_umma.cu (row tiles of 128, two to an item) or tree.cu
+  int keys;                // keys of a tile
+  int tile_rows, row_tiles;
+  int item_rows;           // query rows of an item
+  int items;               // items per unit
   int ctas;
 };
 TreePlan tree_plan(int rows, int head_dim, int sms);
@@ -83,11 +86,14 @@ size_t tree_ws_bytes(const TreePlan& plan, int head_dim);
 
 // maps: k_pages, v_pages [layers * n_pages * hkv][page_rows][d] in boxes of
 // box_rows x 64; k_tree, v_tree [batch * layers * hkv][T][d] in boxes of
-// kTreeKeys x 64
-cudaError_t launch_tree_attention(bool fp16, int head_dim, const CUtensorMap (&maps)[4], const TreeParams& p,
+// plan.keys x 64; q [batch * layers * hkv][rows][d] in boxes of 128 x 64 (wide only)
+cudaError_t launch_tree_attention(bool fp16, int head_dim, const CUtensorMap (&maps)[5], const TreeParams& p,
                                   const TreePlan& plan, cudaStream_t stream);
+cudaError_t launch_tree_umma(bool fp16, int head_dim, const CUtensorMap (&maps)[5], const TreeParams& p,
+                             cudaStream_t stream);
 cudaError_t launch_tree_mask(const int* parents, const int* n_live, int batch, int T, uint32_t* mask, int* depth,
                              cudaStream_t stream);
 cudaError_t device_errors_tree(int* code, int* site, bool clear);
+cudaError_t device_errors_tree_umma(int* code, int* site, bool clear);
 
 }  // namespace spk

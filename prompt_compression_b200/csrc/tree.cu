@@ -6,17 +6,18 @@
 //   out  = sum_j 2^(c2 s_j - m) v_j / sum_j 2^(c2 s_j - m),  lse2 = m + log2 sum,
 // in one pass with the running maximum m and sum (log2 domain, fp32).
 //
-// Work split: the key tiles (64 keys: first the cached rows, then the nodes)
-// of all units, in the order (batch element, layer, KV head, row tile, tile),
-// form one sequence that the CTAs take in equal consecutive shares, so ragged
-// lengths balance and a few long sequences still fill the GPU.  The shares
-// follow from seq_lens on the device.  A unit inside one share is finished
-// there; the others leave (m, sum, unnormalised output) of each share in the
-// workspace, and tree_join_kernel adds them in the order of the shares: the
-// results do not depend on timing.
+// This kernel has the units of few query rows (row tiles of 8 to 64, on
+// mma.sync); tree_umma.cu has the others.  How the work is shared out:
+// tree_shares.cuh.  An item inside one share is finished there; the others
+// leave (m, sum, unnormalised output) of each share in the workspace, and
+// tree_join_kernel adds them in the order of the shares: the results do not
+// depend on timing.
+#include <type_traits>
+
 #include "common.cuh"
 #include "mma.cuh"
 #include "paged.cuh"
+#include "tree_shares.cuh"
 
 namespace spk {
 
@@ -24,104 +25,12 @@ SPK_ERROR_READER(device_errors_tree)
 
 namespace {
 
+constexpr int kTreeKeys = 64;                   // keys of a tile
 constexpr int kWarps = 4;                       // consumer warps
 constexpr int kThreads = (kWarps + 1) * 32;     // and the producer warp
 constexpr int kSmemPerCta = 113 * 1024;         // two CTAs share an SM
 
 __device__ __forceinline__ int site(int which) { return 600 + which; }
-
-// --------------------------------------------------------------------------
-// the shares
-// --------------------------------------------------------------------------
-struct Element {           // a batch element
-  int seq, len, live, tiles;
-};
-
-// Length and live nodes of batch element b; an element whose sequence, length
-// or node count is out of range has no rows (its outputs stay unwritten).
-__device__ __forceinline__ Element element_of(const TreeParams& p, int b, bool record) {
-  Element e;
-  e.seq = p.seqs != nullptr ? __ldg(p.seqs + b) : b;
-  e.live = p.n_live != nullptr ? __ldg(p.n_live + b) : p.T;
-  bool ok = e.seq >= 0 && e.seq < p.n_seqs && e.live >= 0 && e.live <= p.T;
-  e.len = ok ? __ldg(p.lens + e.seq) : 0;
-  ok = ok && e.len >= 0 && e.len <= static_cast<long long>(p.max_pages) * p.page_rows;
-  if (!ok) {
-    if (record) record_error(SPK_DEVERR_INDEX, b);
-    e.seq = 0;
-    e.len = 0;
-    e.live = 0;
-  }
-  const int nodes = p.has_tree ? (e.live + kTreeKeys - 1) / kTreeKeys : 0;
-  const int t = (e.len + kTreeKeys - 1) / kTreeKeys + nodes;
-  e.tiles = e.live == 0 ? 0 : (t > 0 ? t : 1);   // rows without any key still get their zeros
-  return e;
-}
-
-// prefix[b] = tiles of the batch elements before b, by the calling warp.
-__device__ __forceinline__ void tree_prefix(const TreeParams& p, int* prefix, bool record) {
-  const int lane = threadIdx.x & 31;
-  const int units = p.layers * p.hkv * p.row_tiles;
-  int base = 0;
-  for (int b0 = 0; b0 < p.batch; b0 += 32) {
-    const int b = b0 + lane;
-    const int x = b < p.batch ? element_of(p, b, record).tiles * units : 0;
-    int s = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += y;
-    }
-    if (b < p.batch) prefix[b] = base + s - x;
-    base += __shfl_sync(0xffffffffu, s, 31);
-  }
-  if (lane == 0) prefix[p.batch] = base;
-}
-
-__device__ __forceinline__ int share_of(const TreeParams& p, int total) {
-  const int even = (total + p.ctas - 1) / p.ctas;
-  return even > p.min_chunk ? even : p.min_chunk;
-}
-
-// The part of a share that lies in one unit: tiles [t0, t1) of its `e.tiles`.
-struct Run {
-  int b, unit, row0, t0, t1;   // unit = (b * layers + l) * hkv + h; row0 = first row of the row tile
-  Element e;
-};
-
-struct Walker {
-  int x, end, b;
-  __device__ __forceinline__ bool next(const TreeParams& p, const int* prefix, int tile_rows, Run& r) {
-    if (x >= end) return false;
-    while (x >= prefix[b + 1]) ++b;
-    r.b = b;
-    r.e = element_of(p, b, false);
-    const int y = x - prefix[b];
-    const int w = y / r.e.tiles;
-    r.t0 = y - w * r.e.tiles;
-    r.t1 = min(r.e.tiles, r.t0 + (end - x));
-    const int lh = w / p.row_tiles;
-    r.unit = b * p.layers * p.hkv + lh;
-    r.row0 = (w - lh * p.row_tiles) * tile_rows;
-    x += r.t1 - r.t0;
-    return true;
-  }
-};
-
-// Keys of tile t of a batch element: [0, n) of the tile are there.
-struct Tile {
-  bool cached;
-  int first;      // first cached row or first node
-  int n;
-};
-__device__ __forceinline__ Tile tile_of(const TreeParams& p, const Element& e, int t) {
-  Tile k;
-  const int cached = (e.len + kTreeKeys - 1) / kTreeKeys;
-  k.cached = t < cached;
-  k.first = (k.cached ? t : t - cached) * kTreeKeys;
-  k.n = k.cached ? min(kTreeKeys, e.len - k.first) : (p.has_tree ? min(kTreeKeys, e.live - k.first) : 0);
-  return k;
-}
 
 // --------------------------------------------------------------------------
 // main kernel
@@ -134,7 +43,7 @@ struct TreeCfg {
   static constexpr int kStageBytes = 2 * kAtoms * kHalf;
   static constexpr int kQBytes = kRows * D * 2;
   static constexpr int kPBytes = kRows * kTreeKeys * 2;
-  static constexpr int kStages = (kSmemPerCta - 2048 - 1024 - kTreeMaxBatch * 4 - 4 * kRows * 8 - kQBytes - kPBytes) /
+  static constexpr int kStages = (kSmemPerCta - 2048 - 1024 - 4 * kRows * 4 - kQBytes - kPBytes) /
                                  kStageBytes;
   static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kQBytes + kPBytes;
   static_assert(kStages >= 2, "a tile is loaded while another is used");
@@ -167,7 +76,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t q_s = smem_u32(q_p), p_s = q_s + C::kQBytes;
 
   __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages];
-  __shared__ int prefix[kTreeMaxBatch + 1];
+  __shared__ TreeStart start_s;
   __shared__ __align__(16) float wmax[kWarps][C::kRows];   // read and written in pairs
   __shared__ int abort_flag;
 
@@ -180,18 +89,19 @@ __global__ void __launch_bounds__(kThreads, 2)
     abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 0) tree_prefix(p, prefix, blockIdx.x == 0);
+  if (warp == 0) {
+    const TreeStart s = tree_start<kTreeKeys>(p, blockIdx.x, blockIdx.x == 0);
+    if (lane == 0) start_s = s;
+  }
   if (warp == kWarps && lane == 0) {
     tma_prefetch_map(&kmap);
     tma_prefetch_map(&vmap);
   }
   __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   volatile int* const abort_v = &abort_flag;
-  const int total = prefix[p.batch];
-  const int share = share_of(p, total);
-  const int begin = static_cast<int>(min(static_cast<long long>(total), static_cast<long long>(share) * blockIdx.x));
-  Walker walk{begin, min(total - begin, share) + begin, 0};
-  Run run;
+  TreeWalker<kTreeKeys, false> walk(start_s);
+  TreeRun run;
 
   if (warp == kWarps) {
     // ---------------------------------------------------------------- producer
@@ -200,12 +110,12 @@ __global__ void __launch_bounds__(kThreads, 2)
     int last[C::kStages];
 #pragma unroll
     for (int s = 0; s < C::kStages; ++s) last[s] = -1;
-    while (ok && walk.next(p, prefix, C::kRows, run)) {
+    while (ok && walk.next(p, run)) {
       const int* row = p.table + static_cast<size_t>(run.e.seq) * p.max_pages;
       const int lh = run.unit - run.b * p.layers * p.hkv;
       const int layer = lh / p.hkv, head = lh - layer * p.hkv;
       for (int t = run.t0; t < run.t1; ++t, ++count) {
-        const Tile tile = tile_of(p, run.e, t);
+        const TreeTile tile = tree_tile<kTreeKeys>(p, run.e, t);
         const int st = count % C::kStages;
         const uint32_t ph = (count / C::kStages) & 1;
         // lane i: the page of box i of the tile
@@ -267,8 +177,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     // barriers (every later wait returns at once) and the error word says so.
     const int gr = lane >> 2, gc = lane & 3;
     uint32_t count = 0;
-    int runs = 0;
-    while (walk.next(p, prefix, C::kRows, run)) {
+    while (walk.next(p, run)) {
       const int rows = min(C::kRows, p.rows - run.row0);     // rows of this tile that exist
       // Q rows of the tile (they lie together: a unit's heads and nodes), zeros behind them
       {
@@ -291,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int j = 0; j < MT; ++j) o[j][n][0] = o[j][n][1] = o[j][n][2] = o[j][n][3] = 0.f;
       }
       for (int t = run.t0; t < run.t1; ++t, ++count) {
-        const Tile tile = tile_of(p, run.e, t);
+        const TreeTile tile = tree_tile<kTreeKeys>(p, run.e, t);
         const int st = count % C::kStages;
         const uint32_t ks = stage_s + st * C::kStageBytes, vs = ks + C::kAtoms * C::kHalf;
         const int key0 = warp * 16;
@@ -485,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             dst[x] = *reinterpret_cast<const uint4*>(q_p + row * (D * 2) + ((ch ^ (row & 7)) << 4));
         }
       } else {
-        const size_t part = (static_cast<size_t>(blockIdx.x) * 2 + (runs > 0 ? 1 : 0)) * C::kRows;
+        const size_t part = (static_cast<size_t>(blockIdx.x) * 2 + run.slot) * C::kRows;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -502,69 +411,157 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
       consumers_sync();                          // Q, the staged outputs and the sums are free
-      ++runs;
     }
   }
 }
 
 // --------------------------------------------------------------------------
-// the units that several shares hold
+// the items that several shares hold
 // --------------------------------------------------------------------------
-// Block (c, y): the unit that the border between shares c - 1 and c cuts, if
-// this is the first border inside it; rows y * 4 .. of its row tile, a warp a
-// row.  A row's shares are added in their order:
+// A row's shares are added in their order:
 //   M = max m_c,  out = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) tree_join_kernel(const __grid_constant__ TreeParams p, int tile_rows) {
-  __shared__ int prefix[kTreeMaxBatch + 1];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == 0) tree_prefix(p, prefix, false);
-  __syncthreads();
-  const int total = prefix[p.batch];
-  const int share = share_of(p, total);
-  const int c = blockIdx.x + 1;
-  if (static_cast<long long>(c) * share >= total) return;
-  const int x = c * share;
-  int b = 0;
-  while (x >= prefix[b + 1]) ++b;
-  const Element e = element_of(p, b, false);
-  const int w = (x - prefix[b]) / e.tiles;
-  const int u0 = prefix[b] + w * e.tiles, u1 = u0 + e.tiles;
-  const int c0 = u0 / share, c1 = (u1 - 1) / share;
-  if (u0 == x || c0 != c - 1) return;
-  const int lh = w / p.row_tiles;
-  const size_t unit = static_cast<size_t>(b) * p.layers * p.hkv + lh;
-  const int row = blockIdx.y * 4 + warp;                     // in the row tile
-  const int r = (w - lh * p.row_tiles) * tile_rows + row;    // in the unit
-  if (row >= tile_rows || r >= p.rows || r % p.T >= e.live) return;
+// A block has one item and MANY ? one row of it (eight warps, each every
+// eighth share) : 32 rows (a warp takes four, one after the other).
+// by_border: the item that the border between shares c and c + 1 cuts, if this
+// is the first border inside it; otherwise item c of the call.  The blocks
+// start while the main kernel still runs and find their item (the line does
+// not depend on it), and wait before they read; every block waits, so the
+// join ends after the main kernel.
+constexpr int kJoinWarps = 8;
+constexpr int kJoinRows = 32;                   // rows of a block (not MANY)
 
-  auto slot = [&](int i) { return (static_cast<size_t>(i) * 2 + (i == c0 && u0 > c0 * share ? 1 : 0)) * tile_rows + row; };
-  float M = -INFINITY;
-  for (int i = c0 + lane; i <= c1; i += 32) M = fmaxf(M, p.part_ml[slot(i) * 2]);
+template <typename T, int D, int KEYS, bool PAIRS, bool MANY>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+    tree_join_kernel(const __grid_constant__ TreeParams p, int item_rows, bool by_border) {
+  constexpr int V = D / 32;                     // columns a lane
+  constexpr int W = MANY ? kJoinWarps : 1;      // warps a row
+  __shared__ float acc_s[MANY ? kJoinWarps : 1][D], l_s[kJoinWarps], m_s[kJoinWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  TreeStart s = tree_start<KEYS>(p, by_border ? blockIdx.x + 1 : 0, false);
+  int x = s.begin;
+  if (!by_border) {                             // every unit has the same number of items
+    const int per = PAIRS ? (p.row_tiles + 1) / 2 : p.row_tiles;
+    const int unit = blockIdx.x / per, k = blockIdx.x - unit * per, of_b = p.layers * p.hkv;
+    s.b = unit / of_b;
+    int before = 0;
+    for (int b = lane; b < s.b; b += 32) before += tree_jobs(p, tree_element<KEYS>(p, b, false));
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  const float ref = M == -INFINITY ? 0.f : M;
-  constexpr int V = D / 32;
-  float acc[V], L = 0.f;
-#pragma unroll
-  for (int v = 0; v < V; ++v) acc[v] = 0.f;
-  for (int i = c0; i <= c1; ++i) {
-    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + slot(i) * 2);
-    const float f = ex2_approx(ml.x - ref);
-    L = fmaf(ml.y, f, L);
-    const float* src = p.part_o + slot(i) * D + lane * V;
-#pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] = fmaf(src[v], f, acc[v]);
+    for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+    s.base = before;
+    const int tiles = tree_element<KEYS>(p, s.b, false).tiles;
+    x = tiles == 0 ? s.total : before + (unit - s.b * of_b) * tiles * p.row_tiles + k * tiles * (PAIRS ? 2 : 1);
   }
-  const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
-  uint32_t* dst = reinterpret_cast<uint32_t*>(p.out) + (unit * p.rows + r) * (D / 2) + lane * (V / 2);
+  TreeElement e{};
+  TreeItem item{};
+  int c0 = 0, c1 = 0;
+  if (x < s.total) {
+    e = tree_element<KEYS>(p, s.b, false);
+    item = tree_item<PAIRS>(p, e, s.b, s.base, x);
+    c0 = item.first / s.share;
+    c1 = (item.first + item.jobs - 1) / s.share;
+    if (by_border && (item.first == x || c0 != static_cast<int>(blockIdx.x))) c1 = c0;
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (c0 == c1) return;                         // no item, or one share has it
+  const int rows_here = min(PAIRS ? (item.pair ? 256 : 128) : item_rows, p.rows - item.row0);
+  const int row_end = MANY ? blockIdx.y + 1 : min(rows_here, static_cast<int>(blockIdx.y + 1) * kJoinRows);
+  for (int row = MANY ? blockIdx.y : blockIdx.y * kJoinRows + warp; row < row_end; row += kJoinWarps) {
+    const int r = item.row0 + row;              // in the unit
+    if (row >= rows_here || r % p.T >= e.live) {
+      if (MANY) return;                         // the whole block
+      continue;
+    }
+    float m = -INFINITY, l = 0.f, acc[V];
 #pragma unroll
-  for (int v = 0; v < V; v += 2) dst[v / 2] = Half16<T>::pack(acc[v] * inv, acc[v + 1] * inv);
-  if (lane == 0 && p.lse2 != nullptr) p.lse2[unit * p.rows + r] = L == 0.f ? -INFINITY : M + lg2_approx(L);
+    for (int v = 0; v < V; ++v) acc[v] = 0.f;
+    // four shares at a time: their loads are in flight together
+    for (int i0 = c0 + (MANY ? warp : 0); i0 <= c1; i0 += 4 * W) {
+      float2 ml[4];
+      float o[4][V];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + u * W;
+        int t0 = 0, t1 = 0, slot = 0;
+        if (i <= c1) tree_part(item, e.tiles, i * s.share, (i + 1) * s.share, t0, t1, slot);
+        ml[u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[u][v] = 0.f;
+        if (t0 < t1) {
+          const size_t at = (static_cast<size_t>(i) * 2 + slot) * item_rows + row;
+          ml[u] = __ldcs(reinterpret_cast<const float2*>(p.part_ml + at * 2));
+#pragma unroll
+          for (int v = 0; v < V; v += 2) {
+            const float2 y = __ldcs(reinterpret_cast<const float2*>(p.part_o + at * D + lane * V + v));
+            o[u][v] = y.x;
+            o[u][v + 1] = y.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float M = fmaxf(m, ml[u].x), ref = M == -INFINITY ? 0.f : M;
+        const float a = ex2_approx(m - ref), f = ex2_approx(ml[u].x - ref);
+        l = fmaf(l, a, ml[u].y * f);
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] = fmaf(acc[v], a, o[u][v] * f);
+        m = M;
+      }
+    }
+    if (MANY) {                                 // the row's warps, in their order
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc_s[MANY ? warp : 0][lane * V + v] = acc[v];
+      if (lane == 0) {
+        m_s[warp] = m;
+        l_s[warp] = l;
+      }
+      __syncthreads();
+      if (warp != 0) return;
+      float M = m;
+      for (int w = 1; w < kJoinWarps; ++w) M = fmaxf(M, m_s[w]);
+      const float ref = M == -INFINITY ? 0.f : M;
+      const float a = ex2_approx(m - ref);
+      l *= a;
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] *= a;
+      for (int w = 1; w < kJoinWarps; ++w) {
+        const float f = ex2_approx(m_s[w] - ref);
+        l = fmaf(l_s[w], f, l);
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] = fmaf(acc_s[MANY ? w : 0][lane * V + v], f, acc[v]);
+      }
+      m = M;
+    }
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out) + (static_cast<size_t>(item.unit) * p.rows + r) * (D / 2) + lane * (V / 2);
+#pragma unroll
+    for (int v = 0; v < V; v += 2) dst[v / 2] = Half16<T>::pack(acc[v] * inv, acc[v + 1] * inv);
+    if (lane == 0 && p.lse2 != nullptr)
+      p.lse2[static_cast<size_t>(item.unit) * p.rows + r] = l == 0.f ? -INFINITY : m + lg2_approx(l);
+  }
+}
+
+template <typename T, int D, int KEYS, bool PAIRS>
+cudaError_t launch_join(const TreeParams& p, const TreePlan& plan, cudaStream_t stream) {
+  if (plan.ctas == 1) return cudaSuccess;
+  const long long items = static_cast<long long>(p.batch) * p.layers * p.hkv * plan.items;
+  const bool by_border = items > plan.ctas - 1;
+  const int rows = p.rows < plan.item_rows ? p.rows : plan.item_rows;
+  const bool many = items * 4 <= plan.ctas;     // many shares an item: eight warps a row
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(by_border ? plan.ctas - 1 : static_cast<unsigned>(items), many ? rows : (rows + kJoinRows - 1) / kJoinRows);
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return many ? cudaLaunchKernelEx(&cfg, tree_join_kernel<T, D, KEYS, PAIRS, true>, p, plan.item_rows, by_border)
+              : cudaLaunchKernelEx(&cfg, tree_join_kernel<T, D, KEYS, PAIRS, false>, p, plan.item_rows, by_border);
 }
 
 template <typename T, int D, int NT>
-cudaError_t launch_nt(const CUtensorMap (&maps)[4], const TreeParams& p, const TreePlan& plan, cudaStream_t stream) {
+cudaError_t launch_nt(const CUtensorMap (&maps)[5], const TreeParams& p, const TreePlan& plan, cudaStream_t stream) {
   using C = TreeCfg<D, NT>;
   static thread_local int configured_device = -1;
   int dev = 0;
@@ -576,20 +573,22 @@ cudaError_t launch_nt(const CUtensorMap (&maps)[4], const TreeParams& p, const T
     configured_device = dev;
   }
   tree_kernel<T, D, NT><<<plan.ctas, kThreads, C::kSmemBytes, stream>>>(maps[0], maps[1], maps[2], maps[3], p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || plan.ctas == 1) return e;
-  tree_join_kernel<T, D><<<dim3(plan.ctas - 1, (C::kRows + 3) / 4), 128, 0, stream>>>(p, C::kRows);
   return cudaGetLastError();
 }
 
 template <typename T, int D>
-cudaError_t launch_d(const CUtensorMap (&maps)[4], const TreeParams& p, const TreePlan& plan, cudaStream_t stream) {
-  switch (plan.tile_rows) {
-    case 8: return launch_nt<T, D, 1>(maps, p, plan, stream);
-    case 16: return launch_nt<T, D, 2>(maps, p, plan, stream);
-    case 32: return launch_nt<T, D, 4>(maps, p, plan, stream);
-    default: return launch_nt<T, D, 8>(maps, p, plan, stream);
+cudaError_t launch_d(const CUtensorMap (&maps)[5], const TreeParams& p, const TreePlan& plan, cudaStream_t stream) {
+  if (plan.wide) {
+    cudaError_t e = launch_tree_umma(std::is_same<T, __half>::value, D, maps, p, stream);
+    return e != cudaSuccess ? e : launch_join<T, D, 128, true>(p, plan, stream);
   }
+  cudaError_t e;
+  switch (plan.tile_rows) {
+    case 8: e = launch_nt<T, D, 1>(maps, p, plan, stream); break;
+    case 16: e = launch_nt<T, D, 2>(maps, p, plan, stream); break;
+    default: e = launch_nt<T, D, 4>(maps, p, plan, stream); break;
+  }
+  return e != cudaSuccess ? e : launch_join<T, D, kTreeKeys, false>(p, plan, stream);
 }
 
 // --------------------------------------------------------------------------
@@ -643,19 +642,25 @@ __global__ void __launch_bounds__(128) tree_mask_kernel(const int* __restrict__ 
 
 }  // namespace
 
+// Up to 32 rows a unit fit one narrow tile, which wastes less than a tile of
+// 128 rows; above that the tcgen05 kernel.
 TreePlan tree_plan(int rows, int head_dim, int sms) {
   TreePlan plan;
-  plan.tile_rows = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  plan.wide = rows > 32;
+  plan.keys = plan.wide ? 128 : kTreeKeys;
+  plan.tile_rows = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 128;
   plan.row_tiles = (rows + plan.tile_rows - 1) / plan.tile_rows;
-  plan.ctas = 2 * sms;
+  plan.item_rows = plan.wide && rows > 128 ? 256 : plan.tile_rows;
+  plan.items = (rows + plan.item_rows - 1) / plan.item_rows;
+  plan.ctas = plan.wide ? sms : 2 * sms;
   return plan;
 }
 
 size_t tree_ws_bytes(const TreePlan& plan, int head_dim) {
-  return static_cast<size_t>(plan.ctas) * 2 * plan.tile_rows * (head_dim + 2) * sizeof(float);
+  return static_cast<size_t>(plan.ctas) * 2 * plan.item_rows * (head_dim + 2) * sizeof(float);
 }
 
-cudaError_t launch_tree_attention(bool fp16, int head_dim, const CUtensorMap (&maps)[4], const TreeParams& p,
+cudaError_t launch_tree_attention(bool fp16, int head_dim, const CUtensorMap (&maps)[5], const TreeParams& p,
                                   const TreePlan& plan, cudaStream_t stream) {
   if (head_dim == 128)
     return fp16 ? launch_d<__half, 128>(maps, p, plan, stream) : launch_d<__nv_bfloat16, 128>(maps, p, plan, stream);

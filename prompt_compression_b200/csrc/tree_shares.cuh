@@ -1,0 +1,189 @@
+// tree_shares.cuh -- how the tree attention's work is shared out.
+//
+// A unit is one (batch element, layer, KV head); its query rows are the
+// element's nodes of the unit's g query heads.  An item is a part of a unit's
+// rows that one CTA takes at a time, with all of the unit's key tiles (first
+// the cached rows, then the nodes).  The items of all units, in the order
+// (batch element, layer, KV head, rows, key tile), form one line of jobs, and
+// CTA c takes the jobs [c * share, (c + 1) * share): ragged lengths balance,
+// and a few long sequences still fill the GPU.  The line follows from seq_lens
+// on the device; kernel and join compute it alike.
+//   narrow kernel (PAIRS false): an item is one row tile, a job one key tile
+//   wide kernel (PAIRS true):    row tiles of 128, two to an item while there
+//     are two left (a job is then one (row tile, key tile); a border between
+//     shares falls on the key tile that holds it)
+#pragma once
+
+#include "common.cuh"
+#include "paged.cuh"
+
+namespace spk {
+
+struct TreeElement {       // a batch element
+  int seq, len, live, tiles;
+};
+
+// Length and live nodes of batch element b; an element whose sequence, length
+// or node count is out of range has no rows (its outputs stay unwritten).
+template <int KEYS>
+__device__ __forceinline__ TreeElement tree_element(const TreeParams& p, int b, bool record) {
+  TreeElement e;
+  e.seq = p.seqs != nullptr ? __ldg(p.seqs + b) : b;
+  e.live = p.n_live != nullptr ? __ldg(p.n_live + b) : p.T;
+  bool ok = e.seq >= 0 && e.seq < p.n_seqs && e.live >= 0 && e.live <= p.T;
+  e.len = ok ? __ldg(p.lens + e.seq) : 0;
+  ok = ok && e.len >= 0 && e.len <= static_cast<long long>(p.max_pages) * p.page_rows;
+  if (!ok) {
+    if (record) record_error(SPK_DEVERR_INDEX, b);
+    e.seq = 0;
+    e.len = 0;
+    e.live = 0;
+  }
+  const int nodes = p.has_tree ? (e.live + KEYS - 1) / KEYS : 0;
+  const int t = (e.len + KEYS - 1) / KEYS + nodes;
+  e.tiles = e.live == 0 ? 0 : (t > 0 ? t : 1);   // rows without any key still get their zeros
+  return e;
+}
+
+// Keys of tile t of an element: [first, first + n) of the cached rows or of the nodes.
+struct TreeTile {
+  bool cached;
+  int first, n;
+};
+template <int KEYS>
+__device__ __forceinline__ TreeTile tree_tile(const TreeParams& p, const TreeElement& e, int t) {
+  TreeTile k;
+  const int cached = (e.len + KEYS - 1) / KEYS;
+  k.cached = t < cached;
+  k.first = (k.cached ? t : t - cached) * KEYS;
+  k.n = k.cached ? min(KEYS, e.len - k.first) : (p.has_tree ? min(KEYS, e.live - k.first) : 0);
+  return k;
+}
+
+__device__ __forceinline__ int tree_jobs(const TreeParams& p, const TreeElement& e) {
+  return e.tiles * p.row_tiles * p.layers * p.hkv;
+}
+
+struct TreeStart {
+  int total, share;
+  int begin, end;          // the CTA's jobs
+  int b, base;             // the batch element that holds `begin`, and the jobs before it
+};
+
+// The share of CTA `cta`, by the calling warp (every lane gets it).
+template <int KEYS>
+__device__ __forceinline__ TreeStart tree_start(const TreeParams& p, int cta, bool record) {
+  const int lane = threadIdx.x & 31;
+  TreeStart s;
+  int jobs = lane < p.batch ? tree_jobs(p, tree_element<KEYS>(p, lane, record)) : 0;
+  const int first32 = jobs;
+  for (int b = lane + 32; b < p.batch; b += 32) jobs += tree_jobs(p, tree_element<KEYS>(p, b, record));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) jobs += __shfl_xor_sync(0xffffffffu, jobs, o);
+  s.total = jobs;
+  const int even = (s.total + p.ctas - 1) / p.ctas;
+  s.share = even > p.min_share ? even : p.min_share;
+  const long long begin = static_cast<long long>(s.share) * cta;
+  s.begin = begin < s.total ? static_cast<int>(begin) : s.total;
+  s.end = s.begin + min(s.total - s.begin, s.share);
+  s.b = 0;
+  s.base = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += 32) {
+    const int b = b0 + lane;
+    const int x = b0 == 0 ? first32 : (b < p.batch ? tree_jobs(p, tree_element<KEYS>(p, b, false)) : 0);
+    int sum = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += y;
+    }
+    const int base = s.base + sum - x;                         // jobs before element b
+    const uint32_t in = __ballot_sync(0xffffffffu, s.begin >= base && s.begin < base + x);
+    if (in != 0) {
+      const int at = __ffs(in) - 1;
+      s.b = b0 + at;
+      s.base = __shfl_sync(0xffffffffu, base, at);
+      return s;
+    }
+    s.base += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  return s;                                                    // no jobs: begin == end == total
+}
+
+// An item as the line holds it: jobs [first, first + jobs).
+struct TreeItem {
+  int unit, row0;          // unit = (b * layers + l) * hkv + h
+  bool pair;
+  int first, jobs;
+};
+
+// The item that holds job x of batch element b, whose jobs begin at base.
+template <bool PAIRS>
+__device__ __forceinline__ TreeItem tree_item(const TreeParams& p, const TreeElement& e, int b, int base, int x) {
+  TreeItem i;
+  const int per = e.tiles * p.row_tiles;                       // jobs of a unit
+  const int y = x - base;
+  const int lh = y / per;
+  const int z = y - lh * per;
+  i.unit = b * p.layers * p.hkv + lh;
+  if (PAIRS) {
+    const int k = z / (2 * e.tiles);
+    i.pair = 2 * k + 1 < p.row_tiles;
+    i.row0 = k * 256;
+    i.first = base + lh * per + k * 2 * e.tiles;
+    i.jobs = i.pair ? 2 * e.tiles : e.tiles;
+  } else {
+    const int k = z / e.tiles;
+    i.pair = false;
+    i.row0 = k * p.tile_rows;
+    i.first = base + lh * per + k * e.tiles;
+    i.jobs = e.tiles;
+  }
+  return i;
+}
+
+// Key tiles [t0, t1) of an item that lie in the jobs [begin, end), and whether
+// they are its slot 1 (the item starts behind the share's first job) or 0 of
+// the share's two places for partial results.
+__device__ __forceinline__ void tree_part(const TreeItem& i, int tiles, int begin, int end, int& t0, int& t1, int& slot) {
+  const int lo = max(begin, i.first) - i.first, hi = min(end, i.first + i.jobs) - i.first;
+  t0 = i.pair ? lo >> 1 : lo;
+  t1 = hi == i.jobs ? tiles : (i.pair ? hi >> 1 : hi);
+  slot = i.first > begin ? 1 : 0;
+}
+
+struct TreeRun {           // a part of an item that a CTA works on
+  int b, unit, row0, t0, t1, slot;
+  bool pair;
+  TreeElement e;
+  __device__ __forceinline__ int jobs() const { return (t1 - t0) * (pair ? 2 : 1); }
+};
+
+template <int KEYS, bool PAIRS>
+struct TreeWalker {
+  int begin, end, x, b, base;
+  __device__ __forceinline__ explicit TreeWalker(const TreeStart& s)
+      : begin(s.begin), end(s.end), x(s.begin), b(s.b), base(s.base) {}
+  __device__ __forceinline__ bool next(const TreeParams& p, TreeRun& r) {
+    while (x < end) {
+      r.e = tree_element<KEYS>(p, b, false);
+      const int jobs = tree_jobs(p, r.e);
+      if (x >= base + jobs) {
+        base += jobs;
+        ++b;
+        continue;
+      }
+      const TreeItem i = tree_item<PAIRS>(p, r.e, b, base, x);
+      tree_part(i, r.e.tiles, begin, end, r.t0, r.t1, r.slot);
+      r.b = b;
+      r.unit = i.unit;
+      r.row0 = i.row0;
+      r.pair = i.pair;
+      x = min(end, i.first + i.jobs);
+      if (r.t0 < r.t1) return true;
+    }
+    return false;
+  }
+};
+
+}  // namespace spk
