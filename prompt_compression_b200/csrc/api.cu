@@ -856,7 +856,6 @@ spk_status tree_attention(const spk_tree_shape* s, const void* q, const void* k_
   p.box_rows = box_rows_of(s->page_rows, plan.keys);
   p.c2 = s->scale * 1.4426950408889634f;
   p.ctas = plan.ctas;
-  p.min_share = 1;
   p.part_o = static_cast<float*>(ws);
   p.part_ml = p.part_o + static_cast<size_t>(plan.ctas) * 2 * plan.item_rows * s->head_dim;
   const bool fp16 = s->dtype == SPK_FP16;

@@ -68,7 +68,6 @@ struct TreeParams {
   int box_rows;            // rows of one page copy: divides page_rows and the key tile
   float c2;                // scale * log2(e)
   int ctas;                // CTAs of the main kernel
-  int min_share;           // jobs a CTA takes at least
   float* part_o;           // [ctas * 2][rows of an item][d] partial outputs
   float* part_ml;          // [ctas * 2][rows of an item][2] their row maxima and sums
 };

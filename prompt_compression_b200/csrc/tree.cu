@@ -394,19 +394,20 @@ __global__ void __launch_bounds__(kThreads, 2)
             dst[x] = *reinterpret_cast<const uint4*>(q_p + row * (D * 2) + ((ch ^ (row & 7)) << 4));
         }
       } else {
-        const size_t part = (static_cast<size_t>(blockIdx.x) * 2 + run.slot) * C::kRows;
+        const size_t part = static_cast<size_t>(blockIdx.x) * 2 + run.slot;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const size_t row = part + 8 * n + 2 * gc + c;
+            const int row = 8 * n + 2 * gc + c;
 #pragma unroll
             for (int j = 0; j < MT; ++j) {
-              const int d = warp * DW + 16 * j + gr;
-              p.part_o[row * D + d] = o[j][n][c];
-              p.part_o[row * D + d + 8] = o[j][n][2 + c];
+              const int d = warp * DW + 16 * j + gr;           // [4 columns][row], as the join reads it
+              p.part_o[((part * (D / 4) + d / 4) * C::kRows + row) * 4 + d % 4] = o[j][n][c];
+              p.part_o[((part * (D / 4) + d / 4 + 2) * C::kRows + row) * 4 + d % 4] = o[j][n][2 + c];
             }
-            if (warp == 0 && gr == 0) *reinterpret_cast<float2*>(p.part_ml + row * 2) = make_float2(m[n][c], l[n][c]);
+            if (warp == 0 && gr == 0)
+              *reinterpret_cast<float2*>(p.part_ml + (part * C::kRows + row) * 2) = make_float2(m[n][c], l[n][c]);
           }
         }
       }
@@ -420,23 +421,28 @@ __global__ void __launch_bounds__(kThreads, 2)
 // --------------------------------------------------------------------------
 // A row's shares are added in their order:
 //   M = max m_c,  out = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c.
-// A block has one item and MANY ? one row of it (eight warps, each every
-// eighth share) : 32 rows (a warp takes four, one after the other).
+// A block has eight rows of one item; a thread has four columns of a row, and
+// adds them over the shares, four shares' loads in flight together.  MANY (an
+// item has many shares): four groups of such threads, each with every fourth
+// share, joined through shared memory in the groups' order.
 // by_border: the item that the border between shares c and c + 1 cuts, if this
 // is the first border inside it; otherwise item c of the call.  The blocks
 // start while the main kernel still runs and find their item (the line does
 // not depend on it), and wait before they read; every block waits, so the
 // join ends after the main kernel.
-constexpr int kJoinWarps = 8;
-constexpr int kJoinRows = 32;                   // rows of a block (not MANY)
+constexpr int kJoinRows = 8;
+constexpr int kJoinGroups = 4;                  // MANY
 
 template <typename T, int D, int KEYS, bool PAIRS, bool MANY>
-__global__ void __launch_bounds__(kJoinWarps * 32)
+__global__ void __launch_bounds__(kJoinRows * (D / 4) * (MANY ? kJoinGroups : 1))
     tree_join_kernel(const __grid_constant__ TreeParams p, int item_rows, bool by_border) {
-  constexpr int V = D / 32;                     // columns a lane
-  constexpr int W = MANY ? kJoinWarps : 1;      // warps a row
-  __shared__ float acc_s[MANY ? kJoinWarps : 1][D], l_s[kJoinWarps], m_s[kJoinWarps];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kGroup = kJoinRows * (D / 4);   // threads that hold eight rows
+  constexpr int G = MANY ? kJoinGroups : 1;
+  __shared__ float4 acc_s[MANY ? kGroup * (G - 1) : 1];
+  __shared__ float2 ml_s[MANY ? kGroup * (G - 1) : 1];
+  const int lane = threadIdx.x & 31;
+  const int group = threadIdx.x / kGroup, me = threadIdx.x % kGroup;
+  const int col4 = me / kJoinRows;
   TreeStart s = tree_start<KEYS>(p, by_border ? blockIdx.x + 1 : 0, false);
   int x = s.begin;
   if (!by_border) {                             // every unit has the same number of items
@@ -448,96 +454,70 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
     s.base = before;
-    const int tiles = tree_element<KEYS>(p, s.b, false).tiles;
-    x = tiles == 0 ? s.total : before + (unit - s.b * of_b) * tiles * p.row_tiles + k * tiles * (PAIRS ? 2 : 1);
+    s.e = tree_element<KEYS>(p, s.b, false);
+    x = s.e.tiles == 0 ? s.total : before + (unit - s.b * of_b) * s.e.tiles * p.row_tiles + k * s.e.tiles * (PAIRS ? 2 : 1);
   }
-  TreeElement e{};
   TreeItem item{};
   int c0 = 0, c1 = 0;
   if (x < s.total) {
-    e = tree_element<KEYS>(p, s.b, false);
-    item = tree_item<PAIRS>(p, e, s.b, s.base, x);
+    item = tree_item<PAIRS>(p, s.e, s.b, s.base, x);
     c0 = item.first / s.share;
     c1 = (item.first + item.jobs - 1) / s.share;
     if (by_border && (item.first == x || c0 != static_cast<int>(blockIdx.x))) c1 = c0;
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (c0 == c1) return;                         // no item, or one share has it
-  const int rows_here = min(PAIRS ? (item.pair ? 256 : 128) : item_rows, p.rows - item.row0);
-  const int row_end = MANY ? blockIdx.y + 1 : min(rows_here, static_cast<int>(blockIdx.y + 1) * kJoinRows);
-  for (int row = MANY ? blockIdx.y : blockIdx.y * kJoinRows + warp; row < row_end; row += kJoinWarps) {
-    const int r = item.row0 + row;              // in the unit
-    if (row >= rows_here || r % p.T >= e.live) {
-      if (MANY) return;                         // the whole block
-      continue;
-    }
-    float m = -INFINITY, l = 0.f, acc[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] = 0.f;
-    // four shares at a time: their loads are in flight together
-    for (int i0 = c0 + (MANY ? warp : 0); i0 <= c1; i0 += 4 * W) {
+  const int row = blockIdx.y * kJoinRows + me % kJoinRows;   // in the item
+  const int r = item.row0 + row;                             // in the unit
+  const bool on = row < (PAIRS ? (item.pair ? 256 : 128) : item_rows) && r < p.rows && r % p.T < s.e.live;
+  float m = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](float2 ml, float4 o) {
+    const float M = fmaxf(m, ml.x), ref = M == -INFINITY ? 0.f : M;
+    const float a = ex2_approx(m - ref), f = ex2_approx(ml.x - ref);
+    l = fmaf(l, a, ml.y * f);
+    acc.x = fmaf(acc.x, a, o.x * f);
+    acc.y = fmaf(acc.y, a, o.y * f);
+    acc.z = fmaf(acc.z, a, o.z * f);
+    acc.w = fmaf(acc.w, a, o.w * f);
+    m = M;
+  };
+  if (on) {
+    for (int i0 = c0 + group; i0 <= c1; i0 += 4 * G) {
       float2 ml[4];
-      float o[4][V];
+      float4 o[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const int i = i0 + u * W;
+        const int i = i0 + u * G;
         int t0 = 0, t1 = 0, slot = 0;
-        if (i <= c1) tree_part(item, e.tiles, i * s.share, (i + 1) * s.share, t0, t1, slot);
+        if (i <= c1) tree_part(item, s.e.tiles, i * s.share, (i + 1) * s.share, t0, t1, slot);
         ml[u] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-        for (int v = 0; v < V; ++v) o[u][v] = 0.f;
+        o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (t0 < t1) {
-          const size_t at = (static_cast<size_t>(i) * 2 + slot) * item_rows + row;
-          ml[u] = __ldcs(reinterpret_cast<const float2*>(p.part_ml + at * 2));
-#pragma unroll
-          for (int v = 0; v < V; v += 2) {
-            const float2 y = __ldcs(reinterpret_cast<const float2*>(p.part_o + at * D + lane * V + v));
-            o[u][v] = y.x;
-            o[u][v + 1] = y.y;
-          }
+          const size_t part = static_cast<size_t>(i) * 2 + slot;
+          ml[u] = __ldcs(reinterpret_cast<const float2*>(p.part_ml) + part * item_rows + row);
+          o[u] = __ldcs(reinterpret_cast<const float4*>(p.part_o) + (part * (D / 4) + col4) * item_rows + row);
         }
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float M = fmaxf(m, ml[u].x), ref = M == -INFINITY ? 0.f : M;
-        const float a = ex2_approx(m - ref), f = ex2_approx(ml[u].x - ref);
-        l = fmaf(l, a, ml[u].y * f);
-#pragma unroll
-        for (int v = 0; v < V; ++v) acc[v] = fmaf(acc[v], a, o[u][v] * f);
-        m = M;
-      }
+      for (int u = 0; u < 4; ++u) add(ml[u], o[u]);
     }
-    if (MANY) {                                 // the row's warps, in their order
-#pragma unroll
-      for (int v = 0; v < V; ++v) acc_s[MANY ? warp : 0][lane * V + v] = acc[v];
-      if (lane == 0) {
-        m_s[warp] = m;
-        l_s[warp] = l;
-      }
-      __syncthreads();
-      if (warp != 0) return;
-      float M = m;
-      for (int w = 1; w < kJoinWarps; ++w) M = fmaxf(M, m_s[w]);
-      const float ref = M == -INFINITY ? 0.f : M;
-      const float a = ex2_approx(m - ref);
-      l *= a;
-#pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] *= a;
-      for (int w = 1; w < kJoinWarps; ++w) {
-        const float f = ex2_approx(m_s[w] - ref);
-        l = fmaf(l_s[w], f, l);
-#pragma unroll
-        for (int v = 0; v < V; ++v) acc[v] = fmaf(acc_s[MANY ? w : 0][lane * V + v], f, acc[v]);
-      }
-      m = M;
-    }
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out) + (static_cast<size_t>(item.unit) * p.rows + r) * (D / 2) + lane * (V / 2);
-#pragma unroll
-    for (int v = 0; v < V; v += 2) dst[v / 2] = Half16<T>::pack(acc[v] * inv, acc[v + 1] * inv);
-    if (lane == 0 && p.lse2 != nullptr)
-      p.lse2[static_cast<size_t>(item.unit) * p.rows + r] = l == 0.f ? -INFINITY : m + lg2_approx(l);
   }
+  if (MANY) {
+    if (group > 0) {
+      acc_s[MANY ? (group - 1) * kGroup + me : 0] = acc;
+      ml_s[MANY ? (group - 1) * kGroup + me : 0] = make_float2(m, l);
+    }
+    __syncthreads();
+    if (group > 0) return;
+    for (int g = 0; g < G - 1; ++g) add(ml_s[MANY ? g * kGroup + me : 0], acc_s[MANY ? g * kGroup + me : 0]);
+  }
+  if (!on) return;
+  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+  const size_t at = static_cast<size_t>(item.unit) * p.rows + r;
+  reinterpret_cast<uint2*>(p.out)[at * (D / 4) + col4] =
+      make_uint2(Half16<T>::pack(acc.x * inv, acc.y * inv), Half16<T>::pack(acc.z * inv, acc.w * inv));
+  if (col4 == 0 && p.lse2 != nullptr) p.lse2[at] = l == 0.f ? -INFINITY : m + lg2_approx(l);
 }
 
 template <typename T, int D, int KEYS, bool PAIRS>
@@ -546,10 +526,10 @@ cudaError_t launch_join(const TreeParams& p, const TreePlan& plan, cudaStream_t 
   const long long items = static_cast<long long>(p.batch) * p.layers * p.hkv * plan.items;
   const bool by_border = items > plan.ctas - 1;
   const int rows = p.rows < plan.item_rows ? p.rows : plan.item_rows;
-  const bool many = items * 4 <= plan.ctas;     // many shares an item: eight warps a row
+  const bool many = items * 4 <= plan.ctas;     // many shares an item
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(by_border ? plan.ctas - 1 : static_cast<unsigned>(items), many ? rows : (rows + kJoinRows - 1) / kJoinRows);
-  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.gridDim = dim3(by_border ? plan.ctas - 1 : static_cast<unsigned>(items), (rows + kJoinRows - 1) / kJoinRows);
+  cfg.blockDim = dim3(kJoinRows * (D / 4) * (many ? kJoinGroups : 1));
   cfg.stream = stream;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -19,6 +19,8 @@
 
 namespace spk {
 
+constexpr int kJoinJobs = 6;   // what joining partial results costs, in jobs (about 5 us against 0.8 us a job)
+
 struct TreeElement {       // a batch element
   int seq, len, live, tiles;
 };
@@ -68,6 +70,7 @@ struct TreeStart {
   int total, share;
   int begin, end;          // the CTA's jobs
   int b, base;             // the batch element that holds `begin`, and the jobs before it
+  TreeElement e;           // that element
 };
 
 // The share of CTA `cta`, by the calling warp (every lane gets it).
@@ -75,22 +78,33 @@ template <int KEYS>
 __device__ __forceinline__ TreeStart tree_start(const TreeParams& p, int cta, bool record) {
   const int lane = threadIdx.x & 31;
   TreeStart s;
-  int jobs = lane < p.batch ? tree_jobs(p, tree_element<KEYS>(p, lane, record)) : 0;
-  const int first32 = jobs;
+  TreeElement first = {0, 0, 0, 0};
+  if (lane < p.batch) first = tree_element<KEYS>(p, lane, record);
+  int jobs = tree_jobs(p, first);
   for (int b = lane + 32; b < p.batch; b += 32) jobs += tree_jobs(p, tree_element<KEYS>(p, b, record));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) jobs += __shfl_xor_sync(0xffffffffu, jobs, o);
   s.total = jobs;
-  const int even = (s.total + p.ctas - 1) / p.ctas;
-  s.share = even > p.min_share ? even : p.min_share;
+  s.share = max(1, (s.total + p.ctas - 1) / p.ctas);
+  // whole units where that costs few jobs more: no unit is then cut and joined
+  const int unit = p.row_tiles * __shfl_sync(0xffffffffu, first.tiles, 0);
+  bool same = unit > 0;
+  for (int b = lane; b < p.batch; b += 32) same = same && (b < 32 ? first : tree_element<KEYS>(p, b, false)).tiles * p.row_tiles == unit;
+  if (__all_sync(0xffffffffu, same)) {
+    const int whole = (s.share + unit - 1) / unit * unit;
+    if (whole - s.share <= kJoinJobs) s.share = whole;
+  }
   const long long begin = static_cast<long long>(s.share) * cta;
   s.begin = begin < s.total ? static_cast<int>(begin) : s.total;
   s.end = s.begin + min(s.total - s.begin, s.share);
   s.b = 0;
   s.base = 0;
+  s.e = {0, 0, 0, 0};
   for (int b0 = 0; b0 < p.batch; b0 += 32) {
     const int b = b0 + lane;
-    const int x = b0 == 0 ? first32 : (b < p.batch ? tree_jobs(p, tree_element<KEYS>(p, b, false)) : 0);
+    TreeElement e = {0, 0, 0, 0};
+    if (b0 == 0) e = first; else if (b < p.batch) e = tree_element<KEYS>(p, b, false);
+    const int x = tree_jobs(p, e);
     int sum = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -103,6 +117,10 @@ __device__ __forceinline__ TreeStart tree_start(const TreeParams& p, int cta, bo
       const int at = __ffs(in) - 1;
       s.b = b0 + at;
       s.base = __shfl_sync(0xffffffffu, base, at);
+      s.e.seq = __shfl_sync(0xffffffffu, e.seq, at);
+      s.e.len = __shfl_sync(0xffffffffu, e.len, at);
+      s.e.live = __shfl_sync(0xffffffffu, e.live, at);
+      s.e.tiles = __shfl_sync(0xffffffffu, e.tiles, at);
       return s;
     }
     s.base += __shfl_sync(0xffffffffu, sum, 31);
@@ -162,23 +180,24 @@ struct TreeRun {           // a part of an item that a CTA works on
 template <int KEYS, bool PAIRS>
 struct TreeWalker {
   int begin, end, x, b, base;
+  TreeElement e;
   __device__ __forceinline__ explicit TreeWalker(const TreeStart& s)
-      : begin(s.begin), end(s.end), x(s.begin), b(s.b), base(s.base) {}
+      : begin(s.begin), end(s.end), x(s.begin), b(s.b), base(s.base), e(s.e) {}
   __device__ __forceinline__ bool next(const TreeParams& p, TreeRun& r) {
     while (x < end) {
-      r.e = tree_element<KEYS>(p, b, false);
-      const int jobs = tree_jobs(p, r.e);
-      if (x >= base + jobs) {
+      int jobs = tree_jobs(p, e);
+      while (x >= base + jobs) {
         base += jobs;
-        ++b;
-        continue;
+        e = tree_element<KEYS>(p, ++b, false);
+        jobs = tree_jobs(p, e);
       }
-      const TreeItem i = tree_item<PAIRS>(p, r.e, b, base, x);
-      tree_part(i, r.e.tiles, begin, end, r.t0, r.t1, r.slot);
+      const TreeItem i = tree_item<PAIRS>(p, e, b, base, x);
+      tree_part(i, e.tiles, begin, end, r.t0, r.t1, r.slot);
       r.b = b;
       r.unit = i.unit;
       r.row0 = i.row0;
       r.pair = i.pair;
+      r.e = e;
       x = min(end, i.first + i.jobs);
       if (r.t0 < r.t1) return true;
     }
