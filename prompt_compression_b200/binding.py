@@ -10,6 +10,7 @@ only when none is given, and then on the stream the kernels run on.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -481,20 +482,22 @@ def vs_sparse_attention(q, k, v, vertical, slash, out=None, lse2=None, workspace
 
 # --------------------------------------------------------------------- paged cache, tree attention
 # These entry points launch on the device of their tensors, whichever device
-# is current, and refuse tensors of several devices.
-def _cuda_device(t: torch.Tensor, name: str) -> torch.device:
+# is current, and refuse tensors of several devices.  They are called once a
+# layer or a step, so the checks are kept short: a tensor costs about 0.3 us.
+def _device_index(t: torch.Tensor, name: str) -> int:
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
+    return t.get_device()
 
 
-def _ptr(t: Optional[torch.Tensor], name: str, dtype, dev, numel: Optional[int] = None) -> Optional[int]:
-    """Data pointer of a contiguous tensor of `dtype` (None: any) on `dev`; None for None."""
+def _ptr(t: Optional[torch.Tensor], name: str, dtype, index: int, numel: Optional[int] = None) -> Optional[int]:
+    """Data pointer of a contiguous tensor of `dtype` (None: any) on CUDA device
+    `index`; None for None."""
     if t is None:
         return None
-    if t.device != dev:
-        raise ValueError(f"{name} must be a CUDA tensor on {dev}, got one on {t.device}")
-    if dtype is not None and t.dtype != dtype:
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be a CUDA tensor on cuda:{index}, got one on {t.device}")
+    if t.dtype is not dtype and dtype is not None:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -503,20 +506,34 @@ def _ptr(t: Optional[torch.Tensor], name: str, dtype, dev, numel: Optional[int] 
     return t.data_ptr()
 
 
-def _launch(dev, stream, fn, *args):
-    """fn(*args, stream) with `dev` current."""
-    if isinstance(stream, torch.cuda.Stream) and stream.device != dev:
-        raise ValueError(f"the stream is one of {stream.device}, the tensors are on {dev}")
-    if torch.cuda.current_device() == dev.index:
-        _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)))
+# torch.cuda.current_stream() builds a Python object (3 us); this returns the handle
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _launch(index: int, stream, fn, *args):
+    """fn(*args, stream) with CUDA device `index` current."""
+    if stream is None:
+        handle = _raw_stream(index)
+    elif isinstance(stream, torch.cuda.Stream):
+        if stream.device.index != index:
+            raise ValueError(f"the stream is one of {stream.device}, the tensors are on cuda:{index}")
+        handle = stream.cuda_stream
     else:
-        with torch.cuda.device(dev):
-            _check(fn(*args, _stream(stream)))
+        handle = int(stream)
+    if torch.cuda.current_device() == index:
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, handle)
+    if status != SPK_OK:
+        _check(status)
 
 
-def _new(shape, dtype, dev, stream) -> torch.Tensor:
+def _new(shape, dtype, index: int, stream) -> torch.Tensor:
     """An output of a call on `stream`: allocated there, and known to the
     caller's stream too, so that its memory is not given away while either uses it."""
+    dev = torch.device("cuda", index)
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=dev)
     with torch.cuda.stream(_stream_object(stream, dev)):
@@ -525,12 +542,14 @@ def _new(shape, dtype, dev, stream) -> torch.Tensor:
     return t
 
 
-def _scratch(ws: Optional[torch.Tensor], nbytes: int, dev, stream) -> torch.Tensor:
+def _scratch(ws: Optional[torch.Tensor], nbytes: int, index: int, stream) -> torch.Tensor:
     """The caller's workspace, or a temporary one on the launch stream."""
-    if ws is None:
-        ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev) if stream is None else \
-            _workspace(None, nbytes, dev, stream)
-    return ws
+    if ws is not None:
+        return ws
+    dev = torch.device("cuda", index)
+    if stream is None:
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+    return _workspace(None, nbytes, dev, stream)
 
 
 def pages_shape(k_pages, v_pages, page_refs, page_table, seq_lens) -> PagesShape:
@@ -576,7 +595,7 @@ def kv_pages_reserve(k_pages, v_pages, page_refs, page_table, seq_lens, seqs, n_
     sequences hold too.  Returns result int32 [1] (on the device): 0 done, > 0
     that many pages were missing, -1 a wrong argument; nothing changed unless 0."""
     lib = load_library()
-    dev = _cuda_device(k_pages, "k_pages")
+    dev = _device_index(k_pages, "k_pages")
     shape = pages_shape(k_pages, v_pages, page_refs, page_table, seq_lens)
     n = seqs.numel()
     result, res = _result(result, dev, stream)
@@ -594,7 +613,7 @@ def kv_pages_write(k, v, k_pages, v_pages, page_refs, page_table, seq_lens, seqs
     the rows idx int32 [n * L * Hkv / units_per_idx, n_idx] selects (None: all),
     of which the first counts int32 [n] are written (None: all)."""
     lib = load_library()
-    dev = _cuda_device(k_pages, "k_pages")
+    dev = _device_index(k_pages, "k_pages")
     shape = pages_shape(k_pages, v_pages, page_refs, page_table, seq_lens)
     n = seqs.numel()
     if k.dim() != 5 or k.shape != v.shape or tuple(k.shape[:3]) != (n, shape.layers, shape.hkv) \
@@ -619,7 +638,7 @@ def kv_pages_compact(k_pages, v_pages, page_refs, page_table, seq_lens, src, dst
     units_per_idx, n_idx] of sequences src int32 [n], in pages of their own
     (dst = src: in place).  Returns result as kv_pages_reserve does."""
     lib = load_library()
-    dev = _cuda_device(k_pages, "k_pages")
+    dev = _device_index(k_pages, "k_pages")
     shape = pages_shape(k_pages, v_pages, page_refs, page_table, seq_lens)
     n, n_idx = src.numel(), idx.shape[-1]
     units = n * shape.layers * shape.hkv
@@ -641,7 +660,7 @@ def kv_pages_fork(page_refs, page_table, seq_lens, src, dst, page_rows: int, n_r
     the call (their first n_rows int32 [n] rows where given), by holding their
     pages.  Returns result as kv_pages_reserve does."""
     lib = load_library()
-    dev = _cuda_device(page_table, "page_table")
+    dev = _device_index(page_table, "page_table")
     shape = _table_shape(page_refs, page_table, seq_lens, page_rows)
     n = src.numel()
     result, res = _result(result, dev, stream)
@@ -657,7 +676,7 @@ def kv_pages_free(page_refs, page_table, seq_lens, seqs, page_rows: int, keep_ro
     """Sequences seqs int32 [n] keep their first keep_rows int32 [n] rows (None:
     none); the pages behind them are released."""
     lib = load_library()
-    dev = _cuda_device(page_table, "page_table")
+    dev = _device_index(page_table, "page_table")
     shape = _table_shape(page_refs, page_table, seq_lens, page_rows)
     n = seqs.numel()
     _launch(dev, stream, lib.kv_pages_free, ctypes.byref(shape), *_book(page_refs, page_table, seq_lens, dev),
@@ -666,6 +685,9 @@ def kv_pages_free(page_refs, page_table, seq_lens, seqs, page_rows: int, keep_ro
 
 SPK_BF16, SPK_FP16 = 0, 1
 _TREE_DTYPES = {torch.bfloat16: SPK_BF16, torch.float16: SPK_FP16}
+
+
+_NO_CONTEXT = contextlib.nullcontext()
 
 
 def tree_shape(q, k_pages, page_table, scale: float = 1.0) -> TreeShape:
@@ -694,7 +716,7 @@ def tree_attention(q, k_pages, v_pages, page_table, seq_lens, k_tree=None, v_tre
     many of the tokens count (None: T).  Returns out [B, L, Hq, T, d]; fills
     lse2 fp32 [B, L, Hq, T] when given."""
     lib = load_library()
-    dev = _cuda_device(q, "q")
+    dev = _device_index(q, "q")
     shape = tree_shape(q, k_pages, page_table, scale)
     Bsz, L, hq, T, d = q.shape
     if v_pages.shape != k_pages.shape:
@@ -708,12 +730,10 @@ def tree_attention(q, k_pages, v_pages, page_table, seq_lens, k_tree=None, v_tre
     if out is None:
         out = _new(q.shape, q.dtype, dev, stream)
     i32 = torch.int32
-    if torch.cuda.current_device() == dev.index:
-        need = tree_attention_workspace_size(shape)
-    else:
-        with torch.cuda.device(dev):
-            need = tree_attention_workspace_size(shape)
-    ws = _scratch(workspace, need, dev, stream)
+    ws = workspace
+    if ws is None:
+        with torch.cuda.device(dev) if torch.cuda.current_device() != dev else _NO_CONTEXT:
+            ws = _scratch(None, tree_attention_workspace_size(shape), dev, stream)
     _launch(dev, stream, lib.tree_attention, ctypes.byref(shape), _ptr(q, "q", None, dev),
             _ptr(k_pages, "k_pages", q.dtype, dev), _ptr(v_pages, "v_pages", q.dtype, dev),
             _ptr(page_table, "page_table", i32, dev), _ptr(seq_lens, "seq_lens", i32, dev, shape.n_seqs),
@@ -731,7 +751,7 @@ def tree_mask(parents, n_live=None, mask=None, depth=None, stream=None):
     lib = load_library()
     if parents.dim() != 2:
         raise ValueError("parents is [B, T]")
-    dev = _cuda_device(parents, "parents")
+    dev = _device_index(parents, "parents")
     Bsz, T = parents.shape
     words = (T + 31) // 32
     if mask is None:

@@ -4,6 +4,7 @@
 // tensor maps, picks the persistent grid and enqueues the kernels on the
 // caller's stream.  No allocation, no host synchronisation on the compute
 // paths.
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -48,9 +49,12 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 int num_sms() {
+  static std::atomic<int> known[64] = {};      // by device: an attribute does not change
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+  if (dev >= 0 && dev < 64 && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) return 148;
+  if (dev >= 0 && dev < 64) known[dev].store(sms, std::memory_order_relaxed);
   return sms;
 }
 
@@ -783,7 +787,7 @@ static spk_status check_tree(const spk_tree_shape* s) {
   const long long rows = static_cast<long long>(s->hq / s->hkv) * s->n_nodes;
   const long long most = static_cast<long long>(s->max_pages) * s->page_rows;
   const long long units = static_cast<long long>(s->layers) * s->hkv;      // of a batch element
-  if (most > 0x7fffffffLL || rows > 0x7fffffffLL / 2 || units > 0x7fffffffLL / s->batch ||
+  if (most > 0x3fffffffLL || rows > 0x7fffffffLL / 2 || units > 0x7fffffffLL / s->batch ||
       static_cast<long long>(s->n_pages) > 0x7fffffffLL / units)
     return fail(SPK_ERR_UNSUPPORTED, "too many units, rows or pages");
   // jobs of all units: 32-bit on the device
@@ -851,9 +855,11 @@ spk_status tree_attention(const spk_tree_shape* s, const void* q, const void* k_
   p.rows = g * s->n_nodes;
   p.tile_rows = plan.tile_rows;
   p.row_tiles = plan.row_tiles;
+  p.item_rows = plan.item_rows;
   p.has_tree = k_tree != nullptr;
   p.n_seqs = s->n_seqs; p.max_pages = s->max_pages; p.n_pages = s->n_pages; p.page_rows = s->page_rows;
   p.box_rows = box_rows_of(s->page_rows, plan.keys);
+  p.node_rows = s->n_nodes >= plan.keys ? plan.keys : (s->n_nodes + 7) / 8 * 8;
   p.c2 = s->scale * 1.4426950408889634f;
   p.ctas = plan.ctas;
   p.part_o = static_cast<float*>(ws);
@@ -861,16 +867,18 @@ spk_status tree_attention(const spk_tree_shape* s, const void* q, const void* k_
   const bool fp16 = s->dtype == SPK_FP16;
   const long long pool = static_cast<long long>(s->layers) * s->n_pages * s->hkv;
   const long long units = static_cast<long long>(s->batch) * s->layers * s->hkv;
-  CUtensorMap maps[5];
+  CUtensorMap maps[7];
   st = make_map16(&maps[0], fp16, k_pages, s->head_dim, s->page_rows, pool, p.box_rows);
   if (st == SPK_OK) st = make_map16(&maps[1], fp16, v_pages, s->head_dim, s->page_rows, pool, p.box_rows);
   if (st == SPK_OK && k_tree != nullptr) {
-    st = make_map16(&maps[2], fp16, k_tree, s->head_dim, s->n_nodes, units, plan.keys);
-    if (st == SPK_OK) st = make_map16(&maps[3], fp16, v_tree, s->head_dim, s->n_nodes, units, plan.keys);
+    st = make_map16(&maps[2], fp16, k_tree, s->head_dim, s->n_nodes, units, p.node_rows);
+    if (st == SPK_OK) st = make_map16(&maps[3], fp16, v_tree, s->head_dim, s->n_nodes, units, p.node_rows);
   } else {
     maps[2] = maps[0];
     maps[3] = maps[1];
   }
+  if (st == SPK_OK) st = make_map16(&maps[5], fp16, k_pages, s->head_dim, s->page_rows, pool, 8);
+  if (st == SPK_OK) st = make_map16(&maps[6], fp16, v_pages, s->head_dim, s->page_rows, pool, 8);
   if (st == SPK_OK && plan.wide) st = make_map16(&maps[4], fp16, q, s->head_dim, p.rows, units, 128);
   if (st != SPK_OK) return st;
   cudaError_t e = launch_tree_attention(fp16, s->head_dim, maps, p, plan, static_cast<cudaStream_t>(stream));

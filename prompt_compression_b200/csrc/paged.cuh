@@ -63,9 +63,11 @@ struct TreeParams {
   int rows;                // query rows per unit = g * T, ordered [query head][node]
   int tile_rows;           // query rows of a row tile (wide kernel: 128)
   int row_tiles;           // row tiles per unit
+  int item_rows;           // rows of an item, in the partial results
   int has_tree;            // k_tree and v_tree are given
   int n_seqs, max_pages, n_pages, page_rows;
   int box_rows;            // rows of one page copy: divides page_rows and the key tile
+  int node_rows;           // rows of one copy of nodes: min(T, key tile), a multiple of 8
   float c2;                // scale * log2(e)
   int ctas;                // CTAs of the main kernel
   float* part_o;           // [ctas * 2][rows of an item][d] partial outputs
@@ -78,17 +80,18 @@ struct TreePlan {
   int tile_rows, row_tiles;
   int item_rows;           // query rows of an item
   int items;               // items per unit
-  int ctas;
+  int sms, ctas;
 };
 TreePlan tree_plan(int rows, int head_dim, int sms);
 size_t tree_ws_bytes(const TreePlan& plan, int head_dim);
 
 // maps: k_pages, v_pages [layers * n_pages * hkv][page_rows][d] in boxes of
 // box_rows x 64; k_tree, v_tree [batch * layers * hkv][T][d] in boxes of
-// plan.keys x 64; q [batch * layers * hkv][rows][d] in boxes of 128 x 64 (wide only)
-cudaError_t launch_tree_attention(bool fp16, int head_dim, const CUtensorMap (&maps)[5], const TreeParams& p,
+// node_rows x 64; q [batch * layers * hkv][rows][d] in boxes of 128 x 64 (wide only);
+// k_pages, v_pages in boxes of 8 x 64
+cudaError_t launch_tree_attention(bool fp16, int head_dim, const CUtensorMap (&maps)[7], const TreeParams& p,
                                   const TreePlan& plan, cudaStream_t stream);
-cudaError_t launch_tree_umma(bool fp16, int head_dim, const CUtensorMap (&maps)[5], const TreeParams& p,
+cudaError_t launch_tree_umma(bool fp16, int head_dim, const CUtensorMap (&maps)[7], const TreeParams& p,
                              cudaStream_t stream);
 cudaError_t launch_tree_mask(const int* parents, const int* n_live, int batch, int T, uint32_t* mask, int* depth,
                              cudaStream_t stream);

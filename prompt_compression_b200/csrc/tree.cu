@@ -64,6 +64,7 @@ template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kThreads, 2)
     tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                 const __grid_constant__ CUtensorMap ktmap, const __grid_constant__ CUtensorMap vtmap,
+                const __grid_constant__ CUtensorMap k8map, const __grid_constant__ CUtensorMap v8map,
                 const __grid_constant__ TreeParams p) {
   using C = TreeCfg<D, NT>;
   constexpr int KS = D / 16;              // k-steps of the logits
@@ -112,52 +113,53 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int s = 0; s < C::kStages; ++s) last[s] = -1;
     while (ok && walk.next(p, run)) {
       const int* row = p.table + static_cast<size_t>(run.e.seq) * p.max_pages;
-      const int lh = run.unit - run.b * p.layers * p.hkv;
-      const int layer = lh / p.hkv, head = lh - layer * p.hkv;
       for (int t = run.t0; t < run.t1; ++t, ++count) {
         const TreeTile tile = tree_tile<kTreeKeys>(p, run.e, t);
         const int st = count % C::kStages;
         const uint32_t ph = (count / C::kStages) & 1;
-        // lane i: the page of box i of the tile
-        const int boxes = tile.cached ? (tile.n + p.box_rows - 1) / p.box_rows : 0;
+        // lane i: the page of box i of the tile's cached rows
+        // (a tile that ends early in parts of 8 rows: the nodes may lie right behind)
+        const int part_rows = tile.rows == kTreeKeys ? p.box_rows : 8, boxes = (tile.rows + part_rows - 1) / part_rows;
+        const CUtensorMap* const km = tile.rows == kTreeKeys ? &kmap : &k8map;
+        const CUtensorMap* const vm = tile.rows == kTreeKeys ? &vmap : &v8map;
         int unit = 0, in_page = 0;
         if (lane < boxes) {
-          const int t_row = tile.first + lane * p.box_rows;
+          const int t_row = tile.first + lane * part_rows;
           const int slot = t_row / p.page_rows;
           in_page = t_row - slot * p.page_rows;
-          int page = __ldg(row + slot);
+          const int page = __ldg(row + slot);
           if (page < 0 || page >= p.n_pages) {
             record_error(SPK_DEVERR_INDEX, run.b);
             unit = p.layers * p.n_pages * p.hkv;     // outside the map: the box reads as zeros
           } else {
-            unit = (layer * p.n_pages + page) * p.hkv + head;
+            unit = run.pool + page * p.hkv;
           }
         }
         ok = mbar_wait(&empty[st], ph ^ 1, abort_v, site(0));
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
+        const int bytes = (boxes * part_rows + (tile.nodes > 0 ? p.node_rows : 0)) * 128 * 2 * C::kAtoms;
         if (lane == 0) {
-          if (tile.cached)
-            mbar_arrive_expect_tx(&full[st], boxes * p.box_rows * 128 * 2 * C::kAtoms);
-          else if (tile.n > 0)
-            mbar_arrive_expect_tx(&full[st], C::kStageBytes);
+          if (bytes > 0)
+            mbar_arrive_expect_tx(&full[st], bytes);
           else
             mbar_arrive(&full[st]);
         }
         __syncwarp();
         uint8_t* const kp = smem + st * C::kStageBytes;
         if (lane < boxes) {
-          uint8_t* const dst = kp + lane * p.box_rows * 128;
+          uint8_t* const dst = kp + lane * part_rows * 128;
 #pragma unroll
           for (int a = 0; a < C::kAtoms; ++a) {
-            tma_load_3d(dst + a * C::kHalf, &kmap, &full[st], a * 64, in_page, unit);
-            tma_load_3d(dst + (C::kAtoms + a) * C::kHalf, &vmap, &full[st], a * 64, in_page, unit);
+            tma_load_3d(dst + a * C::kHalf, km, &full[st], a * 64, in_page, unit);
+            tma_load_3d(dst + (C::kAtoms + a) * C::kHalf, vm, &full[st], a * 64, in_page, unit);
           }
-        } else if (!tile.cached && tile.n > 0 && lane == 0) {
+        }
+        if (tile.nodes > 0 && lane == 0) {
 #pragma unroll
           for (int a = 0; a < C::kAtoms; ++a) {
-            tma_load_3d(kp + a * C::kHalf, &ktmap, &full[st], a * 64, tile.first, run.unit);
-            tma_load_3d(kp + (C::kAtoms + a) * C::kHalf, &vtmap, &full[st], a * 64, tile.first, run.unit);
+            tma_load_3d(kp + a * C::kHalf + tile.off * 128, &ktmap, &full[st], a * 64, tile.node0, run.unit);
+            tma_load_3d(kp + (C::kAtoms + a) * C::kHalf + tile.off * 128, &vtmap, &full[st], a * 64, tile.node0, run.unit);
           }
         }
 #pragma unroll
@@ -206,27 +208,17 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int key0 = warp * 16;
         // which of keys gr, gr + 8 each row sees
         uint32_t sees[NT][2];
-        if (tile.cached) {
-          const uint32_t bits = (key0 + gr < tile.n ? 1u : 0u) | (key0 + gr + 8 < tile.n ? 2u : 0u);
+        if (tile.rows == kTreeKeys) {
 #pragma unroll
-          for (int n = 0; n < NT; ++n) sees[n][0] = sees[n][1] = bits;
+          for (int n = 0; n < NT; ++n) sees[n][0] = sees[n][1] = 3u;
         } else {
-          const int node0 = tile.first + key0;
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               const int r = run.row0 + 8 * n + 2 * gc + c;
-              uint32_t w = 0;
-              if (r < p.rows && key0 < tile.n) {
-                const int i = r % p.T;
-                if (p.mask != nullptr)
-                  w = __ldg(p.mask + (static_cast<size_t>(run.b) * p.T + i) * p.words + (node0 >> 5)) >> (node0 & 31);
-                else
-                  w = i >= node0 ? (i - node0 >= 31 ? 0xffffffffu : (2u << (i - node0)) - 1u) : 0u;
-              }
-              sees[n][c] = ((w >> gr) & (key0 + gr < tile.n ? 1u : 0u)) |
-                           (((w >> (gr + 8)) & (key0 + gr + 8 < tile.n ? 1u : 0u)) << 1);
+              const uint32_t w = tree_word(p, run.b, tile, key0, r % p.T, r < p.rows);
+              sees[n][c] = ((w >> gr) & 1u) | (((w >> (gr + 8)) & 1u) << 1);
             }
           }
         }
@@ -301,14 +293,15 @@ __global__ void __launch_bounds__(kThreads, 2)
             o[j][n][3] *= alpha[1];
           }
         }
-        // V rows behind the tile's last key: whatever the slot holds (it may be
-        // NaN) must not meet the zeros of P, so the rest of the last k-step is cleared
+        // V rows without a key: whatever the slot holds (it may be NaN) must not meet
+        // the zeros of P, so they are cleared, up to the end of the last k-step
         const int steps = (tile.n + 15) / 16;
-        if (tile.n < steps * 16) {
+        const int gap = tile.nodes > 0 ? tile.off - tile.rows : 0, bad = gap + steps * 16 - tile.n;
+        if (bad > 0) {
           constexpr int kCh = DW / 8;            // this warp's 16-byte columns
-          const int bad = steps * 16 - tile.n;
           for (int x = lane; x < bad * kCh; x += 32) {
-            const int row = tile.n + x / kCh, ch = warp * kCh + x % kCh;
+            const int b = x / kCh, ch = warp * kCh + x % kCh;
+            const int row = b < gap ? tile.rows + b : tile.n + b - gap;
             uint8_t* at = smem + st * C::kStageBytes + C::kAtoms * C::kHalf + (ch >> 3) * C::kHalf + row * 128 +
                           (((ch & 7) ^ (row & 7)) << 4);
             *reinterpret_cast<uint4*>(at) = make_uint4(0u, 0u, 0u, 0u);
@@ -421,8 +414,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 // --------------------------------------------------------------------------
 // A row's shares are added in their order:
 //   M = max m_c,  out = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c.
-// A block has eight rows of one item; a thread has four columns of a row, and
-// adds them over the shares, four shares' loads in flight together.  MANY (an
+// A block has eight rows of one item at a time; a thread has four columns of a
+// row, and adds them over the shares, four shares' loads in flight together.  MANY (an
 // item has many shares): four groups of such threads, each with every fourth
 // share, joined through shared memory in the groups' order.
 // by_border: the item that the border between shares c and c + 1 cuts, if this
@@ -467,57 +460,61 @@ __global__ void __launch_bounds__(kJoinRows * (D / 4) * (MANY ? kJoinGroups : 1)
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (c0 == c1) return;                         // no item, or one share has it
-  const int row = blockIdx.y * kJoinRows + me % kJoinRows;   // in the item
-  const int r = item.row0 + row;                             // in the unit
-  const bool on = row < (PAIRS ? (item.pair ? 256 : 128) : item_rows) && r < p.rows && r % p.T < s.e.live;
-  float m = -INFINITY, l = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](float2 ml, float4 o) {
-    const float M = fmaxf(m, ml.x), ref = M == -INFINITY ? 0.f : M;
-    const float a = ex2_approx(m - ref), f = ex2_approx(ml.x - ref);
-    l = fmaf(l, a, ml.y * f);
-    acc.x = fmaf(acc.x, a, o.x * f);
-    acc.y = fmaf(acc.y, a, o.y * f);
-    acc.z = fmaf(acc.z, a, o.z * f);
-    acc.w = fmaf(acc.w, a, o.w * f);
-    m = M;
-  };
-  if (on) {
-    for (int i0 = c0 + group; i0 <= c1; i0 += 4 * G) {
-      float2 ml[4];
-      float4 o[4];
+  const int rows_here = min(PAIRS ? (item.pair ? 256 : 128) : item_rows, p.rows - item.row0);
+  for (int row0 = blockIdx.y * kJoinRows; row0 < rows_here; row0 += gridDim.y * kJoinRows) {
+    const int row = row0 + me % kJoinRows;                   // in the item
+    const int r = item.row0 + row;                           // in the unit
+    const bool on = row < rows_here && r % p.T < s.e.live;
+    float m = -INFINITY, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](float2 ml, float4 o) {
+      const float M = fmaxf(m, ml.x), ref = M == -INFINITY ? 0.f : M;
+      const float a = ex2_approx(m - ref), f = ex2_approx(ml.x - ref);
+      l = fmaf(l, a, ml.y * f);
+      acc.x = fmaf(acc.x, a, o.x * f);
+      acc.y = fmaf(acc.y, a, o.y * f);
+      acc.z = fmaf(acc.z, a, o.z * f);
+      acc.w = fmaf(acc.w, a, o.w * f);
+      m = M;
+    };
+    if (on) {
+      for (int i0 = c0 + group; i0 <= c1; i0 += 4 * G) {
+        float2 ml[4];
+        float4 o[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int i = i0 + u * G;
-        int t0 = 0, t1 = 0, slot = 0;
-        if (i <= c1) tree_part(item, s.e.tiles, i * s.share, (i + 1) * s.share, t0, t1, slot);
-        ml[u] = make_float2(-INFINITY, 0.f);
-        o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (t0 < t1) {
-          const size_t part = static_cast<size_t>(i) * 2 + slot;
-          ml[u] = __ldcs(reinterpret_cast<const float2*>(p.part_ml) + part * item_rows + row);
-          o[u] = __ldcs(reinterpret_cast<const float4*>(p.part_o) + (part * (D / 4) + col4) * item_rows + row);
+        for (int u = 0; u < 4; ++u) {
+          const int i = i0 + u * G;
+          int t0 = 0, t1 = 0, slot = 0;
+          if (i <= c1) tree_part(item, s.e.tiles, i * s.share, (i + 1) * s.share, t0, t1, slot);
+          ml[u] = make_float2(-INFINITY, 0.f);
+          o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (t0 < t1) {
+            const size_t part = static_cast<size_t>(i) * 2 + slot;
+            ml[u] = __ldcs(reinterpret_cast<const float2*>(p.part_ml) + part * item_rows + row);
+            o[u] = __ldcs(reinterpret_cast<const float4*>(p.part_o) + (part * (D / 4) + col4) * item_rows + row);
+          }
         }
-      }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) add(ml[u], o[u]);
+        for (int u = 0; u < 4; ++u) add(ml[u], o[u]);
+      }
     }
-  }
-  if (MANY) {
-    if (group > 0) {
-      acc_s[MANY ? (group - 1) * kGroup + me : 0] = acc;
-      ml_s[MANY ? (group - 1) * kGroup + me : 0] = make_float2(m, l);
+    if (MANY) {
+      if (group > 0) {
+        acc_s[MANY ? (group - 1) * kGroup + me : 0] = acc;
+        ml_s[MANY ? (group - 1) * kGroup + me : 0] = make_float2(m, l);
+      }
+      __syncthreads();
+      if (group == 0)
+        for (int g = 0; g < G - 1; ++g) add(ml_s[MANY ? g * kGroup + me : 0], acc_s[MANY ? g * kGroup + me : 0]);
+      __syncthreads();
     }
-    __syncthreads();
-    if (group > 0) return;
-    for (int g = 0; g < G - 1; ++g) add(ml_s[MANY ? g * kGroup + me : 0], acc_s[MANY ? g * kGroup + me : 0]);
+    if (!on || group > 0) continue;
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+    const size_t at = static_cast<size_t>(item.unit) * p.rows + r;
+    reinterpret_cast<uint2*>(p.out)[at * (D / 4) + col4] =
+        make_uint2(Half16<T>::pack(acc.x * inv, acc.y * inv), Half16<T>::pack(acc.z * inv, acc.w * inv));
+    if (col4 == 0 && p.lse2 != nullptr) p.lse2[at] = l == 0.f ? -INFINITY : m + lg2_approx(l);
   }
-  if (!on) return;
-  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-  const size_t at = static_cast<size_t>(item.unit) * p.rows + r;
-  reinterpret_cast<uint2*>(p.out)[at * (D / 4) + col4] =
-      make_uint2(Half16<T>::pack(acc.x * inv, acc.y * inv), Half16<T>::pack(acc.z * inv, acc.w * inv));
-  if (col4 == 0 && p.lse2 != nullptr) p.lse2[at] = l == 0.f ? -INFINITY : m + lg2_approx(l);
 }
 
 template <typename T, int D, int KEYS, bool PAIRS>
@@ -526,9 +523,12 @@ cudaError_t launch_join(const TreeParams& p, const TreePlan& plan, cudaStream_t 
   const long long items = static_cast<long long>(p.batch) * p.layers * p.hkv * plan.items;
   const bool by_border = items > plan.ctas - 1;
   const int rows = p.rows < plan.item_rows ? p.rows : plan.item_rows;
-  const bool many = items * 4 <= plan.ctas;     // many shares an item
+  const bool many = items * 16 <= plan.ctas;    // many shares an item
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(by_border ? plan.ctas - 1 : static_cast<unsigned>(items), (rows + kJoinRows - 1) / kJoinRows);
+  // blocks that are resident together, beside the main kernel's: six an SM
+  const unsigned x = by_border ? plan.ctas - 1 : static_cast<unsigned>(items);
+  const unsigned most = ((many ? 1u : 6u) * plan.sms + x - 1) / x, want = (rows + kJoinRows - 1) / kJoinRows;
+  cfg.gridDim = dim3(x, want < most ? want : most);
   cfg.blockDim = dim3(kJoinRows * (D / 4) * (many ? kJoinGroups : 1));
   cfg.stream = stream;
   cudaLaunchAttribute attr;
@@ -541,7 +541,7 @@ cudaError_t launch_join(const TreeParams& p, const TreePlan& plan, cudaStream_t 
 }
 
 template <typename T, int D, int NT>
-cudaError_t launch_nt(const CUtensorMap (&maps)[5], const TreeParams& p, const TreePlan& plan, cudaStream_t stream) {
+cudaError_t launch_nt(const CUtensorMap (&maps)[7], const TreeParams& p, const TreePlan& plan, cudaStream_t stream) {
   using C = TreeCfg<D, NT>;
   static thread_local int configured_device = -1;
   int dev = 0;
@@ -552,12 +552,12 @@ cudaError_t launch_nt(const CUtensorMap (&maps)[5], const TreeParams& p, const T
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
-  tree_kernel<T, D, NT><<<plan.ctas, kThreads, C::kSmemBytes, stream>>>(maps[0], maps[1], maps[2], maps[3], p);
+  tree_kernel<T, D, NT><<<plan.ctas, kThreads, C::kSmemBytes, stream>>>(maps[0], maps[1], maps[2], maps[3], maps[5], maps[6], p);
   return cudaGetLastError();
 }
 
 template <typename T, int D>
-cudaError_t launch_d(const CUtensorMap (&maps)[5], const TreeParams& p, const TreePlan& plan, cudaStream_t stream) {
+cudaError_t launch_d(const CUtensorMap (&maps)[7], const TreeParams& p, const TreePlan& plan, cudaStream_t stream) {
   if (plan.wide) {
     cudaError_t e = launch_tree_umma(std::is_same<T, __half>::value, D, maps, p, stream);
     return e != cudaSuccess ? e : launch_join<T, D, 128, true>(p, plan, stream);
@@ -632,6 +632,7 @@ TreePlan tree_plan(int rows, int head_dim, int sms) {
   plan.row_tiles = (rows + plan.tile_rows - 1) / plan.tile_rows;
   plan.item_rows = plan.wide && rows > 128 ? 256 : plan.tile_rows;
   plan.items = (rows + plan.item_rows - 1) / plan.item_rows;
+  plan.sms = sms;
   plan.ctas = plan.wide ? sms : 2 * sms;
   return plan;
 }
@@ -640,7 +641,7 @@ size_t tree_ws_bytes(const TreePlan& plan, int head_dim) {
   return static_cast<size_t>(plan.ctas) * 2 * plan.item_rows * (head_dim + 2) * sizeof(float);
 }
 
-cudaError_t launch_tree_attention(bool fp16, int head_dim, const CUtensorMap (&maps)[5], const TreeParams& p,
+cudaError_t launch_tree_attention(bool fp16, int head_dim, const CUtensorMap (&maps)[7], const TreeParams& p,
                                   const TreePlan& plan, cudaStream_t stream) {
   if (head_dim == 128)
     return fp16 ? launch_d<__half, 128>(maps, p, plan, stream) : launch_d<__nv_bfloat16, 128>(maps, p, plan, stream);

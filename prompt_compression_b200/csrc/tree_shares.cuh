@@ -27,39 +27,79 @@ struct TreeElement {       // a batch element
 
 // Length and live nodes of batch element b; an element whose sequence, length
 // or node count is out of range has no rows (its outputs stay unwritten).
+// The nodes lie in the last cached tile, at the next multiple of 8 rows, where
+// all T of them fit behind its rows; otherwise in tiles of their own.
+template <int KEYS>
+__device__ __forceinline__ bool tree_fused(const TreeParams& p, int len) {
+  const int rest = len % KEYS;
+  return p.has_tree && rest > 0 && ((rest + 7) & ~7) + p.node_rows <= KEYS && p.T <= KEYS;
+}
+
 template <int KEYS>
 __device__ __forceinline__ TreeElement tree_element(const TreeParams& p, int b, bool record) {
   TreeElement e;
   e.seq = p.seqs != nullptr ? __ldg(p.seqs + b) : b;
   e.live = p.n_live != nullptr ? __ldg(p.n_live + b) : p.T;
-  bool ok = e.seq >= 0 && e.seq < p.n_seqs && e.live >= 0 && e.live <= p.T;
+  bool ok = e.seq >= 0 && e.seq < p.n_seqs;
   e.len = ok ? __ldg(p.lens + e.seq) : 0;
-  ok = ok && e.len >= 0 && e.len <= static_cast<long long>(p.max_pages) * p.page_rows;
+  ok = ok && e.live >= 0 && e.live <= p.T && e.len >= 0 && e.len <= static_cast<long long>(p.max_pages) * p.page_rows;
   if (!ok) {
     if (record) record_error(SPK_DEVERR_INDEX, b);
     e.seq = 0;
     e.len = 0;
     e.live = 0;
   }
-  const int nodes = p.has_tree ? (e.live + KEYS - 1) / KEYS : 0;
+  const int nodes = p.has_tree && !tree_fused<KEYS>(p, e.len) ? (e.live + KEYS - 1) / KEYS : 0;
   const int t = (e.len + KEYS - 1) / KEYS + nodes;
   e.tiles = e.live == 0 ? 0 : (t > 0 ? t : 1);   // rows without any key still get their zeros
   return e;
 }
 
-// Keys of tile t of an element: [first, first + n) of the cached rows or of the nodes.
+// Key tile t of an element, by columns: [0, rows) the cached rows first ..,
+// [off, off + nodes) the nodes node0 .., nothing behind n.
 struct TreeTile {
-  bool cached;
-  int first, n;
+  int first, rows;
+  int node0, nodes, off;
+  int n;
 };
 template <int KEYS>
 __device__ __forceinline__ TreeTile tree_tile(const TreeParams& p, const TreeElement& e, int t) {
   TreeTile k;
   const int cached = (e.len + KEYS - 1) / KEYS;
-  k.cached = t < cached;
-  k.first = (k.cached ? t : t - cached) * KEYS;
-  k.n = k.cached ? min(KEYS, e.len - k.first) : (p.has_tree ? min(KEYS, e.live - k.first) : 0);
+  k.first = t * KEYS;
+  k.rows = t < cached ? min(KEYS, e.len - k.first) : 0;
+  k.node0 = k.nodes = k.off = 0;
+  if (t >= cached) {
+    k.node0 = (t - cached) * KEYS;
+    k.nodes = p.has_tree ? min(KEYS, e.live - k.node0) : 0;
+  } else if (k.rows < KEYS && tree_fused<KEYS>(p, e.len)) {
+    k.off = (k.rows + 7) & ~7;
+    k.nodes = e.live;
+  }
+  k.n = k.nodes > 0 ? k.off + k.nodes : k.rows;
   return k;
+}
+
+// Which of the columns c0 .. c0 + 31 of a tile the row of node i sees (`there`:
+// the row exists): the cached rows, and the nodes by its visibility words.
+__device__ __forceinline__ uint32_t tree_word(const TreeParams& p, int b, const TreeTile& t, int c0, int i, bool there) {
+  const int rows = t.rows - c0, left = t.n - c0;
+  uint32_t w = rows >= 32 ? 0xffffffffu : rows > 0 ? (1u << rows) - 1u : 0u;
+  if (t.nodes == 0 || left <= 0 || !there) return w;
+  const int s = t.node0 + c0 - t.off;            // node of column c0 (below 0: the gap and the rows before it)
+  if (s <= -32) return w;
+  uint32_t v;
+  if (p.mask != nullptr) {
+    const uint32_t* row = p.mask + (static_cast<size_t>(b) * p.T + i) * p.words;
+    const int k = s >> 5;
+    const uint32_t lo = k >= 0 ? __ldg(row + k) : 0u, hi = k + 1 < p.words ? __ldg(row + k + 1) : 0u;
+    v = __funnelshift_r(lo, hi, s & 31);
+  } else {                                       // a chain: nodes 0 .. i
+    v = i < s ? 0u : i - s >= 31 ? 0xffffffffu : (2u << (i - s)) - 1u;
+    if (s < 0) v &= 0xffffffffu << -s;
+  }
+  if (left < 32) v &= (1u << left) - 1u;
+  return w | v;
 }
 
 __device__ __forceinline__ int tree_jobs(const TreeParams& p, const TreeElement& e) {
@@ -172,6 +212,7 @@ __device__ __forceinline__ void tree_part(const TreeItem& i, int tiles, int begi
 
 struct TreeRun {           // a part of an item that a CTA works on
   int b, unit, row0, t0, t1, slot;
+  int pool;                // (layer * n_pages) * hkv + KV head: the unit of page 0 in the pages' maps
   bool pair;
   TreeElement e;
   __device__ __forceinline__ int jobs() const { return (t1 - t0) * (pair ? 2 : 1); }
@@ -197,6 +238,8 @@ struct TreeWalker {
       r.unit = i.unit;
       r.row0 = i.row0;
       r.pair = i.pair;
+      const int lh = i.unit - b * p.layers * p.hkv, layer = lh / p.hkv;
+      r.pool = layer * p.n_pages * p.hkv + lh - layer * p.hkv;
       r.e = e;
       x = min(end, i.first + i.jobs);
       if (r.t0 < r.t1) return true;

@@ -9,12 +9,12 @@
 // with two softmax groups of four warps (thread = query row), so that one
 // group's exponentials run under the other's products.  Rows of a unit are
 // taken 256 at a time while there are more than 128 of them (a PAIR: group x
-// has the query tile x, both use every K/V tile), the rest 128 at a time
-// (ALONE: both groups have the same query tile, group x the key tiles t = x
-// mod 2, and their states are joined at the end).  A job is one (query tile,
-// key tile) product pair; job j belongs to group j mod 2, and the products are
-// issued in the order S(0), S(1), PV(0), S(2), PV(1), S(3), ...: when S(j + 2)
-// has landed, O of its group is quiescent and may be rescaled.
+// has query tile x, both use every K/V tile), the rest 128 at a time (ALONE:
+// both groups have the query tile, group x the key tiles x, x + 2, ...; their
+// states are joined at the end).  A job is one (query tile, key tile) product
+// pair; the products go out in the order S0(0), S1(0), PV0(0), S0(1), PV1(0),
+// S1(1), ...: when a group's S(i + 1) has landed, its O is quiescent and may be
+// rescaled.
 //   warps 0-3, 4-7  softmax groups 0, 1
 //   warps 8, 9      TMA producers: Q and the K tiles, the V tiles, page by page
 //                   through one ring
@@ -91,7 +91,8 @@ struct UmmaShared {
   int abort_flag;
 };
 
-// QT query tiles of a unit share the K/V tiles (1: no unit has more than 128 rows).
+// QT query tiles of a unit share the K/V tiles (1: no unit has more than 128
+// rows; its place goes to the ring, whose depth hides the memory's latency).
 template <int D, int QT>
 struct UmmaCfg {
   static constexpr int kTileBytes = 128 * D * 2;          // 128 rows of Q, K or V
@@ -111,33 +112,54 @@ constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 constexpr uint32_t kKMajorLo = 1u << 16, kMnMajorLo = (16384u >> 4) << 16;
 
 // D[tmem] (+)= A[smem] B[smem]^T; a, b: low descriptor words.
-__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
+// The whole warp executes these, `leader` alone issues: without a branch, what
+// is the same in every lane can stay in uniform registers.
+__device__ __forceinline__ void umma_ss(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                        bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\t"
       "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}\n" ::"r"(d),
-      "r"(a), "r"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "n"(kDescHi)
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "n"(kDescHi), "r"(leader)
       : "memory");
 }
 // D[tmem] (+)= A[tmem] B[smem]^T
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
+__device__ __forceinline__ void umma_ts(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                        bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\t"
       "mov.b64 db, {%2, %5};\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}\n" ::"r"(d),
-      "r"(a), "r"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "n"(kDescHi)
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "n"(kDescHi), "r"(leader)
       : "memory");
 }
-__device__ __forceinline__ bool elect_one() {
+__device__ __forceinline__ void tma_load_if(uint32_t leader, uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0,
+                                            int c1, int c2) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+      "@q cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];\n\t}\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(leader)
+      : "memory");
+}
+// Arrive on `bar` when the products issued so far are done.
+__device__ __forceinline__ void commit_if(uint32_t leader, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(smem_u32(bar)),
+      "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t elect_one() {
   uint32_t one;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "elect.sync _|p, 0xffffffff;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}\n"
       : "=r"(one));
-  return one != 0;
+  return one;
 }
 // A value that is the same in every lane, as one the compiler knows to be.
 __device__ __forceinline__ int uniform(int v) { return __reduce_max_sync(0xffffffffu, v); }
@@ -200,7 +222,8 @@ template <typename T, int D, int QT>
 __global__ void __launch_bounds__(kUmmaThreads, 1)
     tree_umma_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap ktmap,
-                     const __grid_constant__ CUtensorMap vtmap, const __grid_constant__ TreeParams p) {
+                     const __grid_constant__ CUtensorMap vtmap, const __grid_constant__ CUtensorMap k8map,
+                     const __grid_constant__ CUtensorMap v8map, const __grid_constant__ TreeParams p) {
   using C = UmmaCfg<D, QT>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* const Q_s = smem;                                  // [QT tiles]
@@ -250,7 +273,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
   volatile int* const abort_v = &sh.abort_flag;
   TreeRun run;
   uint32_t taken = 0;
-  // the next run; false behind the last one (or when the CTA gives up: ok)
+  // the next run; false behind the last one, or when the CTA gives up (ok)
   auto next_run = [&](bool& ok) -> bool {
     const uint32_t s = taken % kRunSlots;
     ok = __all_sync(0xffffffffu, bar_wait(&sh.run_full[s], (taken / kRunSlots) & 1, abort_v, umma_site(5, 0)));
@@ -279,63 +302,100 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     }
   } else if (warp == kProducerWarp || warp == kProducerWarp + 1) {
     // --------------------------------------------------------------- producers
-    const int v = warp - kProducerWarp;                        // 0: K (and Q), 1: V
+    const uint32_t leader = elect_one();
+    const int v = uniform(warp - kProducerWarp);               // 0: K (and Q), 1: V
     const CUtensorMap* const pages = v ? &vmap : &kmap;
+    const CUtensorMap* const pages8 = v ? &v8map : &k8map;     // in parts of 8 rows, for a tile that ends early
     const CUtensorMap* const nodes = v ? &vtmap : &ktmap;
     uint32_t seq = v;              // K and V tiles in their order: slot seq % kSlots
     int runs = 0, q_last = -1;
     bool ok = true;
+    const int per_tile = kKeys / p.box_rows;                   // parts of a full tile
     while (ok && next_run(ok)) {
-      const int* const table = p.table + static_cast<size_t>(run.e.seq) * p.max_pages;
-      const int lh = run.unit - run.b * p.layers * p.hkv;
-      const int layer = lh / p.hkv, head = lh - layer * p.hkv;
       if (v == 0) {
         ok = __all_sync(0xffffffffu, bar_wait(&sh.q_empty, (runs & 1) ^ 1, abort_v, umma_site(0, 0)));
         if (!ok) break;
         if (lane == 0) {
           const int tiles = run.pair ? 2 : 1;
           mbar_arrive_expect_tx(&sh.q_full, tiles * C::kTileBytes);
+#pragma unroll 1
           for (int x = 0; x < tiles; ++x)
+#pragma unroll
             for (int a = 0; a < C::kAtoms; ++a)
               tma_load_3d(Q_s + x * C::kTileBytes + a * 16384, &qmap, &sh.q_full, a * 64, run.row0 + x * 128, run.unit);
         }
         q_last = runs & 1;
       }
+      const int full = run.e.len / kKeys;
+      // lane i has the place of part `at` + i of the sequence's full tiles (its page's
+      // unit in the pages' map, the row in the page): the page table is read for 32
+      // parts at a time
+      int at = -64, unit = 0, row = 0;
+#pragma unroll 1
       for (int t = run.t0; t < run.t1; ++t) {
-        const TreeTile tile = tree_tile<kKeys>(p, run.e, t);
-        // lane i: where part i of the tile is
-        const int boxes = tile.cached ? (tile.n + p.box_rows - 1) / p.box_rows : tile.n > 0 ? 1 : 0;
-        int unit = run.unit, first = tile.first;
-        if (tile.cached && lane < boxes) {
-          const int t_row = tile.first + lane * p.box_rows;
-          const int at = t_row / p.page_rows;
-          first = t_row - at * p.page_rows;
-          const int page = __ldg(table + at);
-          if (page < 0 || page >= p.n_pages) {
-            if (v == 0) record_error(SPK_DEVERR_INDEX, run.b);
-            unit = p.layers * p.n_pages * p.hkv;             // outside the map: the box reads as zeros
-          } else {
-            unit = (layer * p.n_pages + page) * p.hkv + head;
+        int parts = per_tile, more = 0, from = t * per_tile;
+        TreeTile tile;
+        tile.nodes = 0;
+        const bool last = t >= full;                           // the last rows, or nodes: see tree_tile
+        if (last) {
+          tile = tree_tile<kKeys>(p, run.e, t);
+          parts = tile.rows / p.box_rows;                      // then the rest in parts of 8 rows
+          more = (tile.rows - parts * p.box_rows + 7) / 8;
+        }
+        if (last || from + per_tile > at + 32) {
+          at = last ? 0 : from;
+          const int t_row = !last ? (from + lane) * p.box_rows
+                            : lane < parts ? tile.first + lane * p.box_rows
+                            : lane < parts + more ? tile.first + parts * p.box_rows + (lane - parts) * 8 : 0x7fffffff;
+          unit = row = 0;
+          if (t_row < run.e.len) {
+            const int pg = t_row / p.page_rows;
+            row = t_row - pg * p.page_rows;
+            const int page = __ldg(p.table + static_cast<size_t>(run.e.seq) * p.max_pages + pg);
+            if (page < 0 || page >= p.n_pages) {
+              if (v == 0) record_error(SPK_DEVERR_INDEX, run.b);
+              unit = p.layers * p.n_pages * p.hkv;             // outside the map: the part reads as zeros
+            } else {
+              unit = run.pool + page * p.hkv;
+            }
           }
         }
+        from = last ? 0 : from - at;
         const int slot = seq % C::kSlots;
         ok = __all_sync(0xffffffffu, bar_wait(&sh.empty[slot], ((seq / C::kSlots) & 1) ^ 1, abort_v, umma_site(0, 1 + v)));
         if (!ok) break;
-        if (lane == 0) {
-          if (boxes == 0)
-            mbar_arrive(&sh.full[slot]);
-          else
-            mbar_arrive_expect_tx(&sh.full[slot], tile.cached ? boxes * p.box_rows * 128 * C::kAtoms : C::kTileBytes);
-        }
-        const CUtensorMap* const map = tile.cached ? pages : nodes;
+        uint64_t* const bar = &sh.full[slot];
         uint8_t* const dst = ring + slot * C::kTileBytes;
-        for (int i = 0; i < boxes; ++i) {                      // lane 0 copies part after part
-          const int u = __shfl_sync(0xffffffffu, unit, i), f = __shfl_sync(0xffffffffu, first, i);
-          if (lane == 0) {
+        const int bytes = (parts * p.box_rows + more * 8 + (tile.nodes > 0 ? p.node_rows : 0)) * 128 * C::kAtoms;
+        if (leader) {
+          if (bytes == 0)
+            mbar_arrive(bar);
+          else
+            mbar_arrive_expect_tx(bar, bytes);
+        }
+        // whole parts, then parts of 8 rows (places from lane 0: of the last rows)
+        const uint32_t d0 = smem_u32(dst), b0 = smem_u32(bar);
+#pragma unroll 1
+        for (int k = 0; k < parts; ++k) {
+          const int u = uniform(lane == from + k ? unit : -1), f = uniform(lane == from + k ? row : -1);
+#pragma unroll
+          for (int a = 0; a < C::kAtoms; ++a)
+            tma_load_if(leader, d0 + a * 16384 + k * p.box_rows * 128, pages, b0, a * 64, f, u);
+        }
+        if (last) {
+#pragma unroll 1
+          for (int k = parts; k < parts + more; ++k) {
+            const int u = uniform(lane == k ? unit : -1), f = uniform(lane == k ? row : -1);
 #pragma unroll
             for (int a = 0; a < C::kAtoms; ++a)
-              tma_load_3d(dst + a * 16384 + i * p.box_rows * 128, map, &sh.full[slot], a * 64, f, u);
+              tma_load_if(leader, d0 + a * 16384 + (parts * p.box_rows + (k - parts) * 8) * 128, pages8, b0, a * 64, f, u);
           }
+          if (tile.nodes > 0) {
+#pragma unroll
+            for (int a = 0; a < C::kAtoms; ++a)
+              tma_load_if(leader, d0 + a * 16384 + tile.off * 128, nodes, b0, a * 64, tile.node0, run.unit);
+          }
+          at = -64;
         }
         __syncwarp();
         seq += 2;
@@ -354,7 +414,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     // the same in every lane and stays in uniform registers; one lane issues.
     // (With one lane in the branch each product took 85 clocks to issue, more
     // than its 64 to run.)
-    const bool leader = elect_one();
+    const uint32_t leader = elect_one();
     bool ok = true;
     int runs = 0;
     constexpr uint32_t idesc_s = idesc_of<T>(128, 128);
@@ -380,73 +440,68 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       tc_fence_after();
       const uint32_t qa = QT == 2 && x == 1 && pair ? q_lo + (C::kTileBytes >> 4) : q_lo;
       const uint32_t ka = ring_lo + ks * (C::kTileBytes >> 4);
-      const bool last = !pair || x == 1;                       // of this K tile
-      if (leader) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-          umma_ss(x * 256, (qa + off) | kKMajorLo, (ka + off) | kKMajorLo, idesc_s, kk > 0);
-        }
-        umma_commit(&sh.s_full[x]);
-        if (last) umma_commit(&sh.empty[ks]);
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+        umma_ss(leader, x * 256, (qa + off) | kKMajorLo, (ka + off) | kKMajorLo, idesc_s, kk > 0);
       }
-      __syncwarp();
-      if (last) advance(ks, kph);
+      commit_if(leader, &sh.s_full[x]);
+      if (!pair || x == 1) {                                   // the K tile's last use
+        commit_if(leader, &sh.empty[ks]);
+        advance(ks, kph);
+      }
       return true;
     };
     // O of group x += P V(next tile, of n keys), in two halves: keys 64 .. 127 as
     // soon as the softmax has stored their P, then keys 0 .. 63; only the k-steps
     // that hold a key
-    auto issue_pv = [&](auto X, bool pair, int n, bool first, bool fresh) -> bool {
+    auto issue_pv = [&](auto X, bool pair, int n, bool fresh) -> bool {
       constexpr int x = decltype(X)::value;
       const uint32_t ph = (pph >> x) & 1u;
       pph ^= 1u << x;
       const uint32_t va = ring_lo + vs * (C::kTileBytes >> 4);
-      const bool last = !pair || x == 1;
       if (!(pair && x == 1) && !wait(&sh.full[vs], vph, 6)) return false;
       // the previous run's O has been read before O is restarted
-      if (first && runs > 0 && !wait(&sh.o_empty, (runs - 1) & 1, 7)) return false;
-      if (!wait(&sh.p_half[x], ph, 2 + x)) return false;
-      tc_fence_after();
-      if (leader && n > 64) {
+      if (fresh && x == 0 && runs > 0 && !wait(&sh.o_empty, (runs - 1) & 1, 7)) return false;
+      if (n > 64) {
+        if (!wait(&sh.p_half[x], ph, 2 + x)) return false;
+        tc_fence_after();
 #pragma unroll
         for (int kk = 4; kk < 8; ++kk)
-          if (kk * 16 < n) umma_ts(x * 256 + 128, x * 256 + 64 + kk * 8, (va + kk * (2048 >> 4)) | kMnMajorLo, idesc_pv, kk > 4 || !fresh);
+          umma_ts(kk * 16 < n ? leader : 0u, x * 256 + 128, x * 256 + 64 + kk * 8, (va + kk * (2048 >> 4)) | kMnMajorLo,
+                  idesc_pv, kk > 4 || !fresh);
       }
-      __syncwarp();
       if (!wait(&sh.p_full[x], ph, 4 + x)) return false;
       tc_fence_after();
-      if (leader) {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          if (kk * 16 < n) umma_ts(x * 256 + 128, x * 256 + 64 + kk * 8, (va + kk * (2048 >> 4)) | kMnMajorLo, idesc_pv, kk > 0 || n > 64 || !fresh);
-        if (last) umma_commit(&sh.empty[vs]);
+      for (int kk = 0; kk < 4; ++kk)
+        umma_ts(kk * 16 < n ? leader : 0u, x * 256 + 128, x * 256 + 64 + kk * 8, (va + kk * (2048 >> 4)) | kMnMajorLo,
+                idesc_pv, kk > 0 || n > 64 || !fresh);
+      if (!pair || x == 1) {
+        commit_if(leader, &sh.empty[vs]);
+        advance(vs, vph);
       }
-      __syncwarp();
-      if (last) advance(vs, vph);
       return true;
     };
     constexpr std::integral_constant<int, 0> G0{};
     constexpr std::integral_constant<int, 1> G1{};
     while (ok && next_run(ok)) {
-      const bool pair = __any_sync(0xffffffffu, run.pair);
-      const int jobs = uniform(run.jobs());
-      const int full_end = uniform(run.e.len / kKeys) - uniform(run.t0);   // tiles before it hold kKeys keys
-      auto keys_of = [&](int t) { return t < full_end ? kKeys : uniform(tree_tile<kKeys>(p, run.e, run.t0 + t).n); };
+      const bool pair = QT == 2 && __any_sync(0xffffffffu, run.pair);
+      const int tiles = uniform(run.t1 - run.t0), full = uniform(run.e.len / kKeys - run.t0);   // tiles before it have kKeys keys
+      const int j0 = pair ? tiles : (tiles + 1) / 2, j1 = pair ? tiles : tiles / 2;
+      auto keys_of = [&](int t) { return t < full ? kKeys : uniform(tree_tile<kKeys>(p, run.e, run.t0 + t).n); };
       if (!(ok = wait(&sh.q_full, runs & 1, 0))) break;
-      // S(j + 2) goes out behind PV(j)
-      for (int j = -2; ok && j < jobs; j += 2) {
-        const int t = pair ? j >> 1 : j;
-        if (j >= 0) ok = issue_pv(G0, pair, keys_of(t), j == 0, j == 0);
-        if (ok && j + 2 < jobs) ok = issue_s(G0, pair);
-        if (ok && j >= 0 && j + 1 < jobs) ok = issue_pv(G1, pair, keys_of(pair ? t : t + 1), false, j == 0);
-        if (ok && j + 3 < jobs) ok = issue_s(G1, pair);
-        if (leader && j + 2 < jobs && j + 4 >= jobs) umma_commit(&sh.q_empty);    // the last S is out
-        __syncwarp();
+      // S(i + 1) goes out behind PV(i)
+#pragma unroll 1
+      for (int i = -1; ok && i < j0; ++i) {
+        if (i >= 0) ok = issue_pv(G0, pair, keys_of(pair ? i : 2 * i), i == 0);
+        if (ok && i + 1 < j0) ok = issue_s(G0, pair);
+        if (ok && i >= 0 && i < j1) ok = issue_pv(G1, pair, keys_of(pair ? i : 2 * i + 1), i == 0);
+        if (ok && i + 1 < j1) ok = issue_s(G1, pair);
+        if (i + 2 == j0) commit_if(leader, &sh.q_empty);                       // the last S is out
       }
       if (!ok) break;
-      if (leader) umma_commit(&sh.run_done);
-      __syncwarp();
+      commit_if(leader, &sh.run_done);
       ++runs;
     }
     if (!ok && leader) {             // the products in flight end before the block does
@@ -468,43 +523,33 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       return __all_sync(0xffffffffu, bar_wait(bar, parity, abort_v, umma_site(2 + x, which)));
     };
     while (ok && next_run(ok)) {
-      const int row = run.row0 + (run.pair ? x * 128 : 0) + r;  // row of the unit
+      const bool pair = QT == 2 && run.pair, alone = !pair;
+      const int tiles = run.t1 - run.t0, jobs = pair ? tiles : (tiles + 1 - x) / 2;
+      const int row = run.row0 + (pair ? x * 128 : 0) + r;      // row of the unit
       const bool there = row < p.rows;
+      const bool idle = row - lane >= p.rows;                  // no row of this warp's exists
       const int node = there ? row % p.T : 0;
-      const int n_jobs = run.jobs();
       float m = -INFINITY, l = 0.f;                            // running maximum of c2 s, sum
-      bool fresh = true;                                       // O holds nothing yet
-      for (int j = x; ok && j < n_jobs; j += 2, ++job) {
-        const int t = run.pair ? j >> 1 : j;
-        const TreeTile tile = tree_tile<kKeys>(p, run.e, run.t0 + t);
-        const bool full_tile = tile.cached && tile.n == kKeys;
+      for (int i = 0; i < jobs; ++i, ++job) {
+        const TreeTile tile = tree_tile<kKeys>(p, run.e, run.t0 + (pair ? i : 2 * i + x));
+        const bool full_tile = tile.rows == kKeys;
         // before S is there: which keys this row sees, as words of 32 columns ...
         uint32_t w0 = 0, w1 = 0, w2 = 0, w3 = 0;
         if (!full_tile) {
-          auto word = [&](int c) -> uint32_t {
-            const int left = tile.n - c * 32;
-            if (left <= 0) return 0u;
-            const uint32_t here = left >= 32 ? 0xffffffffu : (1u << left) - 1u;
-            if (tile.cached) return here;
-            if (!there) return 0u;
-            const int n0 = tile.first + c * 32;
-            if (p.mask != nullptr)
-              return here & __ldg(p.mask + (static_cast<size_t>(run.b) * p.T + node) * p.words + (n0 >> 5));
-            return node < n0 ? 0u : here & (node - n0 >= 31 ? 0xffffffffu : (2u << (node - n0)) - 1u);
-          };
-          w0 = word(0);
-          w1 = word(1);
-          w2 = word(2);
-          w3 = word(3);
-          // ... and zeros in V's rows behind the last key, up to the end of its k-step:
+          w0 = tree_word(p, run.b, tile, 0, node, there);
+          w1 = tree_word(p, run.b, tile, 32, node, there);
+          w2 = tree_word(p, run.b, tile, 64, node, there);
+          w3 = tree_word(p, run.b, tile, 96, node, there);
+          // ... and zeros in V's rows without a key, up to the end of the last k-step:
           // whatever the slot holds there (it may be NaN) must not meet the zeros of P
-          const int bad = (16 - (tile.n & 15)) & 15;
-          if (bad > 0 && !(run.pair && x == 1)) {              // (a pair's group 1 comes behind group 0's products)
-            const uint32_t seq = 2 * (base + t) + 1;
+          const int end = (tile.n + 15) & ~15, gap = tile.nodes > 0 ? tile.off - tile.rows : 0, bad = gap + end - tile.n;
+          if (bad > 0 && !(pair && x == 1)) {                  // (a pair's group 1 comes behind group 0's products)
+            const uint32_t seq = 2 * (base + (pair ? i : 2 * i + x)) + 1;
             const int slot = seq % C::kSlots;
             if (!(ok = wait_all(&sh.full[slot], (seq / C::kSlots) & 1, 1))) break;
-            for (int i = r; i < bad * (D / 8); i += 128) {
-              const int vr = tile.n + i / (D / 8), ch = i % (D / 8);
+            for (int k = r; k < bad * (D / 8); k += 128) {
+              const int b = k / (D / 8), ch = k % (D / 8);
+              const int vr = b < gap ? tile.rows + b : tile.n + b - gap;
               *reinterpret_cast<uint4*>(ring + slot * C::kTileBytes + (ch >> 3) * 16384 + vr * 128 +
                                         (((ch & 7) ^ (vr & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
             }
@@ -517,7 +562,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
           const bool need = mt > m + kRescaleLog2;             // the first key of a row: m = -inf
           if (__any_sync(0xffffffffu, need)) {
             const float alpha = need ? ex2_approx(m - mt) : 1.f;
-            if (!fresh) {
+            if (i > 0) {                                       // O holds this run's products
 #pragma unroll 1
               for (int ch = 0; ch < D / 32; ++ch) {
                 uint32_t o[32];
@@ -542,67 +587,94 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                                  fmaxf(__uint_as_float(a[k + 2]), __uint_as_float(a[k + 3]))));
           return mx;
         };
-        // 32 columns at a time, those that hold a key (loops, not straight code: see
-        // bar_wait).  First the row's maximum; what a row does not see becomes -inf
-        const int chunks = (tile.n + 31) / 32;
-        float mx = -INFINITY;
-#pragma unroll 1
-        for (int c = 0; c < chunks; ++c) {
-          uint32_t a[32];
-          tmem_ld32(mine + c * 32, a);
-          tmem_ld_wait(a);
-          if (!full_tile) {
-            const uint32_t w = c == 0 ? w0 : c == 1 ? w1 : c == 2 ? w2 : w3;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) a[i] = (w >> i) & 1u ? a[i] : __float_as_uint(-INFINITY);
-            tmem_st32(mine + c * 32, a);
-          }
-          mx = max32(a, mx);
-        }
-        if (!full_tile) tmem_st_wait();
-        rescale(mx * p.c2);
-        // then P = 2^(c2 s - m), from the last chunk down: P of chunk c lies over S of
-        // chunk c / 2 + 2
-        const float ref = m == -INFINITY ? 0.f : m;            // no key yet: every weight is 2^-inf = 0
-        const float2 c2v = f2(p.c2, p.c2), nm = f2(-ref, -ref);
+        // The row's maximum, then P = 2^(c2 s - m) in 16 bits over the second half of S.
         float2 acc = f2(0.f, 0.f);
-#pragma unroll 1
-        for (int c = chunks - 1; c >= 0; --c) {
-          uint32_t a[32], pk[16];
-          tmem_ld32(mine + c * 32, a);
-          tmem_ld_wait(a);
+        auto exp32 = [&](const uint32_t (&a)[32], float2 nm, int c) {
+          const float2 c2v = f2(p.c2, p.c2);
+          uint32_t pk[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 e = exp2_mufu_pair(__ffma2_rn(f2(__uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1])), c2v, nm));
+          for (int k = 0; k < 16; ++k) {
+            const float2 e = exp2_mufu_pair(__ffma2_rn(f2(__uint_as_float(a[2 * k]), __uint_as_float(a[2 * k + 1])), c2v, nm));
             acc = __fadd2_rn(acc, e);
-            pk[i] = Half16<T>::pack(e.x, e.y);
+            pk[k] = Half16<T>::pack(e.x, e.y);
           }
           tmem_st16(mine + 64 + c * 16, pk);
-          if (c == 2) {                                        // keys 64 .. 127 are in
-            tmem_st_wait();
-            tc_fence_before();
+        };
+        auto half_done = [&]() {
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.p_half[x]);
+        };
+        if (idle) {
+          // (rows of a product depend on their own row of P only: nothing to store)
+          if (lane == 0) mbar_arrive(&sh.p_half[x]);
+        } else if (full_tile) {
+          // columns 64 .. 127 stay in registers, 0 .. 63 are read twice, the second
+          // time under the exponentials of the others
+          uint32_t a[32], b[32], c[32], d[32];
+          tmem_ld32(mine, a);
+          tmem_ld32(mine + 32, b);
+          tmem_ld_wait2(a, b);
+          tmem_ld32(mine + 64, c);
+          tmem_ld32(mine + 96, d);
+          const float mx = max32(b, max32(a, -INFINITY));
+          tmem_ld_wait2(c, d);
+          rescale(max32(d, max32(c, mx)) * p.c2);
+          const float2 nm = f2(-m, -m);
+          tmem_ld32(mine + 32, b);
+          exp32(d, nm, 3);
+          exp32(c, nm, 2);
+          tmem_ld_wait(b);                                     // (read before P of columns 64 .. 127 is used)
+          half_done();
+          tmem_ld32(mine, a);
+          exp32(b, nm, 1);
+          tmem_ld_wait(a);
+          exp32(a, nm, 0);
+        } else {
+          // what a row does not see becomes -inf
+          const int chunks = (tile.n + 31) / 32;               // of 32 columns that hold a key
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < chunks; ++c) {
+            const uint32_t w = c == 0 ? w0 : c == 1 ? w1 : c == 2 ? w2 : w3;
+            uint32_t a[32];
+            tmem_ld32(mine + c * 32, a);
+            tmem_ld_wait(a);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) a[k] = (w >> k) & 1u ? a[k] : __float_as_uint(-INFINITY);
+            tmem_st32(mine + c * 32, a);
+            mx = max32(a, mx);
+          }
+          tmem_st_wait();
+          rescale(mx * p.c2);
+          const float ref = m == -INFINITY ? 0.f : m;          // no key yet: every weight is 2^-inf = 0
+          // from the last chunk down: P of chunk c lies over S of chunk c / 2 + 2
+#pragma unroll 1
+          for (int c = chunks - 1; c >= 0; --c) {
+            uint32_t a[32];
+            tmem_ld32(mine + c * 32, a);
+            tmem_ld_wait(a);
+            exp32(a, f2(-ref, -ref), c);
+            if (c == 2) half_done();                           // keys 64 .. 127 are in
+          }
+          if (chunks < 3) {
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.p_half[x]);
           }
         }
         l += acc.x + acc.y;
-        if (chunks < 3) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.p_half[x]);
-        }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.p_full[x]);
-        fresh = false;
       }
       if (!ok) break;
-      // ---- the run's outputs: a pair's groups have a query tile each; ALONE, both
-      // groups' states together, half the columns each
+      // ---- the run's outputs; ALONE: of both groups' states together, half the columns each
       if (!(ok = wait_all(&sh.run_done, runs & 1, 2))) break;
       tc_fence_after();
       float f0 = 1.f, f1 = 0.f;                                // weights of O_0 and O_1 (ALONE)
-      if (!run.pair) {
+      if (alone) {
         // (the other group read the previous run's states before run_done of this one)
         sh.ml[x][r] = make_float2(m, l);
         __syncwarp();
@@ -622,66 +694,68 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       f0 *= scale;
       f1 *= scale;
       const bool any = l != 0.f;                               // a row without keys: zeros, whatever O holds
-      const bool both = !run.pair && n_jobs > 1;               // group 1 had a job
-      const uint32_t o_at = (run.pair ? mine : lanes) + 128;
-      const size_t part = static_cast<size_t>(blockIdx.x) * 2 + run.slot;
-      const int part_row = (run.pair ? x * 128 : 0) + r;
-      const int c_end = run.pair ? D : (x + 1) * (D / 2);
+      const bool both = alone && tiles > 1;                 // group 1 had a job
+      const uint32_t o_at = (alone ? lanes : mine) + 128;
+      const size_t place = static_cast<size_t>(blockIdx.x) * 2 + run.slot;
+      const int part_row = (pair ? x * 128 : 0) + r;
+      const int c_end = alone ? (x + 1) * (D / 2) : D;
       const uint32_t lives = __ballot_sync(0xffffffffu, live);
+      if (lives != 0) {
 #pragma unroll 1
-      for (int c = run.pair ? 0 : x * (D / 2); c < c_end; c += 32) {
-        uint32_t o[32];
-        tmem_ld32(o_at + c, o);
-        if (both) {
-          uint32_t o1[32];
-          tmem_ld32(lanes + 256 + 128 + c, o1);
-          tmem_ld_wait2(o, o1);
+        for (int c = alone ? x * (D / 2) : 0; c < c_end; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(o_at + c, o);
+          if (both) {
+            uint32_t o1[32];
+            tmem_ld32(lanes + 256 + 128 + c, o1);
+            tmem_ld_wait2(o, o1);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(fmaf(__uint_as_float(o1[k]), f1, __uint_as_float(o[k]) * f0));
-        } else {
-          tmem_ld_wait(o);
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(fmaf(__uint_as_float(o1[k]), f1, __uint_as_float(o[k]) * f0));
+          } else {
+            tmem_ld_wait(o);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f0);
-        }
-        if (!any) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = 0u;
-        }
-        if (whole) {
-          // 32 columns a row, 8 (16 bytes) to a vector: four lanes exchange vectors so
-          // that each store covers 64 bytes of eight rows
-          uint4 v[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            v[i].x = Half16<T>::pack(__uint_as_float(o[8 * i + 0]), __uint_as_float(o[8 * i + 1]));
-            v[i].y = Half16<T>::pack(__uint_as_float(o[8 * i + 2]), __uint_as_float(o[8 * i + 3]));
-            v[i].z = Half16<T>::pack(__uint_as_float(o[8 * i + 4]), __uint_as_float(o[8 * i + 5]));
-            v[i].w = Half16<T>::pack(__uint_as_float(o[8 * i + 6]), __uint_as_float(o[8 * i + 7]));
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f0);
           }
-          transpose4(v, lane);
-          T* const dst = static_cast<T*>(p.out) + (static_cast<size_t>(run.unit) * p.rows + row - (lane & 3)) * D + c + (lane & 3) * 8;
+          if (!any) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)                          // of row (lane & ~3) + i
-            if ((lives >> ((lane & ~3) + i)) & 1u) *reinterpret_cast<uint4*>(dst + i * D) = v[i];
-        } else if (live) {
-          // partial results lie [4 columns][row]: a store covers 32 rows together
-          float4* const dst = reinterpret_cast<float4*>(p.part_o) + (part * (D / 4) + c / 4) * (QT * 128) + part_row;
+            for (int k = 0; k < 32; ++k) o[k] = 0u;
+          }
+          if (whole) {
+            // 32 columns a row, 8 (16 bytes) to a vector: four lanes exchange vectors so
+            // that each store covers 64 bytes of eight rows
+            uint4 v[4];
 #pragma unroll
-          for (int v = 0; v < 8; ++v)
-            dst[v * (QT * 128)] = make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]),
-                                              __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3]));
+            for (int k = 0; k < 4; ++k) {
+              v[k].x = Half16<T>::pack(__uint_as_float(o[8 * k + 0]), __uint_as_float(o[8 * k + 1]));
+              v[k].y = Half16<T>::pack(__uint_as_float(o[8 * k + 2]), __uint_as_float(o[8 * k + 3]));
+              v[k].z = Half16<T>::pack(__uint_as_float(o[8 * k + 4]), __uint_as_float(o[8 * k + 5]));
+              v[k].w = Half16<T>::pack(__uint_as_float(o[8 * k + 6]), __uint_as_float(o[8 * k + 7]));
+            }
+            transpose4(v, lane);
+            T* const dst = static_cast<T*>(p.out) + (static_cast<size_t>(run.unit) * p.rows + row - (lane & 3)) * D + c + (lane & 3) * 8;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)                        // of row (lane & ~3) + k
+              if ((lives >> ((lane & ~3) + k)) & 1u) *reinterpret_cast<uint4*>(dst + k * D) = v[k];
+          } else if (live) {
+            // partial results lie [4 columns][row]: a store covers 32 rows together
+            float4* const dst = reinterpret_cast<float4*>(p.part_o) + (place * (D / 4) + c / 4) * p.item_rows + part_row;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              dst[k * p.item_rows] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                                 __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+          }
         }
       }
-      if (live && (run.pair || x == 0)) {
+      if (live && (!alone || x == 0)) {
         if (!whole)
-          reinterpret_cast<float2*>(p.part_ml)[part * (QT * 128) + part_row] = make_float2(m, l);
+          reinterpret_cast<float2*>(p.part_ml)[place * p.item_rows + part_row] = make_float2(m, l);
         else if (p.lse2 != nullptr)
           p.lse2[static_cast<size_t>(run.unit) * p.rows + row] = l == 0.f ? -INFINITY : m + lg2_approx(l);
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.o_empty);
-      base += run.t1 - run.t0;
+      base += tiles;
       ++runs;
     }
   }
@@ -696,7 +770,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
 }
 
 template <typename T, int D, int QT>
-cudaError_t launch_qt(const CUtensorMap (&maps)[5], const TreeParams& p, cudaStream_t stream) {
+cudaError_t launch_qt(const CUtensorMap (&maps)[7], const TreeParams& p, cudaStream_t stream) {
   using C = UmmaCfg<D, QT>;
   static thread_local int configured_device = -1;
   int dev = 0;
@@ -707,24 +781,22 @@ cudaError_t launch_qt(const CUtensorMap (&maps)[5], const TreeParams& p, cudaStr
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
-  tree_umma_kernel<T, D, QT><<<p.ctas, kUmmaThreads, C::kSmemBytes, stream>>>(maps[4], maps[0], maps[1], maps[2],
-                                                                             maps[3], p);
+  tree_umma_kernel<T, D, QT><<<p.ctas, kUmmaThreads, C::kSmemBytes, stream>>>(maps[4], maps[0], maps[1], maps[2], maps[3],
+                                                                             maps[5], maps[6], p);
   return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_d(const CUtensorMap (&maps)[7], const TreeParams& p, cudaStream_t stream) {
+  return p.rows > 128 ? launch_qt<T, D, 2>(maps, p, stream) : launch_qt<T, D, 1>(maps, p, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_tree_umma(bool fp16, int head_dim, const CUtensorMap (&maps)[5], const TreeParams& p,
+cudaError_t launch_tree_umma(bool fp16, int head_dim, const CUtensorMap (&maps)[7], const TreeParams& p,
                              cudaStream_t stream) {
-  const bool pairs = p.rows > 128;
-  if (head_dim == 128) {
-    if (fp16) return pairs ? launch_qt<__half, 128, 2>(maps, p, stream) : launch_qt<__half, 128, 1>(maps, p, stream);
-    return pairs ? launch_qt<__nv_bfloat16, 128, 2>(maps, p, stream) : launch_qt<__nv_bfloat16, 128, 1>(maps, p, stream);
-  }
-  if (head_dim == 64) {
-    if (fp16) return pairs ? launch_qt<__half, 64, 2>(maps, p, stream) : launch_qt<__half, 64, 1>(maps, p, stream);
-    return pairs ? launch_qt<__nv_bfloat16, 64, 2>(maps, p, stream) : launch_qt<__nv_bfloat16, 64, 1>(maps, p, stream);
-  }
+  if (head_dim == 128) return fp16 ? launch_d<__half, 128>(maps, p, stream) : launch_d<__nv_bfloat16, 128>(maps, p, stream);
+  if (head_dim == 64) return fp16 ? launch_d<__half, 64>(maps, p, stream) : launch_d<__nv_bfloat16, 64>(maps, p, stream);
   return cudaErrorInvalidValue;
 }
 
