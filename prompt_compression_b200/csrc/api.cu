@@ -5,6 +5,7 @@
 // caller's stream.  No allocation, no host synchronisation on the compute
 // paths.
 #include <atomic>
+#include <chrono>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -822,6 +823,14 @@ static spk_status make_map16(CUtensorMap* map, bool fp16, const void* base, int 
   return SPK_OK;
 }
 
+// A number for each call of the process, from a start that another process's
+// left-over memory does not hold either.
+static unsigned long long next_call() {
+  static std::atomic<unsigned long long> n{static_cast<unsigned long long>(
+      std::chrono::system_clock::now().time_since_epoch().count()) * 0x9E3779B97F4A7C15ull >> 16};
+  return n.fetch_add(1, std::memory_order_relaxed) & 0xffffffffffffull;
+}
+
 size_t tree_attention_workspace_size(const spk_tree_shape* s) {
   if (check_tree(s) != SPK_OK) return 0;
   return round_up(tree_ws_bytes(tree_plan(s->hq / s->hkv * s->n_nodes, s->head_dim, num_sms()), s->head_dim), 256);
@@ -862,8 +871,12 @@ spk_status tree_attention(const spk_tree_shape* s, const void* q, const void* k_
   p.node_rows = s->n_nodes >= plan.keys ? plan.keys : (s->n_nodes + 7) / 8 * 8;
   p.c2 = s->scale * 1.4426950408889634f;
   p.ctas = plan.ctas;
+  p.sms = num_sms();
+  p.join_inside = static_cast<long long>(s->batch) * s->layers * s->hkv * plan.items >= 2LL * plan.ctas;
   p.part_o = static_cast<float*>(ws);
   p.part_ml = p.part_o + static_cast<size_t>(plan.ctas) * 2 * plan.item_rows * s->head_dim;
+  p.arrived = reinterpret_cast<unsigned long long*>(p.part_ml + static_cast<size_t>(plan.ctas) * 2 * plan.item_rows * 2);
+  p.call = next_call();
   const bool fp16 = s->dtype == SPK_FP16;
   const long long pool = static_cast<long long>(s->layers) * s->n_pages * s->hkv;
   const long long units = static_cast<long long>(s->batch) * s->layers * s->hkv;

@@ -70,8 +70,12 @@ struct TreeParams {
   int node_rows;           // rows of one copy of nodes: min(T, key tile), a multiple of 8
   float c2;                // scale * log2(e)
   int ctas;                // CTAs of the main kernel
-  float* part_o;           // [ctas * 2][rows of an item][d] partial outputs
+  int sms;
+  bool join_inside;        // the main kernel joins the items that several shares hold
+  float* part_o;           // [ctas * 2][d / 4][rows of an item][4] partial outputs
   float* part_ml;          // [ctas * 2][rows of an item][2] their row maxima and sums
+  unsigned long long* arrived;   // [ctas] how many shares of a cut item are in, with the call's number
+  unsigned long long call; // the call's number (48 bits)
 };
 
 struct TreePlan {
@@ -80,7 +84,7 @@ struct TreePlan {
   int tile_rows, row_tiles;
   int item_rows;           // query rows of an item
   int items;               // items per unit
-  int sms, ctas;
+  int ctas;
 };
 TreePlan tree_plan(int rows, int head_dim, int sms);
 size_t tree_ws_bytes(const TreePlan& plan, int head_dim);

@@ -9,9 +9,13 @@
 // This kernel has the units of few query rows (row tiles of 8 to 64, on
 // mma.sync); tree_umma.cu has the others.  How the work is shared out:
 // tree_shares.cuh.  An item inside one share is finished there; the others
-// leave (m, sum, unnormalised output) of each share in the workspace, and
-// tree_join_kernel adds them in the order of the shares: the results do not
-// depend on timing.
+// leave (m, sum, unnormalised output) of each share in the workspace, to be
+// added in the order of the shares, so that the results do not depend on
+// timing.  Where there are at least twice as many items as CTAs (an item is
+// then in two shares at most) the share that arrives last does it; otherwise
+// tree_join_kernel, which spreads the many shares of an item over the GPU.
+// (16 nodes over 320 rows, 512 KV heads: 33 us the one way, 37 the other; one
+// node over 16K rows, 8 KV heads in 37 shares each: 37 and 22 us.)
 #include <type_traits>
 
 #include "common.cuh"
@@ -79,7 +83,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages];
   __shared__ TreeStart start_s;
   __shared__ __align__(16) float wmax[kWarps][C::kRows];   // read and written in pairs
-  __shared__ int abort_flag;
+  __shared__ int abort_flag, last_s;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -99,8 +103,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     tma_prefetch_map(&vmap);
   }
   __syncthreads();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   volatile int* const abort_v = &abort_flag;
+  if (!p.join_inside) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   TreeWalker<kTreeKeys, false> walk(start_s);
   TreeRun run;
 
@@ -356,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           l[n][1] += y.y;
         }
       }
-      if (run.t0 == 0 && run.t1 == run.e.tiles) {
+      if (run.from == run.to) {
         // the whole unit: outputs through shared memory (over Q), 16 bytes a store
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -401,6 +405,43 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             if (warp == 0 && gr == 0)
               *reinterpret_cast<float2*>(p.part_ml + (part * C::kRows + row) * 2) = make_float2(m[n][c], l[n][c]);
+          }
+        }
+        // the last of the item's shares joins them:
+        //   M = max m_c,  out = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c
+        bool join = false;
+        if (p.join_inside) {
+          __threadfence();
+          consumers_sync();
+          if (threadIdx.x == 0) last_s = tree_arrive(p, run);
+          consumers_sync();
+          join = last_s;
+        }
+        if (join) {
+#pragma unroll 1
+          for (int y = threadIdx.x; y < C::kRows * (D / 4); y += kWarps * 32) {
+            const int row = y % C::kRows, col4 = y / C::kRows, r = run.row0 + row;
+            if (r >= p.rows || r % p.T >= run.e.live) continue;
+            const float2* const ml = reinterpret_cast<const float2*>(p.part_ml) + row;
+            const float4* const po = reinterpret_cast<const float4*>(p.part_o) + static_cast<size_t>(col4) * C::kRows + row;
+            float M = -INFINITY, L = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int c = run.from; c <= run.to; ++c) {
+              const size_t at = tree_place(run, c);
+              const float2 s = __ldcg(ml + at * C::kRows);
+              const float4 o = __ldcg(po + at * (D / 4) * C::kRows);
+              const float mx = fmaxf(M, s.x), ref = mx == -INFINITY ? 0.f : mx;
+              const float f0 = ex2_approx(M - ref), f = ex2_approx(s.x - ref);
+              M = mx;
+              L = fmaf(s.y, f, L * f0);
+              acc = make_float4(fmaf(o.x, f, acc.x * f0), fmaf(o.y, f, acc.y * f0), fmaf(o.z, f, acc.z * f0),
+                                fmaf(o.w, f, acc.w * f0));
+            }
+            const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+            const size_t at = static_cast<size_t>(run.unit) * p.rows + r;
+            reinterpret_cast<uint2*>(p.out)[at * (D / 4) + col4] =
+                make_uint2(Half16<T>::pack(acc.x * inv, acc.y * inv), Half16<T>::pack(acc.z * inv, acc.w * inv));
+            if (col4 == 0 && p.lse2 != nullptr) p.lse2[at] = L == 0.f ? -INFINITY : M + lg2_approx(L);
           }
         }
       }
@@ -527,7 +568,7 @@ cudaError_t launch_join(const TreeParams& p, const TreePlan& plan, cudaStream_t 
   cudaLaunchConfig_t cfg = {};
   // blocks that are resident together, beside the main kernel's: six an SM
   const unsigned x = by_border ? plan.ctas - 1 : static_cast<unsigned>(items);
-  const unsigned most = ((many ? 1u : 6u) * plan.sms + x - 1) / x, want = (rows + kJoinRows - 1) / kJoinRows;
+  const unsigned most = ((many ? 1u : 6u) * p.sms + x - 1) / x, want = (rows + kJoinRows - 1) / kJoinRows;
   cfg.gridDim = dim3(x, want < most ? want : most);
   cfg.blockDim = dim3(kJoinRows * (D / 4) * (many ? kJoinGroups : 1));
   cfg.stream = stream;
@@ -558,17 +599,18 @@ cudaError_t launch_nt(const CUtensorMap (&maps)[7], const TreeParams& p, const T
 
 template <typename T, int D>
 cudaError_t launch_d(const CUtensorMap (&maps)[7], const TreeParams& p, const TreePlan& plan, cudaStream_t stream) {
-  if (plan.wide) {
-    cudaError_t e = launch_tree_umma(std::is_same<T, __half>::value, D, maps, p, stream);
-    return e != cudaSuccess ? e : launch_join<T, D, 128, true>(p, plan, stream);
-  }
   cudaError_t e;
-  switch (plan.tile_rows) {
-    case 8: e = launch_nt<T, D, 1>(maps, p, plan, stream); break;
-    case 16: e = launch_nt<T, D, 2>(maps, p, plan, stream); break;
-    default: e = launch_nt<T, D, 4>(maps, p, plan, stream); break;
+  if (plan.wide) {
+    e = launch_tree_umma(std::is_same<T, __half>::value, D, maps, p, stream);
+  } else {
+    switch (plan.tile_rows) {
+      case 8: e = launch_nt<T, D, 1>(maps, p, plan, stream); break;
+      case 16: e = launch_nt<T, D, 2>(maps, p, plan, stream); break;
+      default: e = launch_nt<T, D, 4>(maps, p, plan, stream); break;
+    }
   }
-  return e != cudaSuccess ? e : launch_join<T, D, kTreeKeys, false>(p, plan, stream);
+  if (e != cudaSuccess || p.join_inside) return e;
+  return plan.wide ? launch_join<T, D, 128, true>(p, plan, stream) : launch_join<T, D, kTreeKeys, false>(p, plan, stream);
 }
 
 // --------------------------------------------------------------------------
@@ -632,13 +674,12 @@ TreePlan tree_plan(int rows, int head_dim, int sms) {
   plan.row_tiles = (rows + plan.tile_rows - 1) / plan.tile_rows;
   plan.item_rows = plan.wide && rows > 128 ? 256 : plan.tile_rows;
   plan.items = (rows + plan.item_rows - 1) / plan.item_rows;
-  plan.sms = sms;
   plan.ctas = plan.wide ? sms : 2 * sms;
   return plan;
 }
 
 size_t tree_ws_bytes(const TreePlan& plan, int head_dim) {
-  return static_cast<size_t>(plan.ctas) * 2 * plan.item_rows * (head_dim + 2) * sizeof(float);
+  return static_cast<size_t>(plan.ctas) * (2 * plan.item_rows * (head_dim + 2) * sizeof(float) + sizeof(long long));
 }
 
 cudaError_t launch_tree_attention(bool fp16, int head_dim, const CUtensorMap (&maps)[7], const TreeParams& p,

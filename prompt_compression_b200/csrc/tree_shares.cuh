@@ -7,7 +7,7 @@
 // (batch element, layer, KV head, rows, key tile), form one line of jobs, and
 // CTA c takes the jobs [c * share, (c + 1) * share): ragged lengths balance,
 // and a few long sequences still fill the GPU.  The line follows from seq_lens
-// on the device; kernel and join compute it alike.
+// on the device.
 //   narrow kernel (PAIRS false): an item is one row tile, a job one key tile
 //   wide kernel (PAIRS true):    row tiles of 128, two to an item while there
 //     are two left (a job is then one (row tile, key tile); a border between
@@ -125,7 +125,8 @@ __device__ __forceinline__ TreeStart tree_start(const TreeParams& p, int cta, bo
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) jobs += __shfl_xor_sync(0xffffffffu, jobs, o);
   s.total = jobs;
-  s.share = max(1, (s.total + p.ctas - 1) / p.ctas);
+  // (two jobs at least where items are pairs: no share inside an item is then without a tile)
+  s.share = max(p.row_tiles > 1 ? 2 : 1, (s.total + p.ctas - 1) / p.ctas);
   // whole units where that costs few jobs more: no unit is then cut and joined
   const int unit = p.row_tiles * __shfl_sync(0xffffffffu, first.tiles, 0);
   bool same = unit > 0;
@@ -213,6 +214,8 @@ __device__ __forceinline__ void tree_part(const TreeItem& i, int tiles, int begi
 struct TreeRun {           // a part of an item that a CTA works on
   int b, unit, row0, t0, t1, slot;
   int pool;                // (layer * n_pages) * hkv + KV head: the unit of page 0 in the pages' maps
+  int c0, slot0;           // the share in which the item begins, and its slot there
+  int from, to;            // the shares that hold some of its tiles (equal: the run is the whole item)
   bool pair;
   TreeElement e;
   __device__ __forceinline__ int jobs() const { return (t1 - t0) * (pair ? 2 : 1); }
@@ -220,10 +223,10 @@ struct TreeRun {           // a part of an item that a CTA works on
 
 template <int KEYS, bool PAIRS>
 struct TreeWalker {
-  int begin, end, x, b, base;
+  int begin, end, x, b, base, share;
   TreeElement e;
   __device__ __forceinline__ explicit TreeWalker(const TreeStart& s)
-      : begin(s.begin), end(s.end), x(s.begin), b(s.b), base(s.base), e(s.e) {}
+      : begin(s.begin), end(s.end), x(s.begin), b(s.b), base(s.base), share(s.share), e(s.e) {}
   __device__ __forceinline__ bool next(const TreeParams& p, TreeRun& r) {
     while (x < end) {
       int jobs = tree_jobs(p, e);
@@ -242,10 +245,50 @@ struct TreeWalker {
       r.pool = layer * p.n_pages * p.hkv + lh - layer * p.hkv;
       r.e = e;
       x = min(end, i.first + i.jobs);
-      if (r.t0 < r.t1) return true;
+      if (r.t0 >= r.t1) continue;
+      if (r.t0 == 0 && r.t1 == e.tiles) {
+        r.c0 = r.slot0 = r.from = r.to = 0;
+      } else {
+        r.c0 = r.from = i.first / share;
+        r.to = (i.first + i.jobs - 1) / share;
+        int t0, t1, slot;
+        tree_part(i, e.tiles, r.c0 * share, (r.c0 + 1) * share, t0, t1, r.slot0);
+        if (t0 == t1) ++r.from;                  // (a pair's border inside its first tile)
+        tree_part(i, e.tiles, r.to * share, (r.to + 1) * share, t0, t1, slot);
+        if (t0 == t1) --r.to;
+      }
+      return true;
     }
     return false;
   }
 };
+
+// Where the partial results of share c of an item lie.
+__device__ __forceinline__ size_t tree_place(const TreeRun& r, int c) {
+  return static_cast<size_t>(c) * 2 + (c == r.c0 ? r.slot0 : 0);
+}
+
+// One more share of a cut item has left its results; true for the last one,
+// which joins them.  A word holds the call's number and a count; a word with
+// another number counts as 0, so the workspace needs no clearing, and the last
+// arrival leaves 0, so that a captured call can be replayed.  Which share is
+// the last does not change a result: the shares are added in their order.
+__device__ __forceinline__ bool tree_arrive(const TreeParams& p, const TreeRun& r) {
+  unsigned long long* const word = p.arrived + r.c0;
+  const unsigned long long call = p.call << 16;
+  const int parts = r.to - r.from + 1;
+  __threadfence();
+  unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(word);
+  while (true) {
+    const unsigned long long count = (old & ~0xffffull) == call ? old & 0xffffull : 0;
+    const bool last = static_cast<int>(count) + 1 == parts;
+    const unsigned long long seen = atomicCAS(word, old, call | (last ? 0ull : count + 1));
+    if (seen == old) {
+      __threadfence();
+      return last;
+    }
+    old = seen;
+  }
+}
 
 }  // namespace spk

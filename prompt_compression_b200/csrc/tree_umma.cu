@@ -84,11 +84,11 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatil
 template <int SLOTS>
 struct UmmaShared {
   uint64_t q_full, q_empty, full[SLOTS], empty[SLOTS], s_full[2], p_half[2], p_full[2], run_done, o_empty, ml_ready,
-      run_full[kRunSlots], run_empty[kRunSlots];
+      parts_in, joined, run_full[kRunSlots], run_empty[kRunSlots];
   TreeRun run[kRunSlots];
   float2 ml[2][128];          // both groups' row states, for the other
   uint32_t tmem_holder;
-  int abort_flag;
+  int abort_flag, last;
 };
 
 // QT query tiles of a unit share the K/V tiles (1: no unit has more than 128
@@ -246,6 +246,8 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     mbar_init(&sh.run_done, 1);
     mbar_init(&sh.o_empty, 2 * kGroupWarps);
     mbar_init(&sh.ml_ready, 2 * kGroupWarps);
+    mbar_init(&sh.parts_in, 2 * kGroupWarps);
+    mbar_init(&sh.joined, 1);
     for (int s = 0; s < kRunSlots; ++s) {
       mbar_init(&sh.run_full[s], 1);
       mbar_init(&sh.run_empty[s], kRunReaders);
@@ -267,7 +269,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!p.join_inside) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // (all 512 columns: the allocation begins at column 0)
   const uint32_t tmem = 0;
   volatile int* const abort_v = &sh.abort_flag;
@@ -518,7 +520,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     const uint32_t mine = lanes + x * 256;                     // S; O at + 128
     bool ok = true;
     uint32_t job = 0, base = 0;                                // jobs of this group, K/V tiles, before the run
-    int runs = 0, alone_runs = 0;
+    int runs = 0, alone_runs = 0, cut_runs = 0;
     auto wait_all = [&](uint64_t* bar, uint32_t parity, int which) -> bool {
       return __all_sync(0xffffffffu, bar_wait(bar, parity, abort_v, umma_site(2 + x, which)));
     };
@@ -688,7 +690,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         l = s0.y * f0 + s1.y * f1;
         m = M;
       }
-      const bool whole = run.t0 == 0 && run.t1 == run.e.tiles;
+      const bool whole = run.from == run.to;
       const bool live = there && node < run.e.live;
       const float scale = whole ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f;
       f0 *= scale;
@@ -700,6 +702,23 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       const int part_row = (pair ? x * 128 : 0) + r;
       const int c_end = alone ? (x + 1) * (D / 2) : D;
       const uint32_t lives = __ballot_sync(0xffffffffu, live);
+      // 32 columns of the rows, 8 (16 bytes) to a vector: four lanes exchange vectors
+      // so that each store covers 64 bytes of eight rows
+      auto store32 = [&](const uint32_t (&o)[32], int c) {
+        uint4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          v[k].x = Half16<T>::pack(__uint_as_float(o[8 * k + 0]), __uint_as_float(o[8 * k + 1]));
+          v[k].y = Half16<T>::pack(__uint_as_float(o[8 * k + 2]), __uint_as_float(o[8 * k + 3]));
+          v[k].z = Half16<T>::pack(__uint_as_float(o[8 * k + 4]), __uint_as_float(o[8 * k + 5]));
+          v[k].w = Half16<T>::pack(__uint_as_float(o[8 * k + 6]), __uint_as_float(o[8 * k + 7]));
+        }
+        transpose4(v, lane);
+        T* const dst = static_cast<T*>(p.out) + (static_cast<size_t>(run.unit) * p.rows + row - (lane & 3)) * D + c + (lane & 3) * 8;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)                            // of row (lane & ~3) + k
+          if ((lives >> ((lane & ~3) + k)) & 1u) *reinterpret_cast<uint4*>(dst + k * D) = v[k];
+      };
       if (lives != 0) {
 #pragma unroll 1
         for (int c = alone ? x * (D / 2) : 0; c < c_end; c += 32) {
@@ -720,22 +739,8 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
 #pragma unroll
             for (int k = 0; k < 32; ++k) o[k] = 0u;
           }
-          if (whole) {
-            // 32 columns a row, 8 (16 bytes) to a vector: four lanes exchange vectors so
-            // that each store covers 64 bytes of eight rows
-            uint4 v[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              v[k].x = Half16<T>::pack(__uint_as_float(o[8 * k + 0]), __uint_as_float(o[8 * k + 1]));
-              v[k].y = Half16<T>::pack(__uint_as_float(o[8 * k + 2]), __uint_as_float(o[8 * k + 3]));
-              v[k].z = Half16<T>::pack(__uint_as_float(o[8 * k + 4]), __uint_as_float(o[8 * k + 5]));
-              v[k].w = Half16<T>::pack(__uint_as_float(o[8 * k + 6]), __uint_as_float(o[8 * k + 7]));
-            }
-            transpose4(v, lane);
-            T* const dst = static_cast<T*>(p.out) + (static_cast<size_t>(run.unit) * p.rows + row - (lane & 3)) * D + c + (lane & 3) * 8;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)                        // of row (lane & ~3) + k
-              if ((lives >> ((lane & ~3) + k)) & 1u) *reinterpret_cast<uint4*>(dst + k * D) = v[k];
+            if (whole) {
+            store32(o, c);
           } else if (live) {
             // partial results lie [4 columns][row]: a store covers 32 rows together
             float4* const dst = reinterpret_cast<float4*>(p.part_o) + (place * (D / 4) + c / 4) * p.item_rows + part_row;
@@ -755,6 +760,64 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.o_empty);
+      if (!whole && p.join_inside) {
+        // The last of the item's shares joins them (the products of the next run go
+        // on meanwhile): M = max m_c, out = sum 2^(m_c - M) o_c / sum 2^(m_c - M) l_c
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.parts_in);
+        if (threadIdx.x == 0) {
+          ok = bar_wait(&sh.parts_in, cut_runs & 1, abort_v, umma_site(2, 4));
+          sh.last = ok && tree_arrive(p, run);
+          mbar_arrive(&sh.joined);
+        }
+        __syncwarp();
+        if (!(ok = wait_all(&sh.joined, cut_runs & 1, 5))) break;
+        ++cut_runs;
+        if (sh.last && lives != 0) {
+          const float2* const ml = reinterpret_cast<const float2*>(p.part_ml) + part_row;
+          float M = -INFINITY, L = 0.f;
+          for (int k = run.from; k <= run.to; ++k) M = fmaxf(M, live ? __ldcg(ml + tree_place(run, k) * p.item_rows).x : 0.f);
+          const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll 1
+          for (int c = alone ? x * (D / 2) : 0; c < c_end; c += 32) {
+            float a[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) a[k] = 0.f;
+            L = 0.f;
+#pragma unroll 2
+            for (int q = run.from; q <= run.to; ++q) {
+              const size_t at = tree_place(run, q);
+              float2 s = make_float2(-INFINITY, 0.f);
+              float4 o[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (live) {
+                s = __ldcg(ml + at * p.item_rows);
+                const float4* const src = reinterpret_cast<const float4*>(p.part_o) + (at * (D / 4) + c / 4) * p.item_rows + part_row;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) o[k] = __ldcg(src + k * p.item_rows);
+              }
+              const float f = ex2_approx(s.x - ref);
+              L = fmaf(s.y, f, L);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                a[4 * k] = fmaf(o[k].x, f, a[4 * k]);
+                a[4 * k + 1] = fmaf(o[k].y, f, a[4 * k + 1]);
+                a[4 * k + 2] = fmaf(o[k].z, f, a[4 * k + 2]);
+                a[4 * k + 3] = fmaf(o[k].w, f, a[4 * k + 3]);
+              }
+            }
+            const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+            uint32_t o[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(a[k] * inv);
+            store32(o, c);
+          }
+          if (live && (!alone || x == 0) && p.lse2 != nullptr)
+            p.lse2[static_cast<size_t>(run.unit) * p.rows + row] = L == 0.f ? -INFINITY : M + lg2_approx(L);
+        }
+      }
       base += tiles;
       ++runs;
     }
