@@ -10,7 +10,6 @@ only when none is given, and then on the stream the kernels run on.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -533,59 +532,53 @@ def _launch(index: int, stream, fn, *args):
 def _new(shape, dtype, index: int, stream) -> torch.Tensor:
     """An output of a call on `stream`: allocated there, and known to the
     caller's stream too, so that its memory is not given away while either uses it."""
-    dev = torch.device("cuda", index)
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=index)
+    dev = torch.device("cuda", index)
     with torch.cuda.stream(_stream_object(stream, dev)):
         t = torch.empty(shape, dtype=dtype, device=dev)
     t.record_stream(torch.cuda.current_stream(dev))
     return t
 
 
-def _scratch(ws: Optional[torch.Tensor], nbytes: int, index: int, stream) -> torch.Tensor:
-    """The caller's workspace, or a temporary one on the launch stream."""
+def _scratch(ws: Optional[torch.Tensor], nbytes: int, index: int, stream):
+    """(pointer, bytes) of the caller's workspace, or of a temporary one on the
+    launch stream, and the tensor that holds it."""
     if ws is not None:
-        return ws
-    dev = torch.device("cuda", index)
+        return _ptr(ws, "workspace", None, index), ws.numel() * ws.element_size(), ws
     if stream is None:
-        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
-    return _workspace(None, nbytes, dev, stream)
+        ws = torch.empty(nbytes or 256, dtype=torch.uint8, device=index)
+    else:
+        ws = _workspace(None, nbytes, torch.device("cuda", index), stream)
+    return ws.data_ptr(), nbytes or 256, ws
 
 
 def pages_shape(k_pages, v_pages, page_refs, page_table, seq_lens) -> PagesShape:
-    if k_pages.dim() != 5 or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype:
+    if k_pages.dim() != 5 or k_pages.shape != v_pages.shape or k_pages.dtype is not v_pages.dtype:
         raise ValueError("k_pages and v_pages are [L, n_pages, Hkv, page_rows, d], of the same dtype")
     L, n_pages, hkv, rows, d = k_pages.shape
-    return _table_shape(page_refs, page_table, seq_lens, rows, (L, hkv, d, k_pages.element_size()), n_pages)
+    if page_refs.numel() != n_pages:
+        raise ValueError(f"page_refs has {page_refs.numel()} elements, the call needs {n_pages}")
+    return _table_shape(page_refs, page_table, seq_lens, rows, L, hkv, d, k_pages.element_size())
 
 
-def _table_shape(page_refs, page_table, seq_lens, page_rows, lhde=(1, 1, 16, 1), n_pages=None) -> PagesShape:
+def _table_shape(page_refs, page_table, seq_lens, page_rows, layers=1, hkv=1, d=16, elem_bytes=1) -> PagesShape:
     if page_table.dim() != 2:
         raise ValueError("page_table is [n_seqs, max_pages]")
     n_seqs, max_pages = page_table.shape
-    if n_pages is None:
-        n_pages = page_refs.numel()
-    if page_refs.numel() != n_pages:
-        raise ValueError(f"page_refs has {page_refs.numel()} elements, the call needs {n_pages}")
     if seq_lens.numel() != n_seqs:
         raise ValueError(f"seq_lens has {seq_lens.numel()} elements, the call needs {n_seqs}")
-    return PagesShape(lhde[0], n_pages, lhde[1], int(page_rows), lhde[2], lhde[3], n_seqs, max_pages)
+    return PagesShape(layers, page_refs.numel(), hkv, int(page_rows), d, elem_bytes, n_seqs, max_pages)
 
 
 def kv_pages_workspace_size(shape: PagesShape, n: int) -> int:
-    return int(load_library().kv_pages_workspace_size(ctypes.byref(shape), n))
+    return load_library().kv_pages_workspace_size(ctypes.byref(shape), n)
 
 
-def _book(page_refs, page_table, seq_lens, dev):
+def _book(page_refs, page_table, seq_lens, index):
     i32 = torch.int32
-    return (_ptr(page_refs, "page_refs", i32, dev), _ptr(page_table, "page_table", i32, dev),
-            _ptr(seq_lens, "seq_lens", i32, dev))
-
-
-def _result(result, dev, stream):
-    if result is None:
-        result = _new((1,), torch.int32, dev, stream)
-    return result, _ptr(result, "result", torch.int32, dev, 1)
+    return (_ptr(page_refs, "page_refs", i32, index), _ptr(page_table, "page_table", i32, index),
+            _ptr(seq_lens, "seq_lens", i32, index))
 
 
 def kv_pages_reserve(k_pages, v_pages, page_refs, page_table, seq_lens, seqs, n_new, result=None, workspace=None,
@@ -595,15 +588,17 @@ def kv_pages_reserve(k_pages, v_pages, page_refs, page_table, seq_lens, seqs, n_
     sequences hold too.  Returns result int32 [1] (on the device): 0 done, > 0
     that many pages were missing, -1 a wrong argument; nothing changed unless 0."""
     lib = load_library()
-    dev = _device_index(k_pages, "k_pages")
-    shape = pages_shape(k_pages, v_pages, page_refs, page_table, seq_lens)
-    n = seqs.numel()
-    result, res = _result(result, dev, stream)
-    ws = _scratch(workspace, kv_pages_workspace_size(shape, n), dev, stream)
-    _launch(dev, stream, lib.kv_pages_reserve, ctypes.byref(shape), _ptr(k_pages, "k_pages", None, dev),
-            _ptr(v_pages, "v_pages", None, dev), *_book(page_refs, page_table, seq_lens, dev),
-            _ptr(seqs, "seqs", torch.int32, dev), _ptr(n_new, "n_new", torch.int32, dev, n), n, res,
-            _ptr(ws, "workspace", None, dev), ws.numel() * ws.element_size())
+    index = _device_index(k_pages, "k_pages")
+    shape = ctypes.byref(pages_shape(k_pages, v_pages, page_refs, page_table, seq_lens))
+    n, i32 = seqs.numel(), torch.int32
+    if result is None:
+        result = _new((1,), i32, index, stream)
+    ws, ws_bytes, _hold = _scratch(workspace, 0 if workspace is not None else lib.kv_pages_workspace_size(shape, n),
+                                   index, stream)
+    _launch(index, stream, lib.kv_pages_reserve, shape, _ptr(k_pages, "k_pages", None, index),
+            _ptr(v_pages, "v_pages", None, index), *_book(page_refs, page_table, seq_lens, index),
+            _ptr(seqs, "seqs", i32, index), _ptr(n_new, "n_new", i32, index, n), n,
+            _ptr(result, "result", i32, index, 1), ws, ws_bytes)
     return result
 
 
@@ -613,23 +608,25 @@ def kv_pages_write(k, v, k_pages, v_pages, page_refs, page_table, seq_lens, seqs
     the rows idx int32 [n * L * Hkv / units_per_idx, n_idx] selects (None: all),
     of which the first counts int32 [n] are written (None: all)."""
     lib = load_library()
-    dev = _device_index(k_pages, "k_pages")
+    index = _device_index(k_pages, "k_pages")
     shape = pages_shape(k_pages, v_pages, page_refs, page_table, seq_lens)
-    n = seqs.numel()
-    if k.dim() != 5 or k.shape != v.shape or tuple(k.shape[:3]) != (n, shape.layers, shape.hkv) \
-            or k.shape[4] != shape.head_dim:
+    n, i32 = seqs.numel(), torch.int32
+    if k.dim() != 5 or k.shape != v.shape:
+        raise ValueError("k and v are [n, L, Hkv, n_src, d]")
+    kn, kl, kh, n_src, kd = k.shape
+    if kn != n or kl != shape.layers or kh != shape.hkv or kd != shape.head_dim:
         raise ValueError("k and v are [n, L, Hkv, n_src, d] with the pages' L, Hkv and d")
-    if k.dtype != k_pages.dtype or v.dtype != k_pages.dtype:
+    if k.dtype is not k_pages.dtype or v.dtype is not k_pages.dtype:
         raise ValueError(f"k and v must be {k_pages.dtype} like the pages")
-    n_src, units = k.shape[3], n * shape.layers * shape.hkv
+    units = n * kl * kh
     n_idx = n_src if idx is None else idx.shape[-1]
     if units_per_idx < 1 or units % units_per_idx:
         raise ValueError(f"units ({units}) must be a multiple of units_per_idx ({units_per_idx})")
-    _launch(dev, stream, lib.kv_pages_write, ctypes.byref(shape), _ptr(k, "k", None, dev), _ptr(v, "v", None, dev),
-            n_src, _ptr(idx, "idx", torch.int32, dev, units // units_per_idx * n_idx), n_idx, units_per_idx,
-            _ptr(counts, "counts", torch.int32, dev, n), *_book(page_refs, page_table, seq_lens, dev),
-            _ptr(seqs, "seqs", torch.int32, dev), n, _ptr(k_pages, "k_pages", None, dev),
-            _ptr(v_pages, "v_pages", None, dev))
+    _launch(index, stream, lib.kv_pages_write, ctypes.byref(shape), _ptr(k, "k", None, index), _ptr(v, "v", None, index),
+            n_src, _ptr(idx, "idx", i32, index, units // units_per_idx * n_idx), n_idx, units_per_idx,
+            _ptr(counts, "counts", i32, index, n), *_book(page_refs, page_table, seq_lens, index),
+            _ptr(seqs, "seqs", i32, index), n, _ptr(k_pages, "k_pages", None, index),
+            _ptr(v_pages, "v_pages", None, index))
 
 
 def kv_pages_compact(k_pages, v_pages, page_refs, page_table, seq_lens, src, dst, idx, units_per_idx: int = 1,
@@ -638,19 +635,22 @@ def kv_pages_compact(k_pages, v_pages, page_refs, page_table, seq_lens, src, dst
     units_per_idx, n_idx] of sequences src int32 [n], in pages of their own
     (dst = src: in place).  Returns result as kv_pages_reserve does."""
     lib = load_library()
-    dev = _device_index(k_pages, "k_pages")
+    index = _device_index(k_pages, "k_pages")
     shape = pages_shape(k_pages, v_pages, page_refs, page_table, seq_lens)
-    n, n_idx = src.numel(), idx.shape[-1]
+    n, n_idx, i32 = src.numel(), idx.shape[-1], torch.int32
     units = n * shape.layers * shape.hkv
     if units_per_idx < 1 or units % units_per_idx:
         raise ValueError(f"units ({units}) must be a multiple of units_per_idx ({units_per_idx})")
-    result, res = _result(result, dev, stream)
-    ws = _scratch(workspace, kv_pages_workspace_size(shape, n), dev, stream)
-    _launch(dev, stream, lib.kv_pages_compact, ctypes.byref(shape), _ptr(k_pages, "k_pages", None, dev),
-            _ptr(v_pages, "v_pages", None, dev), *_book(page_refs, page_table, seq_lens, dev),
-            _ptr(src, "src", torch.int32, dev), _ptr(dst, "dst", torch.int32, dev, n), n,
-            _ptr(idx, "idx", torch.int32, dev, units // units_per_idx * n_idx), n_idx, units_per_idx, res,
-            _ptr(ws, "workspace", None, dev), ws.numel() * ws.element_size())
+    if result is None:
+        result = _new((1,), i32, index, stream)
+    shape = ctypes.byref(shape)
+    ws, ws_bytes, _hold = _scratch(workspace, 0 if workspace is not None else lib.kv_pages_workspace_size(shape, n),
+                                   index, stream)
+    _launch(index, stream, lib.kv_pages_compact, shape, _ptr(k_pages, "k_pages", None, index),
+            _ptr(v_pages, "v_pages", None, index), *_book(page_refs, page_table, seq_lens, index),
+            _ptr(src, "src", i32, index), _ptr(dst, "dst", i32, index, n), n,
+            _ptr(idx, "idx", i32, index, units // units_per_idx * n_idx), n_idx, units_per_idx,
+            _ptr(result, "result", i32, index, 1), ws, ws_bytes)
     return result
 
 
@@ -660,15 +660,16 @@ def kv_pages_fork(page_refs, page_table, seq_lens, src, dst, page_rows: int, n_r
     the call (their first n_rows int32 [n] rows where given), by holding their
     pages.  Returns result as kv_pages_reserve does."""
     lib = load_library()
-    dev = _device_index(page_table, "page_table")
-    shape = _table_shape(page_refs, page_table, seq_lens, page_rows)
-    n = src.numel()
-    result, res = _result(result, dev, stream)
-    ws = _scratch(workspace, kv_pages_workspace_size(shape, n), dev, stream)
-    _launch(dev, stream, lib.kv_pages_fork, ctypes.byref(shape), *_book(page_refs, page_table, seq_lens, dev),
-            _ptr(src, "src", torch.int32, dev), _ptr(dst, "dst", torch.int32, dev, n),
-            _ptr(n_rows, "n_rows", torch.int32, dev, n), n, res, _ptr(ws, "workspace", None, dev),
-            ws.numel() * ws.element_size())
+    index = _device_index(page_table, "page_table")
+    shape = ctypes.byref(_table_shape(page_refs, page_table, seq_lens, page_rows))
+    n, i32 = src.numel(), torch.int32
+    if result is None:
+        result = _new((1,), i32, index, stream)
+    ws, ws_bytes, _hold = _scratch(workspace, 0 if workspace is not None else lib.kv_pages_workspace_size(shape, n),
+                                   index, stream)
+    _launch(index, stream, lib.kv_pages_fork, shape, *_book(page_refs, page_table, seq_lens, index),
+            _ptr(src, "src", i32, index), _ptr(dst, "dst", i32, index, n), _ptr(n_rows, "n_rows", i32, index, n), n,
+            _ptr(result, "result", i32, index, 1), ws, ws_bytes)
     return result
 
 
@@ -676,18 +677,15 @@ def kv_pages_free(page_refs, page_table, seq_lens, seqs, page_rows: int, keep_ro
     """Sequences seqs int32 [n] keep their first keep_rows int32 [n] rows (None:
     none); the pages behind them are released."""
     lib = load_library()
-    dev = _device_index(page_table, "page_table")
+    index = _device_index(page_table, "page_table")
     shape = _table_shape(page_refs, page_table, seq_lens, page_rows)
-    n = seqs.numel()
-    _launch(dev, stream, lib.kv_pages_free, ctypes.byref(shape), *_book(page_refs, page_table, seq_lens, dev),
-            _ptr(seqs, "seqs", torch.int32, dev), _ptr(keep_rows, "keep_rows", torch.int32, dev, n), n)
+    n, i32 = seqs.numel(), torch.int32
+    _launch(index, stream, lib.kv_pages_free, ctypes.byref(shape), *_book(page_refs, page_table, seq_lens, index),
+            _ptr(seqs, "seqs", i32, index), _ptr(keep_rows, "keep_rows", i32, index, n), n)
 
 
 SPK_BF16, SPK_FP16 = 0, 1
 _TREE_DTYPES = {torch.bfloat16: SPK_BF16, torch.float16: SPK_FP16}
-
-
-_NO_CONTEXT = contextlib.nullcontext()
 
 
 def tree_shape(q, k_pages, page_table, scale: float = 1.0) -> TreeShape:
@@ -716,51 +714,54 @@ def tree_attention(q, k_pages, v_pages, page_table, seq_lens, k_tree=None, v_tre
     many of the tokens count (None: T).  Returns out [B, L, Hq, T, d]; fills
     lse2 fp32 [B, L, Hq, T] when given."""
     lib = load_library()
-    dev = _device_index(q, "q")
+    index = _device_index(q, "q")
     shape = tree_shape(q, k_pages, page_table, scale)
-    Bsz, L, hq, T, d = q.shape
+    Bsz, T, kind, i32 = shape.batch, shape.n_nodes, q.dtype, torch.int32
     if v_pages.shape != k_pages.shape:
         raise ValueError("v_pages must have k_pages' shape")
-    if (k_tree is None) != (v_tree is None):
-        raise ValueError("k_tree and v_tree are given together or not at all")
-    if k_tree is not None:
-        tree = (Bsz, L, shape.hkv, T, d)
-        if tuple(k_tree.shape) != tree or tuple(v_tree.shape) != tree:
+    if k_tree is None or v_tree is None:
+        if k_tree is not v_tree:
+            raise ValueError("k_tree and v_tree are given together or not at all")
+    else:
+        tree = (Bsz, shape.layers, shape.hkv, T, shape.head_dim)
+        if k_tree.shape != tree or v_tree.shape != tree:
             raise ValueError(f"k_tree and v_tree must be {list(tree)}")
     if out is None:
-        out = _new(q.shape, q.dtype, dev, stream)
-    i32 = torch.int32
-    ws = workspace
-    if ws is None:
-        with torch.cuda.device(dev) if torch.cuda.current_device() != dev else _NO_CONTEXT:
-            ws = _scratch(None, tree_attention_workspace_size(shape), dev, stream)
-    _launch(dev, stream, lib.tree_attention, ctypes.byref(shape), _ptr(q, "q", None, dev),
-            _ptr(k_pages, "k_pages", q.dtype, dev), _ptr(v_pages, "v_pages", q.dtype, dev),
-            _ptr(page_table, "page_table", i32, dev), _ptr(seq_lens, "seq_lens", i32, dev, shape.n_seqs),
-            _ptr(seqs, "seqs", i32, dev, Bsz), _ptr(k_tree, "k_tree", q.dtype, dev),
-            _ptr(v_tree, "v_tree", q.dtype, dev), _ptr(mask, "mask", i32, dev, Bsz * T * ((T + 31) // 32)),
-            _ptr(n_live, "n_live", i32, dev, Bsz), _ptr(out, "out", q.dtype, dev, q.numel()),
-            _ptr(lse2, "lse2", torch.float32, dev, Bsz * L * hq * T), _ptr(ws, "workspace", None, dev),
-            ws.numel() * ws.element_size())
+        out = _new(q.shape, kind, index, stream)
+    size = ctypes.byref(shape)
+    rows = Bsz * shape.layers * shape.hq * T
+    if workspace is not None:
+        ws, ws_bytes, _hold = _scratch(workspace, 0, index, stream)
+    elif torch.cuda.current_device() == index:
+        ws, ws_bytes, _hold = _scratch(None, lib.tree_attention_workspace_size(size), index, stream)
+    else:
+        with torch.cuda.device(index):
+            ws, ws_bytes, _hold = _scratch(None, lib.tree_attention_workspace_size(size), index, stream)
+    _launch(index, stream, lib.tree_attention, size, _ptr(q, "q", None, index),
+            _ptr(k_pages, "k_pages", kind, index), _ptr(v_pages, "v_pages", kind, index),
+            _ptr(page_table, "page_table", i32, index), _ptr(seq_lens, "seq_lens", i32, index, shape.n_seqs),
+            _ptr(seqs, "seqs", i32, index, Bsz), _ptr(k_tree, "k_tree", kind, index),
+            _ptr(v_tree, "v_tree", kind, index), _ptr(mask, "mask", i32, index, Bsz * T * ((T + 31) // 32)),
+            _ptr(n_live, "n_live", i32, index, Bsz), _ptr(out, "out", kind, index, rows * shape.head_dim),
+            _ptr(lse2, "lse2", torch.float32, index, rows), ws, ws_bytes)
     return out
 
 
 def tree_mask(parents, n_live=None, mask=None, depth=None, stream=None):
     """Visibility words int32 [B, T, ceil(T/32)] and depths int32 [B, T] of trees
     given by parents int32 [B, T] (the node before node i, in [-1, i))."""
-    lib = load_library()
     if parents.dim() != 2:
         raise ValueError("parents is [B, T]")
-    dev = _device_index(parents, "parents")
+    index = _device_index(parents, "parents")
     Bsz, T = parents.shape
-    words = (T + 31) // 32
+    words, i32 = (T + 31) // 32, torch.int32
     if mask is None:
-        mask = _new((Bsz, T, words), torch.int32, dev, stream)
+        mask = _new((Bsz, T, words), i32, index, stream)
     if depth is None:
-        depth = _new((Bsz, T), torch.int32, dev, stream)
-    i32 = torch.int32
-    _launch(dev, stream, lib.tree_mask, Bsz, T, _ptr(parents, "parents", i32, dev), _ptr(n_live, "n_live", i32, dev, Bsz),
-            _ptr(mask, "mask", i32, dev, Bsz * T * words), _ptr(depth, "depth", i32, dev, Bsz * T))
+        depth = _new((Bsz, T), i32, index, stream)
+    _launch(index, stream, load_library().tree_mask, Bsz, T, _ptr(parents, "parents", i32, index),
+            _ptr(n_live, "n_live", i32, index, Bsz), _ptr(mask, "mask", i32, index, Bsz * T * words),
+            _ptr(depth, "depth", i32, index, Bsz * T))
     return mask, depth
 
 

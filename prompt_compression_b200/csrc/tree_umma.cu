@@ -51,8 +51,8 @@ constexpr float kRescaleLog2 = 8.f;      // O and the sum are rescaled when the 
 
 __device__ __forceinline__ int umma_site(int role, int which) { return 620 + role * 10 + which; }
 
-// Bounded wait with little code: the hardware suspends the thread for up to a
-// microsecond a try.  (Items are short, so this kernel's speed hangs on how
+// Bounded wait with little code: the hardware suspends the thread for a while
+// at each try.  (Items are short, so this kernel's speed hangs on how
 // much of its code stays in the instruction cache; mbar_wait, inlined at every
 // wait, is several times as long.)
 __device__ __noinline__ bool give_up(volatile int* abort_flag, int site) {
@@ -65,13 +65,13 @@ __device__ __noinline__ bool give_up(volatile int* abort_flag, int site) {
 __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int site) {
   uint32_t ok = 0;
 #pragma unroll 1
-  for (int tries = 0; tries < 2000000; ++tries) {
+  for (int tries = 0; tries < 20000000; ++tries) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}\n"
         : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(1000)
+        : "r"(smem_u32(bar)), "r"(parity)
         : "memory");
     if (ok) return true;
     if (*abort_flag) return false;
