@@ -396,7 +396,7 @@ spk_status kv_pages_reserve(const spk_pages_shape* shape, void* k_pages, void* v
  * or the accepted nodes of a token tree (units_per_idx layers * hkv).  A row
  * whose index or position is out of range, or whose page is held by another
  * sequence too, is left unwritten and recorded as SPK_ERR_ARG in the device
- * error word; so are all rows of a sequence that stands earlier in the list. */
+ * error word; so are the rows of an entry whose sequence stands earlier in the list. */
 spk_status kv_pages_write(const spk_pages_shape* shape, const void* k, const void* v, int n_src, const int32_t* idx,
                           int n_idx, int units_per_idx, const int32_t* counts, const int32_t* page_refs,
                           const int32_t* page_table, const int32_t* seq_lens, const int32_t* seqs, int n,

@@ -709,7 +709,8 @@ spk_status kv_pages_write(const spk_pages_shape* s, const void* k, const void* v
   if (st != SPK_OK) return st;
   if (n_src < 0 || n_idx < 0) return fail(SPK_ERR_ARG, "n_src and n_idx must be >= 0");
   const long long units = static_cast<long long>(n) * s->layers * s->hkv;
-  if (units > 0x7fffffffLL) return fail(SPK_ERR_UNSUPPORTED, "n * layers * hkv is too large");
+  if (units > 0x7fffffffLL || units * ((n_idx + 63LL) / 64) > 0x7fffffffLL)
+    return fail(SPK_ERR_UNSUPPORTED, "n * layers * hkv * n_idx is too large");
   if (units_per_idx < 1 || units % units_per_idx != 0)
     return fail(SPK_ERR_ARG, "n * layers * hkv (%lld) must be a multiple of units_per_idx (%d)", units, units_per_idx);
   if (n == 0 || n_idx == 0) return ok();
@@ -733,7 +734,8 @@ spk_status kv_pages_compact(const spk_pages_shape* s, void* k_pages, void* v_pag
   if (n_idx < 0 || n_idx > static_cast<long long>(s->max_pages) * s->page_rows)
     return fail(SPK_ERR_ARG, "need 0 <= n_idx <= max_pages * page_rows");
   const long long units = static_cast<long long>(n) * s->layers * s->hkv;
-  if (units > 0x7fffffffLL) return fail(SPK_ERR_UNSUPPORTED, "n * layers * hkv is too large");
+  if (units > 0x7fffffffLL || units * ((n_idx + 63LL) / 64) > 0x7fffffffLL)
+    return fail(SPK_ERR_UNSUPPORTED, "n * layers * hkv * n_idx is too large");
   if (units_per_idx < 1 || units % units_per_idx != 0)
     return fail(SPK_ERR_ARG, "n * layers * hkv (%lld) must be a multiple of units_per_idx (%d)", units, units_per_idx);
   if (result == nullptr || (n > 0 && (src == nullptr || dst == nullptr || (n_idx > 0 && idx == nullptr))))

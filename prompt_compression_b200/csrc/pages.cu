@@ -4,11 +4,12 @@
 //
 // Bookkeeping (page table, lengths, reference counts) lives on the device and
 // every change is made there, so a decoding loop never waits for the host and
-// can be captured.  One cluster of kBookCtas CTAs makes a change (its phases
-// are ordered by cluster barriers); pages are taken lowest number first, and
-// counts change by integer additions, so the result does not depend on
-// timing.  A call that cannot be carried out (too few free pages, a bad
-// argument) leaves everything as it was and says so in *result.
+// can be captured.  One CTA makes a change, or a cluster of eight where the
+// tables are large (a cluster's barriers cost more than the loads of a small
+// table); pages are taken lowest number first, and counts change by integer
+// additions, so the result does not depend on timing.  A call that cannot be
+// carried out (too few free pages, a bad argument) leaves everything as it was
+// and says so in *result.  Latency bound: a chain of dependent loads.
 // Rows are copied as bytes, 16 at a time per thread: bound by HBM bandwidth.
 #include "common.cuh"
 #include "paged.cuh"
@@ -19,16 +20,31 @@ SPK_ERROR_READER(device_errors_pages)
 
 namespace {
 
-constexpr int kBookCtas = 8;
 constexpr int kBookThreads = 512;
-constexpr int kBookAll = kBookCtas * kBookThreads;
 constexpr int kBadCall = -1;
+
+// CTAS: 1, or the CTAs of the cluster.
+template <int CTAS>
+__device__ __forceinline__ int book_rank() {
+  return CTAS == 1 ? 0 : static_cast<int>(cluster_ctarank());
+}
+template <int CTAS>
+__device__ __forceinline__ void book_sync() {
+  if (CTAS == 1)
+    __syncthreads();
+  else
+    cluster_sync();
+}
 
 // Workspace of a call over n sequences: [n][max_pages] page numbers, then
 // [n][4] words a sequence.
 __host__ __device__ __forceinline__ int* ws_words(void* ws, int n, int max_pages) {
   return static_cast<int*>(ws) + ((static_cast<size_t>(n) * max_pages + 3) & ~size_t(3));
 }
+
+// The rows' kernel starts while the bookkeeping's runs, and waits for its end.
+__device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return a / b + (a % b != 0); }
 
@@ -69,17 +85,19 @@ __device__ __forceinline__ void warp_exclusive(int* x, int n) {
 struct FreePages {
   int all, before;
 };
+template <int CTAS>
 __device__ __forceinline__ FreePages count_free(const int* refs, int n_pages, int* scratch, int* mine_s) {
-  const int rank = cluster_ctarank();
-  const int part = ceil_div(n_pages, kBookCtas);
+  const int rank = book_rank<CTAS>();
+  const int part = ceil_div(n_pages, CTAS);
   const int lo = min(n_pages, rank * part), hi = min(n_pages, lo + part);
   int c = 0;
   for (int i = lo + threadIdx.x; i < hi; i += kBookThreads) c += refs[i] == 0;
   c = block_sum(c, scratch);
+  if (CTAS == 1) return {c, 0};
   if (threadIdx.x == 0) *mine_s = c;
   cluster_sync();
   FreePages f{0, 0};
-  for (int r = 0; r < kBookCtas; ++r) {
+  for (int r = 0; r < CTAS; ++r) {
     const int v = static_cast<int>(dsmem_ld(dsmem_addr(smem_u32(mine_s), r)));
     f.all += v;
     if (r < rank) f.before += v;
@@ -90,10 +108,10 @@ __device__ __forceinline__ FreePages count_free(const int* refs, int n_pages, in
 
 // take(rank, page) for the first `want` free pages, in ascending order: each
 // gets the count 1 and is handed out by the thread that found it.
-template <typename F>
+template <int CTAS, typename F>
 __device__ __forceinline__ void take_free(int* refs, int n_pages, int before, int want, int* scratch, F take) {
-  const int part = ceil_div(n_pages, kBookCtas);
-  const int lo = min(n_pages, static_cast<int>(cluster_ctarank()) * part), hi = min(n_pages, lo + part);
+  const int part = ceil_div(n_pages, CTAS);
+  const int lo = min(n_pages, book_rank<CTAS>() * part), hi = min(n_pages, lo + part);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int rank0 = before;
   for (int i0 = lo; i0 < hi && rank0 < want; i0 += kBookThreads) {
@@ -128,8 +146,9 @@ __device__ __forceinline__ bool bad_list(const int* list_s, int n, int n_seqs, b
   return bad;
 }
 
+template <int CTAS>
 __device__ __forceinline__ void refuse(int* result) {
-  if (cluster_ctarank() == 0 && threadIdx.x == 0) {
+  if (book_rank<CTAS>() == 0 && threadIdx.x == 0) {
     record_error(SPK_DEVERR_INDEX, 700);
     *result = kBadCall;
   }
@@ -143,9 +162,11 @@ __device__ __forceinline__ void refuse(int* result) {
 // too (its rows are copied by copy_tail_kernel, from the words left here:
 // {from, to or -1, rows}).  The sequences leave a shared page in the list's
 // order; the last holder keeps it.
-__global__ void __cluster_dims__(kBookCtas, 1, 1) __launch_bounds__(kBookThreads)
+template <int CTAS>
+__global__ void __launch_bounds__(kBookThreads)
     reserve_kernel(PagesShape s, PagesBook b, const int* __restrict__ seqs, const int* __restrict__ n_new, int n,
                    int* __restrict__ result, int* __restrict__ words) {
+  launch_next();
   __shared__ int seq_s[kPagesMaxCall], first_s[kPagesMaxCall + 1], tail_s[kPagesMaxCall];
   __shared__ int scratch[kBookThreads / 32], mine_s;
   for (int i = threadIdx.x; i < n; i += kBookThreads) seq_s[i] = seqs[i];
@@ -166,9 +187,9 @@ __global__ void __cluster_dims__(kBookCtas, 1, 1) __launch_bounds__(kBookThreads
     tail_s[i] = tail;
   }
   if (__syncthreads_or(bad)) {      // every CTA finds the same
-    refuse(result);
+    refuse<CTAS>(result);
     for (int i = threadIdx.x; i < n; i += kBookThreads)
-      if (cluster_ctarank() == 0) words[4 * i + 1] = -1;
+      if (book_rank<CTAS>() == 0) words[4 * i + 1] = -1;
     return;
   }
   for (int i = threadIdx.x; i < n; i += kBookThreads) {
@@ -192,8 +213,8 @@ __global__ void __cluster_dims__(kBookCtas, 1, 1) __launch_bounds__(kBookThreads
   if (threadIdx.x < 32) warp_exclusive(first_s, n);
   __syncthreads();
   const int want = first_s[n];
-  const FreePages f = count_free(b.refs, s.n_pages, scratch, &mine_s);   // orders the reads above before the changes
-  const bool first_cta = cluster_ctarank() == 0;
+  const FreePages f = count_free<CTAS>(b.refs, s.n_pages, scratch, &mine_s);   // orders the reads above before the changes
+  const bool first_cta = book_rank<CTAS>() == 0;
   if (f.all < want) {
     if (first_cta) {
       if (threadIdx.x == 0) *result = want - f.all;
@@ -201,7 +222,7 @@ __global__ void __cluster_dims__(kBookCtas, 1, 1) __launch_bounds__(kBookThreads
     }
     return;
   }
-  take_free(b.refs, s.n_pages, f.before, want, scratch, [&](int rank, int page) {
+  take_free<CTAS>(b.refs, s.n_pages, f.before, want, scratch, [&](int rank, int page) {
     int lo = 0, hi = n;                       // the sequence whose pages hold this rank
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
@@ -222,7 +243,7 @@ __global__ void __cluster_dims__(kBookCtas, 1, 1) __launch_bounds__(kBookThreads
     }
     row[ceil_div(len, s.page_rows) + at] = page;
   });
-  cluster_sync();                             // lens and the tails' counts have been read
+  book_sync<CTAS>();                             // lens and the tails' counts have been read
   if (!first_cta) return;
   for (int i = threadIdx.x; i < n; i += kBookThreads) {
     b.lens[seq_s[i]] += n_new[i];
@@ -238,6 +259,7 @@ __global__ void __cluster_dims__(kBookCtas, 1, 1) __launch_bounds__(kBookThreads
 // (layer, KV head) blocks y, y + gridDim.y, ... of K and V.
 __global__ void __launch_bounds__(256)
     copy_tail_kernel(PagesShape s, const int* __restrict__ words, uint4* __restrict__ k, uint4* __restrict__ v) {
+  wait_for_previous();
   const int from = words[4 * blockIdx.x], to = words[4 * blockIdx.x + 1];
   if (to < 0) return;
   const int vecs = words[4 * blockIdx.x + 2] * s.row_vecs;
@@ -260,7 +282,8 @@ __global__ void __launch_bounds__(256)
 // is null) that src[i] had before the call, by holding their pages; what
 // dst[i] held is released.  The sources' rows of the table are copied first,
 // so a sequence may be a source and a destination.
-__global__ void __cluster_dims__(kBookCtas, 1, 1) __launch_bounds__(kBookThreads)
+template <int CTAS>
+__global__ void __launch_bounds__(kBookThreads)
     fork_kernel(PagesShape s, PagesBook b, const int* __restrict__ src, const int* __restrict__ dst,
                 const int* __restrict__ n_rows, int n, int* __restrict__ result, int* __restrict__ old) {
   __shared__ int src_s[kPagesMaxCall], dst_s[kPagesMaxCall], len_s[kPagesMaxCall];
@@ -283,27 +306,27 @@ __global__ void __cluster_dims__(kBookCtas, 1, 1) __launch_bounds__(kBookThreads
     len_s[i] = len;
   }
   if (__syncthreads_or(bad)) {
-    refuse(result);
+    refuse<CTAS>(result);
     return;
   }
   const size_t cells = static_cast<size_t>(n) * s.max_pages;
-  const size_t me = static_cast<size_t>(cluster_ctarank()) * kBookThreads + threadIdx.x;
-  for (size_t x = me; x < cells; x += kBookAll) {
+  const size_t me = static_cast<size_t>(book_rank<CTAS>()) * kBookThreads + threadIdx.x;
+  for (size_t x = me; x < cells; x += CTAS * kBookThreads) {
     const int i = static_cast<int>(x / s.max_pages), at = static_cast<int>(x % s.max_pages);
     int page = at < ceil_div(len_s[i], s.page_rows) ? b.table[static_cast<size_t>(src_s[i]) * s.max_pages + at] : -1;
     if (page < 0 || page >= s.n_pages) page = -1;
     old[x] = page;
     if (page >= 0) atomicAdd(b.refs + page, 1);
   }
-  cluster_sync();
-  for (size_t x = me; x < cells; x += kBookAll) {
+  book_sync<CTAS>();
+  for (size_t x = me; x < cells; x += CTAS * kBookThreads) {
     const int i = static_cast<int>(x / s.max_pages), at = static_cast<int>(x % s.max_pages);
     int* cell = b.table + static_cast<size_t>(dst_s[i]) * s.max_pages + at;
     const int gone = *cell;
     if (gone >= 0 && gone < s.n_pages) atomicSub(b.refs + gone, 1);
     *cell = old[x];
   }
-  if (cluster_ctarank() == 0) {
+  if (book_rank<CTAS>() == 0) {
     for (int i = threadIdx.x; i < n; i += kBookThreads) b.lens[dst_s[i]] = len_s[i];
     if (threadIdx.x == 0) *result = 0;
   }
@@ -339,9 +362,11 @@ __global__ void __launch_bounds__(256)
 // a source of this call needs them (dst[i] == src[i]: compacting in place).
 // Leaves the sources' rows of the table in `old` and their lengths (or -1:
 // nothing to copy) in words[4 i].
-__global__ void __cluster_dims__(kBookCtas, 1, 1) __launch_bounds__(kBookThreads)
+template <int CTAS>
+__global__ void __launch_bounds__(kBookThreads)
     compact_book_kernel(PagesShape s, PagesBook b, const int* __restrict__ src, const int* __restrict__ dst, int n,
                         int n_idx, int* __restrict__ result, int* __restrict__ old, int* __restrict__ words) {
+  launch_next();
   __shared__ int src_s[kPagesMaxCall], dst_s[kPagesMaxCall];
   __shared__ int scratch[kBookThreads / 32], mine_s;
   for (int i = threadIdx.x; i < n; i += kBookThreads) {
@@ -350,38 +375,38 @@ __global__ void __cluster_dims__(kBookCtas, 1, 1) __launch_bounds__(kBookThreads
   }
   __syncthreads();
   bool bad = bad_list(src_s, n, s.n_seqs, false) | bad_list(dst_s, n, s.n_seqs, true);
-  const bool first_cta = cluster_ctarank() == 0;
+  const bool first_cta = book_rank<CTAS>() == 0;
   if (__syncthreads_or(bad)) {
-    refuse(result);
+    refuse<CTAS>(result);
     if (first_cta)
       for (int i = threadIdx.x; i < n; i += kBookThreads) words[4 * i] = -1;
     return;
   }
   const int per = ceil_div(n_idx, s.page_rows);
   const size_t cells = static_cast<size_t>(n) * s.max_pages;
-  const size_t me = static_cast<size_t>(cluster_ctarank()) * kBookThreads + threadIdx.x;
-  for (size_t x = me; x < cells; x += kBookAll) {      // hold the sources
+  const size_t me = static_cast<size_t>(book_rank<CTAS>()) * kBookThreads + threadIdx.x;
+  for (size_t x = me; x < cells; x += CTAS * kBookThreads) {      // hold the sources
     const int i = static_cast<int>(x / s.max_pages), at = static_cast<int>(x % s.max_pages);
     int page = b.table[static_cast<size_t>(src_s[i]) * s.max_pages + at];
     if (page < 0 || page >= s.n_pages) page = -1;
     old[x] = page;
     if (page >= 0) atomicAdd(b.refs + page, 1);
   }
-  for (size_t x = me; x < cells; x += kBookAll) {      // release the destinations
+  for (size_t x = me; x < cells; x += CTAS * kBookThreads) {      // release the destinations
     const int i = static_cast<int>(x / s.max_pages), at = static_cast<int>(x % s.max_pages);
     const int page = b.table[static_cast<size_t>(dst_s[i]) * s.max_pages + at];
     if (page >= 0 && page < s.n_pages) atomicSub(b.refs + page, 1);
   }
-  cluster_sync();
+  book_sync<CTAS>();
   const int want = n * per;
-  const FreePages f = count_free(b.refs, s.n_pages, scratch, &mine_s);
+  const FreePages f = count_free<CTAS>(b.refs, s.n_pages, scratch, &mine_s);
   const bool done = f.all >= want;
   if (done)
-    take_free(b.refs, s.n_pages, f.before, want, scratch, [&](int rank, int page) {
+    take_free<CTAS>(b.refs, s.n_pages, f.before, want, scratch, [&](int rank, int page) {
       b.table[static_cast<size_t>(dst_s[rank / per]) * s.max_pages + rank % per] = page;
     });
-  cluster_sync();
-  for (size_t x = me; x < cells; x += kBookAll) {
+  book_sync<CTAS>();
+  for (size_t x = me; x < cells; x += CTAS * kBookThreads) {
     const int i = static_cast<int>(x / s.max_pages), at = static_cast<int>(x % s.max_pages);
     if (old[x] >= 0) atomicSub(b.refs + old[x], 1);
     int* cell = b.table + static_cast<size_t>(dst_s[i]) * s.max_pages + at;
@@ -401,88 +426,165 @@ __global__ void __cluster_dims__(kBookCtas, 1, 1) __launch_bounds__(kBookThreads
   }
 }
 
-// Output row (i, l, h, t) of dst[i]'s pages from row idx[..][t] of the pages
-// that src[i] had (`old`); a thread moves 16 bytes of K and of V.
-__global__ void __launch_bounds__(256)
-    compact_rows_kernel(PagesShape s, PagesBook b, const int* __restrict__ dst, int n_idx,
-                        const int* __restrict__ idx, int units_per_idx, const int* __restrict__ old,
-                        const int* __restrict__ words, uint4* __restrict__ k, uint4* __restrict__ v, size_t total) {
-  const size_t stride = static_cast<size_t>(gridDim.x) * blockDim.x;
-  const int lh_all = s.layers * s.hkv;
-  for (size_t e = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x; e < total; e += stride) {
-    const size_t row = e / s.row_vecs;
-    const int vec = static_cast<int>(e - row * s.row_vecs);
-    const size_t u = row / n_idx;
-    const int t = static_cast<int>(row - u * n_idx);
-    const int i = static_cast<int>(u / lh_all), lh = static_cast<int>(u % lh_all);
-    const int len = words[4 * i];
-    if (len < 0) continue;
-    const int from = __ldg(idx + (u / units_per_idx) * n_idx + t);
-    const int page = from >= 0 && from < len ? old[static_cast<size_t>(i) * s.max_pages + from / s.page_rows] : -1;
-    if (page < 0) {
-      if (vec == 0) record_error(SPK_DEVERR_INDEX, static_cast<int>(u));
-      continue;
+// Rows of one unit in blocks of kCopyRows: the block finds where each row comes
+// from and goes to once (vectors, in shared memory; -1: not copied), then its
+// threads move 16 bytes of K and of V each, four of either in flight.
+// (2048 rows a unit, 128 units, 269 MB read and written: 45 us, 6.0 TB/s; with
+// the three dependent loads in front of every vector it was 60 us.)
+constexpr int kCopyRows = 64;
+
+__device__ __forceinline__ void copy_rows(const long long* from_s, const long long* to_s, int rows, int row_vecs,
+                                          const uint4* __restrict__ k, const uint4* __restrict__ v,
+                                          uint4* __restrict__ kd, uint4* __restrict__ vd) {
+  const int total = rows * row_vecs;
+  for (int e0 = threadIdx.x; e0 < total; e0 += 4 * blockDim.x) {
+    uint4 a[4], b[4];
+    long long to[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int e = e0 + u * blockDim.x;
+      to[u] = -1;
+      if (e < total) {
+        const int row = e / row_vecs, vec = e - row * row_vecs;
+        const long long from = from_s[row];
+        if (from >= 0) {
+          to[u] = to_s[row] + vec;
+          a[u] = __ldcs(k + from + vec);
+          b[u] = __ldcs(v + from + vec);
+        }
+      }
     }
-    const int to = b.table[static_cast<size_t>(dst[i]) * s.max_pages + t / s.page_rows];
-    const size_t base = static_cast<size_t>(lh / s.hkv) * s.n_pages;
-    const int h = lh % s.hkv;
-    const size_t a = (((base + page) * s.hkv + h) * s.page_rows + from % s.page_rows) * s.row_vecs + vec;
-    const size_t z = (((base + to) * s.hkv + h) * s.page_rows + t % s.page_rows) * s.row_vecs + vec;
-    k[z] = k[a];
-    v[z] = v[a];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (to[u] >= 0) {
+        kd[to[u]] = a[u];
+        vd[to[u]] = b[u];
+      }
+    }
   }
+}
+
+// Vector of the pools at which row `row` of page `page` lies, for unit lh = (layer, KV head).
+__device__ __forceinline__ long long pool_row(const PagesShape& s, int lh, int page, int row) {
+  const int l = lh / s.hkv, h = lh - l * s.hkv;
+  return (((static_cast<long long>(l) * s.n_pages + page) * s.hkv + h) * s.page_rows + row) * s.row_vecs;
+}
+
+// Block: rows c * kCopyRows .. of one (layer, KV head) of dst[i], from the pages
+// that src[i] had (`old`).
+__global__ void __launch_bounds__(256)
+    compact_rows_kernel(PagesShape s, PagesBook b, const int* __restrict__ dst, int n_idx, const int* __restrict__ idx,
+                        int units_per_idx, const int* __restrict__ old, const int* __restrict__ words, uint4* k, uint4* v) {
+  __shared__ long long from_s[kCopyRows], to_s[kCopyRows];
+  const int chunks = (n_idx + kCopyRows - 1) / kCopyRows;
+  const int lh_all = s.layers * s.hkv;
+  const size_t u = blockIdx.x / chunks;
+  const int t0 = static_cast<int>(blockIdx.x - u * chunks) * kCopyRows, rows = min(kCopyRows, n_idx - t0);
+  const int i = static_cast<int>(u / lh_all), lh = static_cast<int>(u - static_cast<size_t>(i) * lh_all);
+  int from = -1;
+  if (threadIdx.x < rows) from = __ldg(idx + (u / units_per_idx) * n_idx + t0 + threadIdx.x);
+  wait_for_previous();
+  const int len = words[4 * i];
+  if (len < 0) return;                          // refused
+  if (threadIdx.x < rows) {
+    const int t = t0 + threadIdx.x;
+    const int page = from >= 0 && from < len ? old[static_cast<size_t>(i) * s.max_pages + from / s.page_rows] : -1;
+    if (page < 0) record_error(SPK_DEVERR_INDEX, static_cast<int>(u));
+    const int to = b.table[static_cast<size_t>(dst[i]) * s.max_pages + t / s.page_rows];
+    from_s[threadIdx.x] = page < 0 ? -1 : pool_row(s, lh, page, from % s.page_rows);
+    to_s[threadIdx.x] = pool_row(s, lh, to, t % s.page_rows);
+  }
+  __syncthreads();
+  copy_rows(from_s, to_s, rows, s.row_vecs, k, v, k, v);
 }
 
 // --------------------------------------------------------------------------
 // write
 // --------------------------------------------------------------------------
-// Row t < counts[i] of (i, l, h) goes to row lens[seq] - counts[i] + t of
-// sequence seqs[i]; a thread moves 16 bytes of K and of V.  A page that other
-// sequences hold too is not written.
+// Block: kCopyRows of the rows (i, layer, KV head, t), in that order.  Row
+// t < counts[i] goes to row lens[seq] - counts[i] + t of sequence seqs[i].  A
+// page that other sequences hold too is not written, nor a sequence that an
+// earlier entry names.  (A 16K prompt, 32 layers x 8 KV heads, 4.3 GB read and
+// written: 631 us, 6.8 TB/s.)
 __global__ void __launch_bounds__(256)
     write_kernel(PagesShape s, PagesBook b, const uint4* __restrict__ k, const uint4* __restrict__ v, int n_src,
                  const int* __restrict__ idx, int n_idx, int units_per_idx, const int* __restrict__ counts,
-                 const int* __restrict__ seqs, uint4* __restrict__ kp, uint4* __restrict__ vp, size_t total) {
-  const size_t stride = static_cast<size_t>(gridDim.x) * blockDim.x;
+                 const int* __restrict__ seqs, int n, uint4* __restrict__ kp, uint4* __restrict__ vp) {
+  __shared__ long long from_s[kCopyRows], to_s[kCopyRows];
   const int lh_all = s.layers * s.hkv;
-  for (size_t e = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x; e < total; e += stride) {
-    const size_t row = e / s.row_vecs;
-    const int vec = static_cast<int>(e - row * s.row_vecs);
-    const size_t u = row / n_idx;
-    const int t = static_cast<int>(row - u * n_idx);
-    const int i = static_cast<int>(u / lh_all), lh = static_cast<int>(u % lh_all);
-    const int count = counts != nullptr ? __ldg(counts + i) : n_idx;
-    if (t >= count) continue;
-    const int seq = __ldg(seqs + i);
-    bool ok = seq >= 0 && seq < s.n_seqs && count <= n_idx;
-    const int pos = ok ? b.lens[seq] - count + t : -1;
-    ok = ok && pos >= 0 && pos < static_cast<long long>(s.max_pages) * s.page_rows;
-    const int page = ok ? b.table[static_cast<size_t>(seq) * s.max_pages + pos / s.page_rows] : -1;
-    ok = ok && page >= 0 && page < s.n_pages && b.refs[page] == 1;
-    const int from = idx != nullptr ? __ldg(idx + (u / units_per_idx) * n_idx + t) : t;
-    ok = ok && from >= 0 && from < n_src;
-    if (!ok) {
-      if (vec == 0) record_error(SPK_DEVERR_INDEX, static_cast<int>(u));
-      continue;
+  const long long all = static_cast<long long>(n) * lh_all * n_idx;
+  const long long f0 = static_cast<long long>(blockIdx.x) * kCopyRows;
+  const int rows = static_cast<int>(min(static_cast<long long>(kCopyRows), all - f0));
+  const long long per = static_cast<long long>(lh_all) * n_idx;      // rows of an entry
+  long long from = -1, to = -1;
+  int mine = -1;
+  if (threadIdx.x < rows) {
+    const long long f = f0 + threadIdx.x, u = f / n_idx;
+    const int t = static_cast<int>(f - u * n_idx), i = static_cast<int>(u / lh_all);
+    mine = i;
+    const int count = counts != nullptr ? __ldg(counts + i) : n_idx, seq = __ldg(seqs + i);
+    bool ok = seq >= 0 && seq < s.n_seqs && count >= 0 && count <= n_idx;
+    if (!ok || t < count) {
+      const int src = idx != nullptr ? __ldg(idx + (u / units_per_idx) * n_idx + t) : t;
+      const int pos = ok ? b.lens[seq] - count + t : -1;
+      ok = pos >= 0 && pos < static_cast<long long>(s.max_pages) * s.page_rows && src >= 0 && src < n_src;
+      const int page = ok ? b.table[static_cast<size_t>(seq) * s.max_pages + pos / s.page_rows] : -1;
+      ok = ok && page >= 0 && page < s.n_pages && b.refs[page] == 1;
+      if (ok) {
+        from = (u * n_src + src) * s.row_vecs;
+        to = pool_row(s, static_cast<int>(u - static_cast<long long>(i) * lh_all), page, pos % s.page_rows);
+      } else {
+        record_error(SPK_DEVERR_INDEX, static_cast<int>(u));
+      }
     }
-    const size_t a = (u * n_src + from) * s.row_vecs + vec;
-    const size_t z = ((((static_cast<size_t>(lh / s.hkv) * s.n_pages + page) * s.hkv + lh % s.hkv) * s.page_rows) +
-                      pos % s.page_rows) * s.row_vecs + vec;
-    kp[z] = __ldcs(k + a);
-    vp[z] = __ldcs(v + a);
   }
+  for (int i = static_cast<int>(f0 / per); i <= static_cast<int>((f0 + rows - 1) / per); ++i) {
+    bool twice = false;
+    for (int j = threadIdx.x; j < i; j += blockDim.x) twice |= __ldg(seqs + j) == __ldg(seqs + i);
+    if (__syncthreads_or(twice)) {
+      if (mine == i) from = -1;
+      if (threadIdx.x == 0) record_error(SPK_DEVERR_INDEX, i);
+    }
+  }
+  if (threadIdx.x < rows) {
+    from_s[threadIdx.x] = from;
+    to_s[threadIdx.x] = to;
+  }
+  __syncthreads();
+  copy_rows(from_s, to_s, rows, s.row_vecs, k, v, kp, vp);
 }
 
-int num_sms() {
-  int dev = 0, sms = 148;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms;
+// One CTA, or a cluster of eight for large tables.
+template <typename K, typename... A>
+cudaError_t launch_book(K one, K eight, const PagesShape& s, int n, bool tables, cudaStream_t stream, A... args) {
+  const long long cells = static_cast<long long>(n) * s.max_pages;
+  const bool big = s.n_pages > 8192 || (tables && cells > 2048);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(big ? 8 : 1);
+  cfg.blockDim = dim3(kBookThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 8;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = big ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, big ? eight : one, args...);
 }
 
-unsigned copy_blocks(size_t total) {
-  const size_t blocks = (total + 255) / 256, cap = static_cast<size_t>(num_sms()) * 8;
-  return static_cast<unsigned>(blocks < cap ? blocks : cap);
+// A kernel that starts under the one before it (wait_for_previous).
+template <typename... P, typename... A>
+cudaError_t launch_under(void (*kernel)(P...), dim3 grid, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
 }  // namespace
@@ -495,19 +597,16 @@ cudaError_t launch_pages_reserve(const PagesShape& s, const PagesBook& b, void* 
                                  const int* seqs, const int* n_new, int n, int* result, void* ws,
                                  cudaStream_t stream) {
   int* words = ws_words(ws, n, s.max_pages);
-  reserve_kernel<<<kBookCtas, kBookThreads, 0, stream>>>(s, b, seqs, n_new, n, result, words);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_book(reserve_kernel<1>, reserve_kernel<8>, s, n, false, stream, s, b, seqs, n_new, n, result, words);
   if (e != cudaSuccess || n == 0) return e;
   const int lh = s.layers * s.hkv;
-  copy_tail_kernel<<<dim3(n, lh < 1024 ? lh : 1024), 256, 0, stream>>>(s, words, static_cast<uint4*>(k_pages),
-                                                                       static_cast<uint4*>(v_pages));
-  return cudaGetLastError();
+  return launch_under(copy_tail_kernel, dim3(n, lh < 1024 ? lh : 1024), stream, s, words, k_pages, v_pages);
 }
 
 cudaError_t launch_pages_fork(const PagesShape& s, const PagesBook& b, const int* src, const int* dst,
                               const int* n_rows, int n, int* result, void* ws, cudaStream_t stream) {
-  fork_kernel<<<kBookCtas, kBookThreads, 0, stream>>>(s, b, src, dst, n_rows, n, result, static_cast<int*>(ws));
-  return cudaGetLastError();
+  return launch_book(fork_kernel<1>, fork_kernel<8>, s, n, true, stream, s, b, src, dst, n_rows, n, result,
+                     static_cast<int*>(ws));
 }
 
 cudaError_t launch_pages_free(const PagesShape& s, const PagesBook& b, const int* seqs, const int* keep_rows, int n,
@@ -523,25 +622,22 @@ cudaError_t launch_pages_compact(const PagesShape& s, const PagesBook& b, void* 
                                  int units_per_idx, int* result, void* ws, cudaStream_t stream) {
   int* old = static_cast<int*>(ws);
   int* words = ws_words(ws, n, s.max_pages);
-  compact_book_kernel<<<kBookCtas, kBookThreads, 0, stream>>>(s, b, src, dst, n, n_idx, result, old, words);
-  cudaError_t e = cudaGetLastError();
-  const size_t total = static_cast<size_t>(n) * s.layers * s.hkv * n_idx * s.row_vecs;
-  if (e != cudaSuccess || total == 0) return e;
-  compact_rows_kernel<<<copy_blocks(total), 256, 0, stream>>>(s, b, dst, n_idx, idx, units_per_idx, old, words,
-                                                              static_cast<uint4*>(k_pages),
-                                                              static_cast<uint4*>(v_pages), total);
-  return cudaGetLastError();
+  cudaError_t e = launch_book(compact_book_kernel<1>, compact_book_kernel<8>, s, n, true, stream, s, b, src, dst, n, n_idx,
+                              result, old, words);
+  const long long blocks = static_cast<long long>(n) * s.layers * s.hkv * ((n_idx + kCopyRows - 1) / kCopyRows);
+  if (e != cudaSuccess || blocks == 0) return e;
+  return launch_under(compact_rows_kernel, dim3(static_cast<unsigned>(blocks)), stream, s, b, dst, n_idx, idx, units_per_idx,
+                      old, words, k_pages, v_pages);
 }
 
 cudaError_t launch_pages_write(const PagesShape& s, const PagesBook& b, const void* k, const void* v, int n_src,
                                const int* idx, int n_idx, int units_per_idx, const int* counts, const int* seqs,
                                int n, void* k_pages, void* v_pages, cudaStream_t stream) {
-  const size_t total = static_cast<size_t>(n) * s.layers * s.hkv * n_idx * s.row_vecs;
-  if (total == 0) return cudaSuccess;
-  write_kernel<<<copy_blocks(total), 256, 0, stream>>>(s, b, static_cast<const uint4*>(k),
-                                                       static_cast<const uint4*>(v), n_src, idx, n_idx, units_per_idx,
-                                                       counts, seqs, static_cast<uint4*>(k_pages),
-                                                       static_cast<uint4*>(v_pages), total);
+  const long long rows = static_cast<long long>(n) * s.layers * s.hkv * n_idx;
+  if (rows == 0) return cudaSuccess;
+  write_kernel<<<static_cast<unsigned>((rows + kCopyRows - 1) / kCopyRows), 256, 0, stream>>>(
+      s, b, static_cast<const uint4*>(k), static_cast<const uint4*>(v), n_src, idx, n_idx, units_per_idx, counts, seqs, n,
+      static_cast<uint4*>(k_pages), static_cast<uint4*>(v_pages));
   return cudaGetLastError();
 }
 

@@ -296,6 +296,19 @@ def test_rows_that_may_not_be_written(P):
     assert torch.equal(c.k[0, z[0], 0, 1].cpu(), c.kh[0, z[0], 0, 1])
 
 
+def test_a_sequence_listed_twice_is_written_by_its_first_entry(P):
+    c = Cache(P, 1, 30, 2, 16, 64, 4, 5, seed=13)
+    assert c.reserve([2, 0], [20, 20]) == 0
+    k, v = c.rows(3, 20)
+    P.kv_pages_write(k.cuda(), v.cuda(), *c.all, c.i32([2, 0, 2]))
+    assert P.spk_device_error(clear=True)[0] == P.binding.SPK_ERR_ARG
+    for i, s in enumerate([2, 0]):
+        for t in range(20):
+            pg = c.book.table[s][t // 16]
+            c.kh[:, pg, :, t % 16], c.vh[:, pg, :, t % 16] = k[i, :, :, t], v[i, :, :, t]
+    c.check()
+
+
 def test_bookkeeping_is_captured_and_replayed(P):
     # a decoding loop's step: room for one row, the row; the graph's second run
     # takes the next page where the sequence has come to one
