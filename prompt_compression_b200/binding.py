@@ -1,4 +1,5 @@
-"""ctypes binding of include/speckv.h: argument marshalling only.
+"""Binding of include/speckv.h: argument marshalling only (ctypes; compiled for
+the paged-cache operators and tree attention).
 
 Each function takes torch tensors that already live on the GPU, checks their
 sizes, dtype, device and contiguity, and passes raw pointers, sizes and the
@@ -480,105 +481,59 @@ def vs_sparse_attention(q, k, v, vertical, slash, out=None, lse2=None, workspace
 
 
 # --------------------------------------------------------------------- paged cache, tree attention
-# These entry points launch on the device of their tensors, whichever device
-# is current, and refuse tensors of several devices.  They are called once a
-# layer or a step, so the checks are kept short: a tensor costs about 0.3 us.
-def _device_index(t: torch.Tensor, name: str) -> int:
+# These calls are made once a step or a layer and run for microseconds, so their
+# marshalling is compiled (csrc/bind.cpp): it checks the tensors (CUDA, one
+# device, type, contiguous, size: ValueError), launches on their device,
+# whichever is current, and allocates what is not given.
+_bind_module = None
+
+
+def _bind():
+    global _bind_module
+    if _bind_module is None:
+        load_library()
+        path = os.path.join(_PKG, "_bind.so")
+        if not os.path.exists(path):
+            raise ImportError(f"{path} is missing: build it with `python -m prompt_compression_b200.build`")
+        from . import _bind as module
+        module.set_error(SpeckvError)
+        _bind_module = module
+    return _bind_module
+
+
+def _handle(stream, t: torch.Tensor) -> int:
+    """The handle of an explicit stream for a call on t's device."""
     if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return t.get_device()
+        raise ValueError("the tensors must be CUDA tensors")
+    if isinstance(stream, torch.cuda.Stream):
+        if stream.device != t.device:
+            raise ValueError(f"the stream is one of {stream.device}, the tensors are on {t.device}")
+        return stream.cuda_stream
+    return int(stream)
 
 
-def _ptr(t: Optional[torch.Tensor], name: str, dtype, index: int, numel: Optional[int] = None) -> Optional[int]:
-    """Data pointer of a contiguous tensor of `dtype` (None: any) on CUDA device
-    `index`; None for None."""
-    if t is None:
-        return None
-    if t.get_device() != index:
-        raise ValueError(f"{name} must be a CUDA tensor on cuda:{index}, got one on {t.device}")
-    if t.dtype is not dtype and dtype is not None:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if numel is not None and t.numel() != numel:
-        raise ValueError(f"{name} has {t.numel()} elements, the call needs {numel}")
-    return t.data_ptr()
+def _new_on(stream, t: torch.Tensor, shape, dtype) -> torch.Tensor:
+    """An output of a call on an explicit stream: allocated there, and known to
+    the caller's stream too, so that its memory is not given away while either
+    uses it."""
+    with torch.cuda.stream(_stream_object(stream, t.device)):
+        out = torch.empty(shape, dtype=dtype, device=t.device)
+    out.record_stream(torch.cuda.current_stream(t.device))
+    return out
 
 
-# torch.cuda.current_stream() builds a Python object (3 us); this returns the handle
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
-                      lambda index: torch.cuda.current_stream(index).cuda_stream)
-
-
-def _launch(index: int, stream, fn, *args):
-    """fn(*args, stream) with CUDA device `index` current."""
-    if stream is None:
-        handle = _raw_stream(index)
-    elif isinstance(stream, torch.cuda.Stream):
-        if stream.device.index != index:
-            raise ValueError(f"the stream is one of {stream.device}, the tensors are on cuda:{index}")
-        handle = stream.cuda_stream
-    else:
-        handle = int(stream)
-    if torch.cuda.current_device() == index:
-        status = fn(*args, handle)
-    else:
-        with torch.cuda.device(index):
-            status = fn(*args, handle)
-    if status != SPK_OK:
-        _check(status)
-
-
-def _new(shape, dtype, index: int, stream) -> torch.Tensor:
-    """An output of a call on `stream`: allocated there, and known to the
-    caller's stream too, so that its memory is not given away while either uses it."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=index)
-    dev = torch.device("cuda", index)
-    with torch.cuda.stream(_stream_object(stream, dev)):
-        t = torch.empty(shape, dtype=dtype, device=dev)
-    t.record_stream(torch.cuda.current_stream(dev))
-    return t
-
-
-def _scratch(ws: Optional[torch.Tensor], nbytes: int, index: int, stream):
-    """(pointer, bytes) of the caller's workspace, or of a temporary one on the
-    launch stream, and the tensor that holds it."""
-    if ws is not None:
-        return _ptr(ws, "workspace", None, index), ws.numel() * ws.element_size(), ws
-    if stream is None:
-        ws = torch.empty(nbytes or 256, dtype=torch.uint8, device=index)
-    else:
-        ws = _workspace(None, nbytes, torch.device("cuda", index), stream)
-    return ws.data_ptr(), nbytes or 256, ws
+def _pages_scratch(workspace, shape: "PagesShape", n: int, stream, t: torch.Tensor):
+    return workspace if workspace is not None else _workspace(None, kv_pages_workspace_size(shape, n), t.device, stream)
 
 
 def pages_shape(k_pages, v_pages, page_refs, page_table, seq_lens) -> PagesShape:
-    if k_pages.dim() != 5 or k_pages.shape != v_pages.shape or k_pages.dtype is not v_pages.dtype:
-        raise ValueError("k_pages and v_pages are [L, n_pages, Hkv, page_rows, d], of the same dtype")
+    """The spk_pages_shape of a cache's tensors."""
     L, n_pages, hkv, rows, d = k_pages.shape
-    if page_refs.numel() != n_pages:
-        raise ValueError(f"page_refs has {page_refs.numel()} elements, the call needs {n_pages}")
-    return _table_shape(page_refs, page_table, seq_lens, rows, L, hkv, d, k_pages.element_size())
-
-
-def _table_shape(page_refs, page_table, seq_lens, page_rows, layers=1, hkv=1, d=16, elem_bytes=1) -> PagesShape:
-    if page_table.dim() != 2:
-        raise ValueError("page_table is [n_seqs, max_pages]")
-    n_seqs, max_pages = page_table.shape
-    if seq_lens.numel() != n_seqs:
-        raise ValueError(f"seq_lens has {seq_lens.numel()} elements, the call needs {n_seqs}")
-    return PagesShape(layers, page_refs.numel(), hkv, int(page_rows), d, elem_bytes, n_seqs, max_pages)
+    return PagesShape(L, n_pages, hkv, rows, d, k_pages.element_size(), *page_table.shape)
 
 
 def kv_pages_workspace_size(shape: PagesShape, n: int) -> int:
     return load_library().kv_pages_workspace_size(ctypes.byref(shape), n)
-
-
-def _book(page_refs, page_table, seq_lens, index):
-    i32 = torch.int32
-    return (_ptr(page_refs, "page_refs", i32, index), _ptr(page_table, "page_table", i32, index),
-            _ptr(seq_lens, "seq_lens", i32, index))
 
 
 def kv_pages_reserve(k_pages, v_pages, page_refs, page_table, seq_lens, seqs, n_new, result=None, workspace=None,
@@ -587,19 +542,15 @@ def kv_pages_reserve(k_pages, v_pages, page_refs, page_table, seq_lens, seqs, n_
     for the new rows, and a copy of a partially filled last page that other
     sequences hold too.  Returns result int32 [1] (on the device): 0 done, > 0
     that many pages were missing, -1 a wrong argument; nothing changed unless 0."""
-    lib = load_library()
-    index = _device_index(k_pages, "k_pages")
-    shape = ctypes.byref(pages_shape(k_pages, v_pages, page_refs, page_table, seq_lens))
-    n, i32 = seqs.numel(), torch.int32
-    if result is None:
-        result = _new((1,), i32, index, stream)
-    ws, ws_bytes, _hold = _scratch(workspace, 0 if workspace is not None else lib.kv_pages_workspace_size(shape, n),
-                                   index, stream)
-    _launch(index, stream, lib.kv_pages_reserve, shape, _ptr(k_pages, "k_pages", None, index),
-            _ptr(v_pages, "v_pages", None, index), *_book(page_refs, page_table, seq_lens, index),
-            _ptr(seqs, "seqs", i32, index), _ptr(n_new, "n_new", i32, index, n), n,
-            _ptr(result, "result", i32, index, 1), ws, ws_bytes)
-    return result
+    handle = None
+    if stream is not None:
+        handle = _handle(stream, k_pages)
+        shape = pages_shape(k_pages, v_pages, page_refs, page_table, seq_lens)
+        workspace = _pages_scratch(workspace, shape, seqs.numel(), stream, k_pages)
+        if result is None:
+            result = _new_on(stream, k_pages, (1,), torch.int32)
+    return _bind().kv_pages_reserve(k_pages, v_pages, page_refs, page_table, seq_lens, seqs, n_new, result, workspace,
+                                    handle)
 
 
 def kv_pages_write(k, v, k_pages, v_pages, page_refs, page_table, seq_lens, seqs, idx=None, counts=None,
@@ -607,26 +558,8 @@ def kv_pages_write(k, v, k_pages, v_pages, page_refs, page_table, seq_lens, seqs
     """The newest rows of sequences seqs int32 [n] from k, v [n, L, Hkv, n_src, d]:
     the rows idx int32 [n * L * Hkv / units_per_idx, n_idx] selects (None: all),
     of which the first counts int32 [n] are written (None: all)."""
-    lib = load_library()
-    index = _device_index(k_pages, "k_pages")
-    shape = pages_shape(k_pages, v_pages, page_refs, page_table, seq_lens)
-    n, i32 = seqs.numel(), torch.int32
-    if k.dim() != 5 or k.shape != v.shape:
-        raise ValueError("k and v are [n, L, Hkv, n_src, d]")
-    kn, kl, kh, n_src, kd = k.shape
-    if kn != n or kl != shape.layers or kh != shape.hkv or kd != shape.head_dim:
-        raise ValueError("k and v are [n, L, Hkv, n_src, d] with the pages' L, Hkv and d")
-    if k.dtype is not k_pages.dtype or v.dtype is not k_pages.dtype:
-        raise ValueError(f"k and v must be {k_pages.dtype} like the pages")
-    units = n * kl * kh
-    n_idx = n_src if idx is None else idx.shape[-1]
-    if units_per_idx < 1 or units % units_per_idx:
-        raise ValueError(f"units ({units}) must be a multiple of units_per_idx ({units_per_idx})")
-    _launch(index, stream, lib.kv_pages_write, ctypes.byref(shape), _ptr(k, "k", None, index), _ptr(v, "v", None, index),
-            n_src, _ptr(idx, "idx", i32, index, units // units_per_idx * n_idx), n_idx, units_per_idx,
-            _ptr(counts, "counts", i32, index, n), *_book(page_refs, page_table, seq_lens, index),
-            _ptr(seqs, "seqs", i32, index), n, _ptr(k_pages, "k_pages", None, index),
-            _ptr(v_pages, "v_pages", None, index))
+    _bind().kv_pages_write(k, v, k_pages, v_pages, page_refs, page_table, seq_lens, seqs, idx, counts, units_per_idx,
+                           None if stream is None else _handle(stream, k_pages))
 
 
 def kv_pages_compact(k_pages, v_pages, page_refs, page_table, seq_lens, src, dst, idx, units_per_idx: int = 1,
@@ -634,24 +567,15 @@ def kv_pages_compact(k_pages, v_pages, page_refs, page_table, seq_lens, src, dst
     """Sequences dst int32 [n] become the rows idx int32 [n * L * Hkv /
     units_per_idx, n_idx] of sequences src int32 [n], in pages of their own
     (dst = src: in place).  Returns result as kv_pages_reserve does."""
-    lib = load_library()
-    index = _device_index(k_pages, "k_pages")
-    shape = pages_shape(k_pages, v_pages, page_refs, page_table, seq_lens)
-    n, n_idx, i32 = src.numel(), idx.shape[-1], torch.int32
-    units = n * shape.layers * shape.hkv
-    if units_per_idx < 1 or units % units_per_idx:
-        raise ValueError(f"units ({units}) must be a multiple of units_per_idx ({units_per_idx})")
-    if result is None:
-        result = _new((1,), i32, index, stream)
-    shape = ctypes.byref(shape)
-    ws, ws_bytes, _hold = _scratch(workspace, 0 if workspace is not None else lib.kv_pages_workspace_size(shape, n),
-                                   index, stream)
-    _launch(index, stream, lib.kv_pages_compact, shape, _ptr(k_pages, "k_pages", None, index),
-            _ptr(v_pages, "v_pages", None, index), *_book(page_refs, page_table, seq_lens, index),
-            _ptr(src, "src", i32, index), _ptr(dst, "dst", i32, index, n), n,
-            _ptr(idx, "idx", i32, index, units // units_per_idx * n_idx), n_idx, units_per_idx,
-            _ptr(result, "result", i32, index, 1), ws, ws_bytes)
-    return result
+    handle = None
+    if stream is not None:
+        handle = _handle(stream, k_pages)
+        shape = pages_shape(k_pages, v_pages, page_refs, page_table, seq_lens)
+        workspace = _pages_scratch(workspace, shape, src.numel(), stream, k_pages)
+        if result is None:
+            result = _new_on(stream, k_pages, (1,), torch.int32)
+    return _bind().kv_pages_compact(k_pages, v_pages, page_refs, page_table, seq_lens, src, dst, idx, units_per_idx,
+                                    result, workspace, handle)
 
 
 def kv_pages_fork(page_refs, page_table, seq_lens, src, dst, page_rows: int, n_rows=None, result=None, workspace=None,
@@ -659,50 +583,37 @@ def kv_pages_fork(page_refs, page_table, seq_lens, src, dst, page_rows: int, n_r
     """Sequences dst int32 [n] become sequences src int32 [n] as they were before
     the call (their first n_rows int32 [n] rows where given), by holding their
     pages.  Returns result as kv_pages_reserve does."""
-    lib = load_library()
-    index = _device_index(page_table, "page_table")
-    shape = ctypes.byref(_table_shape(page_refs, page_table, seq_lens, page_rows))
-    n, i32 = src.numel(), torch.int32
-    if result is None:
-        result = _new((1,), i32, index, stream)
-    ws, ws_bytes, _hold = _scratch(workspace, 0 if workspace is not None else lib.kv_pages_workspace_size(shape, n),
-                                   index, stream)
-    _launch(index, stream, lib.kv_pages_fork, shape, *_book(page_refs, page_table, seq_lens, index),
-            _ptr(src, "src", i32, index), _ptr(dst, "dst", i32, index, n), _ptr(n_rows, "n_rows", i32, index, n), n,
-            _ptr(result, "result", i32, index, 1), ws, ws_bytes)
-    return result
+    handle = None
+    if stream is not None:
+        handle = _handle(stream, page_table)
+        shape = PagesShape(1, page_refs.numel(), 1, int(page_rows), 16, 1, *page_table.shape)
+        workspace = _pages_scratch(workspace, shape, src.numel(), stream, page_table)
+        if result is None:
+            result = _new_on(stream, page_table, (1,), torch.int32)
+    return _bind().kv_pages_fork(page_refs, page_table, seq_lens, src, dst, page_rows, n_rows, result, workspace, handle)
 
 
 def kv_pages_free(page_refs, page_table, seq_lens, seqs, page_rows: int, keep_rows=None, stream=None):
     """Sequences seqs int32 [n] keep their first keep_rows int32 [n] rows (None:
     none); the pages behind them are released."""
-    lib = load_library()
-    index = _device_index(page_table, "page_table")
-    shape = _table_shape(page_refs, page_table, seq_lens, page_rows)
-    n, i32 = seqs.numel(), torch.int32
-    _launch(index, stream, lib.kv_pages_free, ctypes.byref(shape), *_book(page_refs, page_table, seq_lens, index),
-            _ptr(seqs, "seqs", i32, index), _ptr(keep_rows, "keep_rows", i32, index, n), n)
+    _bind().kv_pages_free(page_refs, page_table, seq_lens, seqs, page_rows, keep_rows,
+                          None if stream is None else _handle(stream, page_table))
 
 
 SPK_BF16, SPK_FP16 = 0, 1
-_TREE_DTYPES = {torch.bfloat16: SPK_BF16, torch.float16: SPK_FP16}
 
 
 def tree_shape(q, k_pages, page_table, scale: float = 1.0) -> TreeShape:
-    if q.dim() != 5 or k_pages.dim() != 5 or page_table.dim() != 2:
-        raise ValueError("q is [B, L, Hq, T, d], k_pages [L, n_pages, Hkv, page_rows, d], page_table [n_seqs, max_pages]")
+    """The spk_tree_shape of a call of tree_attention."""
     Bsz, L, hq, T, d = q.shape
-    Lk, n_pages, hkv, rows, dk = k_pages.shape
-    if (L, d) != (Lk, dk):
-        raise ValueError("q and k_pages disagree on layers or head_dim")
-    if q.dtype not in _TREE_DTYPES:
-        raise ValueError(f"q must be bfloat16 or float16, got {q.dtype}")
-    n_seqs, max_pages = page_table.shape
-    return TreeShape(Bsz, L, hq, hkv, d, T, n_pages, rows, n_seqs, max_pages, _TREE_DTYPES[q.dtype], float(scale))
+    _, n_pages, hkv, rows, _ = k_pages.shape
+    return TreeShape(Bsz, L, hq, hkv, d, T, n_pages, rows, *page_table.shape,
+                     SPK_FP16 if q.dtype is torch.float16 else SPK_BF16, float(scale))
 
 
 def tree_attention_workspace_size(shape: TreeShape) -> int:
-    return int(load_library().tree_attention_workspace_size(ctypes.byref(shape)))
+    """Bytes, for the current device."""
+    return load_library().tree_attention_workspace_size(ctypes.byref(shape))
 
 
 def tree_attention(q, k_pages, v_pages, page_table, seq_lens, k_tree=None, v_tree=None, mask=None, n_live=None,
@@ -713,56 +624,31 @@ def tree_attention(q, k_pages, v_pages, page_table, seq_lens, k_tree=None, v_tre
     int32 [B]: the elements' sequences (None: 0 .. B-1); n_live int32 [B]: how
     many of the tokens count (None: T).  Returns out [B, L, Hq, T, d]; fills
     lse2 fp32 [B, L, Hq, T] when given."""
-    lib = load_library()
-    index = _device_index(q, "q")
-    shape = tree_shape(q, k_pages, page_table, scale)
-    Bsz, T, kind, i32 = shape.batch, shape.n_nodes, q.dtype, torch.int32
-    if v_pages.shape != k_pages.shape:
-        raise ValueError("v_pages must have k_pages' shape")
-    if k_tree is None or v_tree is None:
-        if k_tree is not v_tree:
-            raise ValueError("k_tree and v_tree are given together or not at all")
-    else:
-        tree = (Bsz, shape.layers, shape.hkv, T, shape.head_dim)
-        if k_tree.shape != tree or v_tree.shape != tree:
-            raise ValueError(f"k_tree and v_tree must be {list(tree)}")
-    if out is None:
-        out = _new(q.shape, kind, index, stream)
-    size = ctypes.byref(shape)
-    rows = Bsz * shape.layers * shape.hq * T
-    if workspace is not None:
-        ws, ws_bytes, _hold = _scratch(workspace, 0, index, stream)
-    elif torch.cuda.current_device() == index:
-        ws, ws_bytes, _hold = _scratch(None, lib.tree_attention_workspace_size(size), index, stream)
-    else:
-        with torch.cuda.device(index):
-            ws, ws_bytes, _hold = _scratch(None, lib.tree_attention_workspace_size(size), index, stream)
-    _launch(index, stream, lib.tree_attention, size, _ptr(q, "q", None, index),
-            _ptr(k_pages, "k_pages", kind, index), _ptr(v_pages, "v_pages", kind, index),
-            _ptr(page_table, "page_table", i32, index), _ptr(seq_lens, "seq_lens", i32, index, shape.n_seqs),
-            _ptr(seqs, "seqs", i32, index, Bsz), _ptr(k_tree, "k_tree", kind, index),
-            _ptr(v_tree, "v_tree", kind, index), _ptr(mask, "mask", i32, index, Bsz * T * ((T + 31) // 32)),
-            _ptr(n_live, "n_live", i32, index, Bsz), _ptr(out, "out", kind, index, rows * shape.head_dim),
-            _ptr(lse2, "lse2", torch.float32, index, rows), ws, ws_bytes)
-    return out
+    handle = None
+    if stream is not None:
+        handle = _handle(stream, q)
+        if out is None:
+            out = _new_on(stream, q, q.shape, q.dtype)
+        if workspace is None:
+            with torch.cuda.device(q.device):
+                need = tree_attention_workspace_size(tree_shape(q, k_pages, page_table, scale))
+            workspace = _workspace(None, need, q.device, stream)
+    return _bind().tree_attention(q, k_pages, v_pages, page_table, seq_lens, k_tree, v_tree, mask, n_live, seqs, out,
+                                  lse2, workspace, scale, handle)
 
 
 def tree_mask(parents, n_live=None, mask=None, depth=None, stream=None):
     """Visibility words int32 [B, T, ceil(T/32)] and depths int32 [B, T] of trees
     given by parents int32 [B, T] (the node before node i, in [-1, i))."""
-    if parents.dim() != 2:
-        raise ValueError("parents is [B, T]")
-    index = _device_index(parents, "parents")
-    Bsz, T = parents.shape
-    words, i32 = (T + 31) // 32, torch.int32
-    if mask is None:
-        mask = _new((Bsz, T, words), i32, index, stream)
-    if depth is None:
-        depth = _new((Bsz, T), i32, index, stream)
-    _launch(index, stream, load_library().tree_mask, Bsz, T, _ptr(parents, "parents", i32, index),
-            _ptr(n_live, "n_live", i32, index, Bsz), _ptr(mask, "mask", i32, index, Bsz * T * words),
-            _ptr(depth, "depth", i32, index, Bsz * T))
-    return mask, depth
+    handle = None
+    if stream is not None:
+        handle = _handle(stream, parents)
+        Bsz, T = parents.shape
+        if mask is None:
+            mask = _new_on(stream, parents, (Bsz, T, (T + 31) // 32), torch.int32)
+        if depth is None:
+            depth = _new_on(stream, parents, (Bsz, T), torch.int32)
+    return _bind().tree_mask(parents, n_live, mask, depth, handle)
 
 
 # --------------------------------------------------------------------- errors
