@@ -859,7 +859,7 @@ spk_status tree_attention(const spk_tree_shape* s, const void* q, const void* k_
   if ((st = check_pages_ws(ws, ws_bytes, tree_ws_bytes(plan, s->head_dim))) != SPK_OK) return st;
   TreeParams p;
   memset(&p, 0, sizeof p);
-  p.q = q; p.out = out; p.lse2 = lse2;
+  p.q = q; p.v_tree = v_tree; p.out = out; p.lse2 = lse2;
   p.table = table; p.lens = lens; p.seqs = seqs; p.n_live = n_live;
   p.mask = mask; p.words = (s->n_nodes + 31) / 32;
   p.batch = s->batch; p.layers = s->layers; p.hkv = s->hkv; p.T = s->n_nodes;

@@ -38,6 +38,7 @@ struct Half16;
 
 template <>
 struct Half16<__nv_bfloat16> {
+  static constexpr uint32_t kExponent = 0x7f80u;
   // d += a * b, m16n8k16, fp32 accumulators
   static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -54,6 +55,7 @@ struct Half16<__nv_bfloat16> {
 
 template <>
 struct Half16<__half> {
+  static constexpr uint32_t kExponent = 0x7c00u;
   static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "

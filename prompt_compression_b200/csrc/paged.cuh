@@ -51,6 +51,7 @@ constexpr int kTreeMaxNodes = 1024;
 
 struct TreeParams {
   const void* q;           // [batch][layers][hq][T][d]
+  const void* v_tree;      // [batch][layers][hkv][T][d] or null
   void* out;               // like q
   float* lse2;             // [batch][layers][hq][T] or null
   const int* table;        // [n_seqs][max_pages]

@@ -84,6 +84,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   __shared__ TreeStart start_s;
   __shared__ __align__(16) float wmax[kWarps][C::kRows];   // read and written in pairs
   __shared__ int abort_flag, last_s;
+  __shared__ int wild_s[2];      // nodes [x, y) whose V holds something that is not finite (y 0: none)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -92,6 +93,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       mbar_init(&empty[s], kWarps);
     }
     abort_flag = 0;
+    wild_s[0] = kTreeMaxNodes;
+    wild_s[1] = 0;
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -312,6 +315,25 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
           fence_proxy_async_smem();              // before the slot's next copy
         }
+        if (tile.nodes > 0) {                    // and in the nodes' rows what is not finite: not every row sees them
+          constexpr int kCh = DW / 8;
+          bool found = false;
+          for (int x = lane; x < tile.nodes * kCh; x += 32) {
+            const int row = tile.off + x / kCh, ch = warp * kCh + x % kCh;
+            uint4* const at = reinterpret_cast<uint4*>(smem + st * C::kStageBytes + C::kAtoms * C::kHalf + (ch >> 3) * C::kHalf +
+                                                       row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+            uint4 w = *at;
+            if (tree_clear_wild(w, Half16<T>::kExponent)) {
+              *at = w;
+              found = true;
+            }
+          }
+          if (found) {
+            atomicMin(&wild_s[0], tile.node0);
+            atomicMax(&wild_s[1], tile.node0 + tile.nodes);
+            fence_proxy_async_smem();
+          }
+        }
         consumers_sync();
 #pragma unroll
         for (int k = 0; k < kTreeKeys / 16; k += 2) {
@@ -360,6 +382,29 @@ __global__ void __launch_bounds__(kThreads, 2)
           l[n][1] += y.y;
         }
       }
+      // rows that see a node whose V is not finite (thread = row, every fourth column)
+      auto patch = [&]() {
+        const int lo = wild_s[0], hi = wild_s[1];
+        if (hi == 0) return;
+        consumers_sync();                        // the outputs are there
+#pragma unroll 1
+        for (int y = threadIdx.x; y < rows * 4; y += kWarps * 32) {
+          const int row = y >> 2, r = run.row0 + row, i = r % p.T;
+          if (i >= run.e.live) continue;
+          if (run.from == run.to)
+            tree_patch<T>(p, run.b, run.unit, i, lo, hi, y & 3, D, 4, D,
+                          static_cast<T*>(p.out) + (static_cast<size_t>(run.unit) * p.rows + r) * D, D, size_t(0));
+          else
+            tree_patch<T>(p, run.b, run.unit, i, lo, hi, y & 3, D, 4, D,
+                          p.part_o + ((static_cast<size_t>(blockIdx.x) * 2 + run.slot) * (D / 4) * C::kRows + row) * 4, 4,
+                          static_cast<size_t>(C::kRows) * 4);
+        }
+        consumers_sync();
+        if (threadIdx.x == 0) {
+          wild_s[0] = kTreeMaxNodes;
+          wild_s[1] = 0;
+        }
+      };
       if (run.from == run.to) {
         // the whole unit: outputs through shared memory (over Q), 16 bytes a store
 #pragma unroll
@@ -390,6 +435,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           if ((run.row0 + row) % p.T < run.e.live)
             dst[x] = *reinterpret_cast<const uint4*>(q_p + row * (D * 2) + ((ch ^ (row & 7)) << 4));
         }
+        patch();
       } else {
         const size_t part = static_cast<size_t>(blockIdx.x) * 2 + run.slot;
 #pragma unroll
@@ -407,6 +453,7 @@ __global__ void __launch_bounds__(kThreads, 2)
               *reinterpret_cast<float2*>(p.part_ml + (part * C::kRows + row) * 2) = make_float2(m[n][c], l[n][c]);
           }
         }
+        patch();
         // the last of the item's shares joins them:
         //   M = max m_c,  out = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c
         bool join = false;
@@ -495,9 +542,8 @@ __global__ void __launch_bounds__(kJoinRows * (D / 4) * (MANY ? kJoinGroups : 1)
   int c0 = 0, c1 = 0;
   if (x < s.total) {
     item = tree_item<PAIRS>(p, s.e, s.b, s.base, x);
-    c0 = item.first / s.share;
-    c1 = (item.first + item.jobs - 1) / s.share;
-    if (by_border && (item.first == x || c0 != static_cast<int>(blockIdx.x))) c1 = c0;
+    const bool mine = !by_border || (item.first != x && item.first / s.share == static_cast<int>(blockIdx.x));
+    if (mine) tree_spread(item, s.e.tiles, s.share, c0, c1);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (c0 == c1) return;                         // no item, or one share has it

@@ -211,6 +211,18 @@ __device__ __forceinline__ void tree_part(const TreeItem& i, int tiles, int begi
   slot = i.first > begin ? 1 : 0;
 }
 
+// The shares [from, to] that hold tiles of an item (a pair's border inside its
+// first tile leaves the share before it without one, and so for the last).
+__device__ __forceinline__ void tree_spread(const TreeItem& i, int tiles, int share, int& from, int& to) {
+  int t0, t1, slot;
+  from = i.first / share;
+  to = (i.first + i.jobs - 1) / share;
+  tree_part(i, tiles, from * share, (from + 1) * share, t0, t1, slot);
+  if (t0 == t1) ++from;
+  tree_part(i, tiles, to * share, (to + 1) * share, t0, t1, slot);
+  if (t0 == t1) --to;
+}
+
 struct TreeRun {           // a part of an item that a CTA works on
   int b, unit, row0, t0, t1, slot;
   int pool;                // (layer * n_pages) * hkv + KV head: the unit of page 0 in the pages' maps
@@ -249,19 +261,76 @@ struct TreeWalker {
       if (r.t0 == 0 && r.t1 == e.tiles) {
         r.c0 = r.slot0 = r.from = r.to = 0;
       } else {
-        r.c0 = r.from = i.first / share;
-        r.to = (i.first + i.jobs - 1) / share;
-        int t0, t1, slot;
-        tree_part(i, e.tiles, r.c0 * share, (r.c0 + 1) * share, t0, t1, r.slot0);
-        if (t0 == t1) ++r.from;                  // (a pair's border inside its first tile)
-        tree_part(i, e.tiles, r.to * share, (r.to + 1) * share, t0, t1, slot);
-        if (t0 == t1) --r.to;
+        r.c0 = i.first / share;
+        r.slot0 = i.first > r.c0 * share ? 1 : 0;
+        tree_spread(i, e.tiles, share, r.from, r.to);
       }
       return true;
     }
     return false;
   }
 };
+
+// Whether node i sees node j.
+__device__ __forceinline__ bool tree_sees(const TreeParams& p, int b, int i, int j) {
+  if (p.mask == nullptr) return j <= i;
+  return (__ldg(p.mask + (static_cast<size_t>(b) * p.T + i) * p.words + (j >> 5)) >> (j & 31)) & 1u;
+}
+
+// Clears what is not finite among eight 16-bit values; true if there was any.
+// (expo: the type's exponent bits.)  A row of V that some query rows see and
+// others do not must not reach the others as 0 * NaN, so such values leave the
+// product, and the rows that see them get their sum (tree_patch).
+__device__ __forceinline__ bool tree_clear_wild(uint4& w, uint32_t expo) {
+  uint32_t* const x = reinterpret_cast<uint32_t*>(&w);
+  bool any = false;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if ((x[k] & expo) == expo) {
+      x[k] &= 0xffff0000u;
+      any = true;
+    }
+    if ((x[k] >> 16 & expo) == expo) {
+      x[k] &= 0xffffu;
+      any = true;
+    }
+  }
+  return any;
+}
+
+// Whether the V rows of nodes [lo, hi) of a unit hold something that is not
+// finite, by a warp.
+template <int D>
+__device__ __forceinline__ bool tree_wild(const TreeParams& p, int unit, int lo, int hi, uint32_t expo) {
+  const uint4* const v = reinterpret_cast<const uint4*>(p.v_tree) + (static_cast<size_t>(unit) * p.T + lo) * (D / 8);
+  bool any = false;
+#pragma unroll 4
+  for (int k = threadIdx.x & 31; k < (hi - lo) * (D / 8); k += 32) {
+    uint4 w = __ldg(v + k);
+    any |= tree_clear_wild(w, expo);
+  }
+  return __any_sync(0xffffffffu, any);
+}
+
+// A row's output (or partial result) where a V row of nodes [lo, hi) that node i
+// sees is not finite: the sum of those values, whatever the finite ones give.
+// Columns d0, d0 + step, .. below d1; column d lies at
+// out[(d / run) * stride + d % run].
+template <typename V, typename O>
+__device__ __noinline__ void tree_patch(const TreeParams& p, int b, int unit, int i, int lo, int hi, int d0, int d1, int step,
+                                        int D, O* out, int run, size_t stride) {
+#pragma unroll 1
+  for (int d = d0; d < d1; d += step) {
+    float sum = 0.f;
+#pragma unroll 1
+    for (int j = lo; j < hi; ++j) {
+      if (!tree_sees(p, b, i, j)) continue;
+      const float v = static_cast<float>(static_cast<const V*>(p.v_tree)[(static_cast<size_t>(unit) * p.T + j) * D + d]);
+      if (!isfinite(v)) sum += v;
+    }
+    if (sum != 0.f) out[(d / run) * stride + d % run] = static_cast<O>(sum);   // (true for NaN too)
+  }
+}
 
 // Where the partial results of share c of an item lie.
 __device__ __forceinline__ size_t tree_place(const TreeRun& r, int c) {

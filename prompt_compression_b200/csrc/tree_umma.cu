@@ -84,11 +84,12 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatil
 template <int SLOTS>
 struct UmmaShared {
   uint64_t q_full, q_empty, full[SLOTS], empty[SLOTS], s_full[2], p_half[2], p_full[2], run_done, o_empty, ml_ready,
-      parts_in, joined, run_full[kRunSlots], run_empty[kRunSlots];
+      parts_in, joined, run_full[kRunSlots], run_empty[kRunSlots], wild_full[kRunSlots];
   TreeRun run[kRunSlots];
   float2 ml[2][128];          // both groups' row states, for the other
   uint32_t tmem_holder;
   int abort_flag, last;
+  int wild[kRunSlots];        // of each run: whether V of its nodes holds something that is not finite
 };
 
 // QT query tiles of a unit share the K/V tiles (1: no unit has more than 128
@@ -251,6 +252,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     for (int s = 0; s < kRunSlots; ++s) {
       mbar_init(&sh.run_full[s], 1);
       mbar_init(&sh.run_empty[s], kRunReaders);
+      mbar_init(&sh.wild_full[s], 1);
     }
     sh.abort_flag = 0;
     fence_mbar_init();
@@ -289,17 +291,39 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
 
   if (warp == kRunWarp) {
     // -------------------------------------------------------------------- runs
-    if (lane == 0) {
-      TreeWalker<kKeys, true> walk(start);
-      for (uint32_t k = 0;; ++k) {
-        const uint32_t s = k % kRunSlots;
+    // lane 0 finds them; the warp looks whether V of a run's nodes holds something
+    // that is not finite, when the next run is out
+    TreeWalker<kKeys, true> walk(start);
+    int lo = 0, hi = 0, unit = 0;
+    bool go = true;
+    for (uint32_t k = 0; go; ++k) {
+      const uint32_t s = k % kRunSlots;
+      const int old_lo = lo, old_hi = hi, old_unit = unit;
+      lo = hi = unit = 0;
+      if (lane == 0) {
         TreeRun r;
-        const bool more = walk.next(p, r);
-        if (!more) r.t0 = -1;
-        if (!bar_wait(&sh.run_empty[s], ((k / kRunSlots) & 1) ^ 1, abort_v, umma_site(5, 1))) break;
+        go = walk.next(p, r);
+        if (!go) r.t0 = -1;
+        go = bar_wait(&sh.run_empty[s], ((k / kRunSlots) & 1) ^ 1, abort_v, umma_site(5, 1)) && go;
+        if (go && p.has_tree && r.t1 * kKeys > r.e.len) {      // (the nodes of these tiles, or all where they lie with rows)
+          const int cached = (r.e.len + kKeys - 1) / kKeys;
+          const bool fused = tree_fused<kKeys>(p, r.e.len);
+          lo = fused ? 0 : max(0, r.t0 - cached) * kKeys;
+          hi = fused ? r.e.live : min(r.e.live, (r.t1 - cached) * kKeys);
+          unit = r.unit;
+        }
         sh.run[s] = r;
         mbar_arrive(&sh.run_full[s]);
-        if (!more) break;
+      }
+      go = __shfl_sync(0xffffffffu, go, 0);
+      lo = __shfl_sync(0xffffffffu, lo, 0);
+      hi = __shfl_sync(0xffffffffu, hi, 0);
+      unit = __shfl_sync(0xffffffffu, unit, 0);
+      if (k == 0) continue;
+      const bool wild = old_lo < old_hi && tree_wild<D>(p, old_unit, old_lo, old_hi, Half16<T>::kExponent);
+      if (lane == 0) {
+        sh.wild[(k - 1) % kRunSlots] = wild;
+        mbar_arrive(&sh.wild_full[(k - 1) % kRunSlots]);
       }
     }
   } else if (warp == kProducerWarp || warp == kProducerWarp + 1) {
@@ -524,7 +548,11 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     auto wait_all = [&](uint64_t* bar, uint32_t parity, int which) -> bool {
       return __all_sync(0xffffffffu, bar_wait(bar, parity, abort_v, umma_site(2 + x, which)));
     };
-    while (ok && next_run(ok)) {
+    // (the run stays in shared memory until its end: its fields would cost 16 registers)
+    for (;; ++taken) {
+      const TreeRun& run = sh.run[taken % kRunSlots];
+      if (!(ok = wait_all(&sh.run_full[taken % kRunSlots], (taken / kRunSlots) & 1, 7))) break;
+      if (run.t0 < 0) break;
       const bool pair = QT == 2 && run.pair, alone = !pair;
       const int tiles = run.t1 - run.t0, jobs = pair ? tiles : (tiles + 1 - x) / 2;
       const int row = run.row0 + (pair ? x * 128 : 0) + r;      // row of the unit
@@ -532,6 +560,8 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       const bool idle = row - lane >= p.rows;                  // no row of this warp's exists
       const int node = there ? row % p.T : 0;
       float m = -INFINITY, l = 0.f;                            // running maximum of c2 s, sum
+      const uint32_t wild_slot = taken % kRunSlots, wild_parity = (taken / kRunSlots) & 1;
+      bool wild = false;                                       // V of the run's nodes holds something that is not finite
       for (int i = 0; i < jobs; ++i, ++job) {
         const TreeTile tile = tree_tile<kKeys>(p, run.e, run.t0 + (pair ? i : 2 * i + x));
         const bool full_tile = tile.rows == kKeys;
@@ -545,7 +575,13 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
           // ... and zeros in V's rows without a key, up to the end of the last k-step:
           // whatever the slot holds there (it may be NaN) must not meet the zeros of P
           const int end = (tile.n + 15) & ~15, gap = tile.nodes > 0 ? tile.off - tile.rows : 0, bad = gap + end - tile.n;
-          if (bad > 0 && !(pair && x == 1)) {                  // (a pair's group 1 comes behind group 0's products)
+          bool clear = false;
+          if (tile.nodes > 0) {
+            if (!(ok = wait_all(&sh.wild_full[wild_slot], wild_parity, 6))) break;
+            clear = sh.wild[wild_slot] != 0;
+            wild = wild || clear;
+          }
+          if ((bad > 0 || clear) && !(pair && x == 1)) {       // (a pair's group 1 comes behind group 0's products)
             const uint32_t seq = 2 * (base + (pair ? i : 2 * i + x)) + 1;
             const int slot = seq % C::kSlots;
             if (!(ok = wait_all(&sh.full[slot], (seq / C::kSlots) & 1, 1))) break;
@@ -554,6 +590,14 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
               const int vr = b < gap ? tile.rows + b : tile.n + b - gap;
               *reinterpret_cast<uint4*>(ring + slot * C::kTileBytes + (ch >> 3) * 16384 + vr * 128 +
                                         (((ch & 7) ^ (vr & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            // and in the nodes' rows what is not finite, if there is any: not every row sees them
+            for (int k = r; k < (clear ? tile.nodes * (D / 8) : 0); k += 128) {
+              const int vr = tile.off + k / (D / 8), ch = k % (D / 8);
+              uint4* const at = reinterpret_cast<uint4*>(ring + slot * C::kTileBytes + (ch >> 3) * 16384 + vr * 128 +
+                                                         (((ch & 7) ^ (vr & 7)) << 4));
+              uint4 w = *at;
+              if (tree_clear_wild(w, Half16<T>::kExponent)) *at = w;
             }
             fence_proxy_async_smem();
           }
@@ -702,6 +746,10 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       const int part_row = (pair ? x * 128 : 0) + r;
       const int c_end = alone ? (x + 1) * (D / 2) : D;
       const uint32_t lives = __ballot_sync(0xffffffffu, live);
+      if (alone && p.has_tree && run.t1 * kKeys > run.e.len) { // (the nodes may have been the other group's)
+        if (!(ok = wait_all(&sh.wild_full[wild_slot], wild_parity, 6))) break;
+        wild = sh.wild[wild_slot] != 0;
+      }
       // 32 columns of the rows, 8 (16 bytes) to a vector: four lanes exchange vectors
       // so that each store covers 64 bytes of eight rows
       auto store32 = [&](const uint32_t (&o)[32], int c) {
@@ -739,7 +787,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
 #pragma unroll
             for (int k = 0; k < 32; ++k) o[k] = 0u;
           }
-            if (whole) {
+          if (whole) {
             store32(o, c);
           } else if (live) {
             // partial results lie [4 columns][row]: a store covers 32 rows together
@@ -750,6 +798,16 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
                                                  __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
           }
         }
+      }
+      if (wild) {
+        __syncwarp();                                          // (the row's outputs are other lanes' stores)
+        const int d0 = alone ? x * (D / 2) : 0;
+        if (live && whole)
+          tree_patch<T>(p, run.b, run.unit, node, 0, run.e.live, d0, c_end, 1, D,
+                        static_cast<T*>(p.out) + (static_cast<size_t>(run.unit) * p.rows + row) * D, D, size_t(0));
+        else if (live)
+          tree_patch<T>(p, run.b, run.unit, node, 0, run.e.live, d0, c_end, 1, D,
+                        p.part_o + (place * (D / 4) * p.item_rows + part_row) * 4, 4, static_cast<size_t>(p.item_rows) * 4);
       }
       if (live && (!alone || x == 0)) {
         if (!whole)
@@ -818,6 +876,8 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             p.lse2[static_cast<size_t>(run.unit) * p.rows + row] = L == 0.f ? -INFINITY : M + lg2_approx(L);
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.run_empty[taken % kRunSlots]);
       base += tiles;
       ++runs;
     }

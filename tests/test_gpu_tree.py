@@ -240,6 +240,100 @@ def test_on_another_stream(P):
     assert torch.equal(out, ref)
 
 
+@pytest.mark.parametrize("T,hq,lens,dt", [(6, 4, [200, 9], "bf16"), (40, 4, [300, 64], "fp16"), (40, 16, [500, 3], "bf16"),
+                                          (150, 8, [129, 0], "bf16")])
+def test_nodes_that_a_row_does_not_see_may_hold_anything(P, T, hq, lens, dt):
+    # node 2 has NaN, infinities and huge values in K and V: the rows that see it
+    # get what the sums give, the others do not notice
+    import torch
+    dtype = torch.bfloat16 if dt == "bf16" else torch.float16
+    t, h = build_case(30 + T, dtype, 2, 1, hq, 2, 128, T, 32, lens, mask="random")
+    seen = h["sees"][:, :, 2].copy()
+    clean = {x: t[x].clone() for x in ("k_tree", "v_tree")}
+    t["v_tree"][:, :, :, 2, 0] = float("nan")
+    t["v_tree"][:, :, :, 2, 1] = float("inf")
+    t["v_tree"][:, :, :, 2, 2] = float("-inf")
+    out, lse2 = (torch.full_like(t["q"], 7.0), torch.full(t["q"].shape[:-1], 7.0, device="cuda"))
+    P.tree_attention(**t, out=out, lse2=lse2)
+    torch.cuda.synchronize()
+    got = out.float().cpu().numpy()
+    for b in range(2):
+        rows = got[b][:, :, seen[b], :]
+        assert np.isnan(rows[..., 0]).all() and np.isposinf(rows[..., 1]).all() and np.isneginf(rows[..., 2]).all()
+    t["v_tree"], h["vt"] = clean["v_tree"], clean["v_tree"].double().cpu().numpy()
+    ref = torch.full_like(t["q"], 7.0)
+    P.tree_attention(**t, out=ref)
+    torch.cuda.synchronize()
+    ref = ref.float().cpu().numpy()
+    for b in range(2):
+        assert np.array_equal(got[b][:, :, ~seen[b]], ref[b][:, :, ~seen[b]])
+        assert np.array_equal(got[b][:, :, seen[b], 3:], ref[b][:, :, seen[b], 3:])
+    t["k_tree"][:, :, :, 2] = float("nan")                          # hidden keys: not even the maximum sees them
+    bad = torch.full_like(t["q"], 7.0)
+    P.tree_attention(**t, out=bad)
+    torch.cuda.synchronize()
+    bad = bad.float().cpu().numpy()
+    for b in range(2):
+        assert np.array_equal(bad[b][:, :, ~seen[b]], ref[b][:, :, ~seen[b]])
+        assert np.isnan(bad[b][:, :, seen[b]]).all()
+    assert P.spk_device_error() == (0, 0)
+
+
+@pytest.mark.parametrize("case", [
+    # seed, B, L, hq, hkv, d, T, page, lens: many units, ragged, so that shares cut them in two
+    (40, 40, 2, 16, 8, 64, 1, 16, 300),          # 640 units of 2 rows
+    (41, 44, 1, 32, 8, 128, 5, 32, 700),         # 352 units of 20 rows, items cut where a share ends
+    (42, 20, 2, 40, 8, 128, 9, 64, 520),         # 320 units of 45 rows
+    (43, 38, 1, 16, 4, 64, 40, 24, 400),         # 152 units of 160 rows: pairs of query tiles
+    (44, 19, 1, 64, 8, 128, 40, 16, 300),        # 152 units of 320 rows: a pair and a single
+])
+def test_many_ragged_units(P, case):
+    import torch
+    seed, B, L, hq, hkv, d, T, page, most = case
+    rng = np.random.default_rng(seed)
+    lens = [int(x) for x in rng.integers(0, most, B)]
+    live = [int(x) for x in rng.integers(1, T + 1, B)]
+    t, h = build_case(seed, torch.bfloat16, B, L, hq, hkv, d, T, page, lens, live, "tree")
+    check(P, t, h, torch.bfloat16)
+
+
+def test_long_rows_of_two_query_tiles_and_more(P):
+    import torch
+    t, h = build_case(50, torch.bfloat16, 1, 1, 10, 2, 64, 64, 64, [6000], None, "tree")      # 320 rows, 47 tiles
+    check(P, t, h, torch.bfloat16)
+
+
+def test_two_calls_at_once(P):
+    # different streams, workspaces of their own
+    import torch
+    a, ha = build_case(51, torch.bfloat16, 2, 1, 8, 2, 128, 5, 16, [700, 90])
+    b, hb = build_case(52, torch.float16, 1, 1, 16, 2, 64, 20, 32, [900])
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = []
+    for _ in range(4):
+        outs.append((P.tree_attention(**a, stream=s1), P.tree_attention(**b, stream=s2)))
+    torch.cuda.synchronize()
+    ra, rb = P.tree_attention(**a), P.tree_attention(**b)
+    torch.cuda.synchronize()
+    for x, y in outs:
+        assert torch.equal(x, ra) and torch.equal(y, rb)
+
+
+def test_a_pool_beyond_32_bit_offsets(P):
+    # the sequence's pages lie behind 2^31 elements of the pool
+    import torch
+    t, h = build_case(53, torch.bfloat16, 1, 1, 4, 1, 128, 3, 64, [200])
+    n_pages = (1 << 31) // (64 * 128) + 10
+    kp = torch.zeros((1, n_pages, 1, 64, 128), dtype=torch.bfloat16, device="cuda")
+    vp = torch.zeros_like(kp)
+    old = t["k_pages"].shape[1]
+    kp[:, n_pages - old:], vp[:, n_pages - old:] = t["k_pages"], t["v_pages"]
+    t["page_table"] = torch.where(t["page_table"] >= 0, t["page_table"] + (n_pages - old), t["page_table"])
+    t["k_pages"], t["v_pages"] = kp, vp
+    check(P, t, h, torch.bfloat16)
+
+
 def test_bad_elements_keep_their_rows_and_are_recorded(P):
     import torch
     t, h = build_case(25, torch.bfloat16, 3, 1, 4, 2, 64, 2, 16, [60, 60, 60], seqs=[0, 1, 2])
