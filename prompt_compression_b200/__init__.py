@@ -1,5 +1,6 @@
 """B200 (sm_100a) lookahead importance scoring: SpecKV / SpecPC scoring, pooling,
-top-k selection and KV compaction.
+top-k selection and KV compaction; a paged KV cache and the attention of drafted
+token trees over it.
 
 This package is a thin binding over ``libspeckv.so`` (the C ABI declared in
 ``include/speckv.h``).  The functions below marshal torch tensors into raw
@@ -24,7 +25,9 @@ from .binding import (  # noqa: F401
     pages_shape, kv_pages_workspace_size, kv_pages_reserve, kv_pages_write, kv_pages_compact, kv_pages_fork,
     kv_pages_free, tree_shape, tree_attention_workspace_size, tree_attention, tree_mask,
 )
-from .pipeline import speckv_compress, specpc_select, cascade_compress  # noqa: F401
+from .pipeline import (  # noqa: F401
+    speckv_compress, specpc_select, cascade_compress, PagedCache, speckv_compress_pages,
+)
 
 __all__ = [
     "SpeckvError", "load_library", "library_path",
@@ -36,4 +39,5 @@ __all__ = [
     "pages_shape", "kv_pages_workspace_size", "kv_pages_reserve", "kv_pages_write", "kv_pages_compact",
     "kv_pages_fork", "kv_pages_free", "tree_shape", "tree_attention_workspace_size", "tree_attention", "tree_mask",
     "speckv_compress", "specpc_select", "cascade_compress",
+    "PagedCache", "speckv_compress_pages",
 ]

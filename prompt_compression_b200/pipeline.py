@@ -4,6 +4,9 @@ speckv_compress   scores -> pool + top-C_max + window -> compacted K/V
 specpc_select     SpecPC scores -> pool + top-K prompt tokens
 cascade_compress  SpecPC on the draft, gather the target K/V at the kept
                   tokens, then SpecKV on the gathered cache (SpecKV-PC)
+PagedCache        the tensors of a paged KV cache, and its operators
+speckv_compress_pages  SpecKV with the kept rows written straight into a
+                  paged cache
 
 "Draft-based Approximate Inference for LLMs" (paper notes), section 关键设计.
 """
@@ -80,3 +83,61 @@ def cascade_compress(draft_q, draft_k, row_weights, l_skip: int, keep: int, targ
     B.kv_compact(target_k, target_v, pc_idx, k_g, v_g, L * hkv, stream)
     out = speckv_compress(target_q, k_g, v_g, n_window, c_max, pool, stream=stream)
     return pc_scores, pc_idx, k_g, v_g, out
+
+
+class PagedCache:
+    """A paged KV cache on the device: k_pages, v_pages [L, n_pages, Hkv, page_rows,
+    d], page_table int32 [n_seqs, max_pages], seq_lens int32 [n_seqs], page_refs
+    int32 [n_pages].  The methods are the operators of the same names; lists of
+    sequences are int32 tensors.  A layer at a time, tree_attention takes
+    k_pages[l:l+1] and v_pages[l:l+1]."""
+
+    def __init__(self, layers: int, n_pages: int, hkv: int, page_rows: int, head_dim: int, n_seqs: int, max_pages: int,
+                 dtype=torch.bfloat16, device="cuda"):
+        shape = (layers, n_pages, hkv, page_rows, head_dim)
+        self.k_pages = torch.empty(shape, dtype=dtype, device=device)
+        self.v_pages = torch.empty(shape, dtype=dtype, device=device)
+        self.page_refs = torch.zeros(n_pages, dtype=torch.int32, device=device)
+        self.page_table = torch.full((n_seqs, max_pages), -1, dtype=torch.int32, device=device)
+        self.seq_lens = torch.zeros(n_seqs, dtype=torch.int32, device=device)
+        self.page_rows = page_rows
+
+    @property
+    def tensors(self):
+        return self.k_pages, self.v_pages, self.page_refs, self.page_table, self.seq_lens
+
+    def reserve(self, seqs, n_new, **kw):
+        return B.kv_pages_reserve(*self.tensors, seqs, n_new, **kw)
+
+    def write(self, k, v, seqs, **kw):
+        B.kv_pages_write(k, v, *self.tensors, seqs, **kw)
+
+    def compact(self, src, dst, idx, **kw):
+        return B.kv_pages_compact(*self.tensors, src, dst, idx, **kw)
+
+    def fork(self, src, dst, **kw):
+        return B.kv_pages_fork(*self.tensors[2:], src, dst, page_rows=self.page_rows, **kw)
+
+    def free(self, seqs, **kw):
+        B.kv_pages_free(*self.tensors[2:], seqs, page_rows=self.page_rows, **kw)
+
+    def attend(self, q, k_tree=None, v_tree=None, **kw):
+        return B.tree_attention(q, self.k_pages, self.v_pages, self.page_table, self.seq_lens, k_tree, v_tree, **kw)
+
+
+def speckv_compress_pages(q, k, v, n_window: int, c_max: int, cache: PagedCache, seqs, pool: int = 7,
+                          scale: float = 1.0, stream=None, pool_mode: int = B.SPK_POOL_MAX):
+    """SpecKV on every unit, with the kept rows written into the pages of
+    sequences seqs int32 [B] (behind what they hold): returns (scores, idx,
+    result); result as kv_pages_reserve's."""
+    Bsz, L, hkv, n_in, _ = k.shape
+    n_pre = n_in - n_window
+    keep = min(c_max, n_pre) + n_window
+    units = Bsz * L * hkv
+    scores = torch.empty((units, n_pre), dtype=torch.float32, device=q.device)
+    idx = torch.empty((units, keep), dtype=torch.int32, device=q.device)
+    B.speckv_score(q, k, n_window, scores, None, None, scale, stream)
+    B.topk_select(scores, c_max, n_window, idx, pool, None, None, stream, pool_mode)
+    result = cache.reserve(seqs, torch.full_like(seqs, keep), stream=stream)
+    cache.write(k, v, seqs, idx=idx, stream=stream)
+    return scores, idx, result

@@ -129,3 +129,26 @@ def test_temporary_workspace_is_allocated_on_the_launch_stream(monkeypatch):
     given = torch.zeros(8, dtype=torch.uint8)
     assert B._workspace(given, 4096, "cpu", 1234) is given      # the caller's workspace is used as is
     assert allocated_under == [sentinel]
+
+
+def _cache(L=2, n_pages=6, hkv=2, page=16, d=64, n_seqs=3, max_pages=4):
+    return [_bf16(L, n_pages, hkv, page, d), _bf16(L, n_pages, hkv, page, d), _i32(n_pages), _i32(n_seqs, max_pages),
+            _i32(n_seqs)]
+
+
+def test_paged_operators_reject_tensors_that_are_not_on_a_gpu():
+    # (the device comes first: everything else is compared with it)
+    c, s = _cache(), _i32(2)
+    for call in (lambda: B.kv_pages_reserve(*c, s, s), lambda: B.kv_pages_compact(*c, s, s, _i32(8, 3)),
+                 lambda: B.kv_pages_write(_bf16(2, 2, 2, 5, 64), _bf16(2, 2, 2, 5, 64), *c, s),
+                 lambda: B.kv_pages_fork(*c[2:], s, s, page_rows=16), lambda: B.kv_pages_free(*c[2:], s, page_rows=16),
+                 lambda: B.tree_attention(_bf16(2, 2, 4, 3, 64), c[0], c[1], c[3], c[4]),
+                 lambda: B.tree_mask(_i32(2, 5))):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+    with pytest.raises(ValueError, match="must be a tensor"):
+        B.tree_mask([[0, 1]])
+    for call in (lambda: B.kv_pages_reserve(*c, s, s, stream=7), lambda: B.kv_pages_free(*c[2:], s, page_rows=16, stream=7),
+                 lambda: B.tree_mask(_i32(2, 5), stream=7)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()

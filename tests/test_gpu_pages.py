@@ -357,3 +357,54 @@ def test_random_runs(P, seed):
             c.compact(a, b, idx, 1 if per else L * H)
         c.check()
     c.no_error()
+
+
+def test_the_binding_refuses_what_does_not_fit(P):
+    import torch
+    c = Cache(P, 2, 10, 2, 16, 64, 3, 4)
+    s, i32 = c.i32([0, 1]), c.i32
+    k = torch.zeros((2, 2, 2, 5, 64), dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros((2, 2, 4, 3, 64), dtype=torch.bfloat16, device="cuda")
+    t = torch.zeros((2, 2, 2, 3, 64), dtype=torch.bfloat16, device="cuda")
+    book = (c.refs, c.table, c.lens)
+    bad = [
+        ("n_new has", lambda: P.kv_pages_reserve(*c.all, s, i32([1]))),
+        ("int|Int", lambda: P.kv_pages_reserve(*c.all, s, i32([1, 1]).long())),
+        ("cuda:0", lambda: P.kv_pages_reserve(*c.all, s.cpu(), i32([1, 1]))),
+        ("n_new is required", lambda: P.kv_pages_reserve(*c.all, s, None)),
+        ("result has", lambda: P.kv_pages_reserve(*c.all, s, i32([1, 1]), result=i32([1, 1]))),
+        ("page_refs has", lambda: P.kv_pages_reserve(c.k, c.v, c.refs[:9], c.table, c.lens, s, s)),
+        ("seq_lens has", lambda: P.kv_pages_reserve(c.k, c.v, c.refs, c.table, c.lens[:2], s, s)),
+        ("same dtype", lambda: P.kv_pages_reserve(c.k, c.v.half(), *book, s, s)),
+        ("contiguous", lambda: P.kv_pages_reserve(c.k, c.v, c.refs, torch.zeros((4, 3), dtype=torch.int32, device="cuda").t(),
+                                                  c.lens, s, s)),
+        ("multiple", lambda: P.kv_pages_write(k, k, *c.all, s, units_per_idx=3)),
+        ("k and v are", lambda: P.kv_pages_write(k[:1], k[:1], *c.all, s)),
+        ("BFloat16", lambda: P.kv_pages_write(k.half(), k.half(), *c.all, s)),
+        ("idx has", lambda: P.kv_pages_write(k, k, *c.all, s, idx=i32([[0, 1]]), units_per_idx=1)),
+        ("counts has", lambda: P.kv_pages_write(k, k, *c.all, s, counts=i32([1]))),
+        ("dst has", lambda: P.kv_pages_compact(*c.all, s, i32([2]), i32([[0], [1]]), units_per_idx=4)),
+        ("n_rows has", lambda: P.kv_pages_fork(*book, s, i32([1, 2]), page_rows=16, n_rows=i32([1]))),
+        ("out of range", lambda: P.kv_pages_free(*book, s, page_rows=1 << 40)),
+        ("disagree", lambda: P.tree_attention(q[:, :1].contiguous(), c.k, c.v, c.table, c.lens)),
+        ("Half", lambda: P.tree_attention(q.float(), c.k.float(), c.v.float(), c.table, c.lens)),
+        ("BFloat16", lambda: P.tree_attention(q, c.k.half(), c.v.half(), c.table, c.lens)),
+        ("together", lambda: P.tree_attention(q, c.k, c.v, c.table, c.lens, t)),
+        ("must be", lambda: P.tree_attention(q, c.k, c.v, c.table, c.lens, t[:, :, :, :2], t[:, :, :, :2])),
+        ("mask has", lambda: P.tree_attention(q, c.k, c.v, c.table, c.lens, t, t, mask=i32([[1, 1, 1]]))),
+        ("lse2 has", lambda: P.tree_attention(q, c.k, c.v, c.table, c.lens, lse2=torch.zeros(5, device="cuda"))),
+        ("out has", lambda: P.tree_attention(q, c.k, c.v, c.table, c.lens, out=q[:1])),
+        ("contiguous", lambda: P.tree_attention(q.transpose(2, 3).contiguous().transpose(2, 3), c.k, c.v, c.table, c.lens)),
+        ("depth has", lambda: P.tree_mask(i32([[-1, 0]]), depth=i32([0]))),
+    ]
+    for needle, call in bad:
+        with pytest.raises(ValueError, match=needle):
+            call()
+    for status, call in ((P.binding.SPK_ERR_WORKSPACE, lambda: P.kv_pages_reserve(*c.all, s, s, workspace=k[0, 0, 0, 0, :2])),
+                         (P.binding.SPK_ERR_ARG, lambda: P.kv_pages_free(*book, s, page_rows=0)),
+                         (P.binding.SPK_ERR_UNSUPPORTED, lambda: P.tree_mask(torch.zeros((1, 1025), dtype=torch.int32, device="cuda")))):
+        with pytest.raises(P.SpeckvError) as e:
+            call()
+        assert e.value.status == status
+    c.check()
+    c.no_error()
