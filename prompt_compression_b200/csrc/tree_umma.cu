@@ -565,15 +565,21 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       for (int i = 0; i < jobs; ++i, ++job) {
         const TreeTile tile = tree_tile<kKeys>(p, run.e, run.t0 + (pair ? i : 2 * i + x));
         const bool full_tile = tile.rows == kKeys;
-        // before S is there: which keys this row sees, as words of 32 columns ...
+        // before S is there: which keys this row sees, as words of 32 columns
         uint32_t w0 = 0, w1 = 0, w2 = 0, w3 = 0;
         if (!full_tile) {
           w0 = tree_word(p, run.b, tile, 0, node, there);
           w1 = tree_word(p, run.b, tile, 32, node, there);
           w2 = tree_word(p, run.b, tile, 64, node, there);
           w3 = tree_word(p, run.b, tile, 96, node, there);
-          // ... and zeros in V's rows without a key, up to the end of the last k-step:
-          // whatever the slot holds there (it may be NaN) must not meet the zeros of P
+        }
+        if (!(ok = wait_all(&sh.s_full[x], job & 1, 0))) break;
+        tc_fence_after();
+        if (!full_tile) {
+          // Zeros in V's rows without a key, up to the end of the last k-step: whatever
+          // the slot holds there (it may be NaN) must not meet the zeros of P. Not before
+          // S of this tile: only then have the products of the slot's last V retired, and
+          // only then does the barrier's parity tell this V from that one.
           const int end = (tile.n + 15) & ~15, gap = tile.nodes > 0 ? tile.off - tile.rows : 0, bad = gap + end - tile.n;
           bool clear = false;
           if (tile.nodes > 0) {
@@ -602,8 +608,6 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
             fence_proxy_async_smem();
           }
         }
-        if (!(ok = wait_all(&sh.s_full[x], job & 1, 0))) break;
-        tc_fence_after();
         auto rescale = [&](float mt) {
           const bool need = mt > m + kRescaleLog2;             // the first key of a row: m = -inf
           if (__any_sync(0xffffffffu, need)) {
@@ -654,6 +658,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         };
         if (idle) {
           // (rows of a product depend on their own row of P only: nothing to store)
+          __syncwarp();
           if (lane == 0) mbar_arrive(&sh.p_half[x]);
         } else if (full_tile) {
           // columns 64 .. 127 stay in registers, 0 .. 63 are read twice, the second

@@ -297,6 +297,21 @@ def test_many_ragged_units(P, case):
     check(P, t, h, torch.bfloat16)
 
 
+def test_many_runs_of_one_query_tile_that_end_in_ragged_tiles(P):
+    # 128 units of 96 rows, several runs of each block: a run's last V is cleared behind its
+    # keys, which must wait for the products of the V before it in the same place
+    import torch
+    rng = np.random.default_rng(45)
+    lens = [int(x) for x in rng.integers(200, 3000 + 1, 16)]
+    live = [int(x) for x in rng.integers(12, 25, 16)]
+    t, h = build_case(45, torch.float16, 16, 1, 32, 8, 128, 24, 32, lens, live, "tree")
+    out, lse2 = check(P, t, h, torch.float16)
+    for _ in range(30):
+        o, l = torch.full_like(out, 7.0), torch.full_like(lse2, 7.0)
+        P.tree_attention(**t, out=o, lse2=l)
+        assert torch.equal(o, out) and torch.equal(l, lse2)
+
+
 def test_long_rows_of_two_query_tiles_and_more(P):
     import torch
     t, h = build_case(50, torch.bfloat16, 1, 1, 10, 2, 64, 64, 64, [6000], None, "tree")      # 320 rows, 47 tiles
