@@ -393,14 +393,15 @@ spk_status kv_pages_reserve(const spk_pages_shape* shape, void* k_pages, void* v
  *           NULL: row t is row t of k (n_idx <= n_src)
  *   counts  int32 [n], each in [0, n_idx]; NULL: n_idx
  * e.g. a prompt's rows (idx NULL), the rows topk_select kept (units_per_idx 1),
- * or the accepted nodes of a token tree (units_per_idx layers * hkv).  A row
- * whose index or position is out of range, or whose page is held by another
+ * or the accepted nodes of a token tree (units_per_idx layers * hkv).  reserved
+ * (int32, device) is the *result of the kv_pages_reserve that made room for the
+ * rows: nothing is written unless it is 0; NULL: there was room.  A row whose index or position is out of range, or whose page is held by another
  * sequence too, is left unwritten and recorded as SPK_ERR_ARG in the device
  * error word; so are the rows of an entry whose sequence stands earlier in the list. */
 spk_status kv_pages_write(const spk_pages_shape* shape, const void* k, const void* v, int n_src, const int32_t* idx,
                           int n_idx, int units_per_idx, const int32_t* counts, const int32_t* page_refs,
                           const int32_t* page_table, const int32_t* seq_lens, const int32_t* seqs, int n,
-                          void* k_pages, void* v_pages, void* stream);
+                          void* k_pages, void* v_pages, const int32_t* reserved, void* stream);
 
 /* Sequence dst[i] becomes the n_idx rows of sequence src[i] that idx selects,
  * in pages of its own (kv_compact for a paged cache):

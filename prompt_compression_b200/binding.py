@@ -107,7 +107,7 @@ def load_library():
         "vs_sparse_attention": (I, [vsp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
         "kv_pages_workspace_size": (sz, [pg, I]),
         "kv_pages_reserve": (I, [pg, vp, vp, vp, vp, vp, vp, vp, I, vp, vp, sz, vp]),
-        "kv_pages_write": (I, [pg, vp, vp, I, vp, I, I, vp, vp, vp, vp, vp, I, vp, vp, vp]),
+        "kv_pages_write": (I, [pg, vp, vp, I, vp, I, I, vp, vp, vp, vp, vp, I, vp, vp, vp, vp]),
         "kv_pages_compact": (I, [pg, vp, vp, vp, vp, vp, vp, vp, I, vp, I, I, vp, vp, sz, vp]),
         "kv_pages_fork": (I, [pg, vp, vp, vp, vp, vp, vp, I, vp, vp, sz, vp]),
         "kv_pages_free": (I, [pg, vp, vp, vp, vp, vp, I, vp]),
@@ -554,11 +554,13 @@ def kv_pages_reserve(k_pages, v_pages, page_refs, page_table, seq_lens, seqs, n_
 
 
 def kv_pages_write(k, v, k_pages, v_pages, page_refs, page_table, seq_lens, seqs, idx=None, counts=None,
-                   units_per_idx: int = 1, stream=None):
+                   units_per_idx: int = 1, reserved=None, stream=None):
     """The newest rows of sequences seqs int32 [n] from k, v [n, L, Hkv, n_src, d]:
     the rows idx int32 [n * L * Hkv / units_per_idx, n_idx] selects (None: all),
-    of which the first counts int32 [n] are written (None: all)."""
-    _bind().kv_pages_write(k, v, k_pages, v_pages, page_refs, page_table, seq_lens, seqs, idx, counts, units_per_idx,
+    of which the first counts int32 [n] are written (None: all).  reserved: the
+    result of the kv_pages_reserve that made room for them; nothing is written
+    unless it is 0."""
+    _bind().kv_pages_write(k, v, k_pages, v_pages, page_refs, page_table, seq_lens, seqs, idx, counts, units_per_idx, reserved,
                            None if stream is None else _handle(stream, k_pages))
 
 

@@ -702,7 +702,7 @@ spk_status kv_pages_reserve(const spk_pages_shape* s, void* k_pages, void* v_pag
 spk_status kv_pages_write(const spk_pages_shape* s, const void* k, const void* v, int n_src, const int32_t* idx,
                           int n_idx, int units_per_idx, const int32_t* counts, const int32_t* refs,
                           const int32_t* table, const int32_t* lens, const int32_t* seqs, int n, void* k_pages,
-                          void* v_pages, void* stream) {
+                          void* v_pages, const int32_t* reserved, void* stream) {
   spk_status st = check_pages(s, n);
   if (st == SPK_OK) st = check_book(refs, table, lens);
   if (st == SPK_OK) st = check_pool(k_pages, v_pages);
@@ -719,7 +719,7 @@ spk_status kv_pages_write(const spk_pages_shape* s, const void* k, const void* v
   if (!aligned16(k) || !aligned16(v)) return fail(SPK_ERR_ARG, "k and v must be 16-byte aligned");
   if (idx == nullptr && n_idx > n_src) return fail(SPK_ERR_ARG, "without idx, n_idx (%d) is at most n_src (%d)", n_idx, n_src);
   cudaError_t e = launch_pages_write(pages_shape(s), {const_cast<int*>(refs), const_cast<int*>(table), const_cast<int*>(lens)},
-                                     k, v, n_src, idx, n_idx, units_per_idx, counts, seqs, n, k_pages, v_pages,
+                                     k, v, n_src, idx, n_idx, units_per_idx, counts, seqs, n, k_pages, v_pages, reserved,
                                      static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ok() : cuda_fail(e, "kv_pages_write launch");
 }

@@ -233,8 +233,8 @@ SPK_CALL(py_kv_pages_reserve, 10) {
   return result.out();
 }
 
-// k v k_pages v_pages page_refs page_table seq_lens seqs idx counts units_per_idx stream
-SPK_CALL(py_kv_pages_write, 12) {
+// k v k_pages v_pages page_refs page_table seq_lens seqs idx counts units_per_idx reserved stream
+SPK_CALL(py_kv_pages_write, 13) {
   const int index = device_of(a[2], "k_pages");
   const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(index));
   spk_pages_shape s{};
@@ -252,7 +252,8 @@ SPK_CALL(py_kv_pages_write, 12) {
                        ints(a[8], "idx", index, lists * n_idx), n_idx, per, ints(a[9], "counts", index, n),
                        need_ints(a[4], "page_refs", index), need_ints(a[5], "page_table", index),
                        need_ints(a[6], "seq_lens", index), need_ints(a[7], "seqs", index), n,
-                       ptr(a[2], "k_pages", kAny, index), ptr(a[3], "v_pages", kAny, index), stream_of(a[11], index)));
+                       ptr(a[2], "k_pages", kAny, index), ptr(a[3], "v_pages", kAny, index),
+                       ints(a[11], "reserved", index, 1), stream_of(a[12], index)));
   Py_RETURN_NONE;
 }
 

@@ -39,7 +39,7 @@ cudaError_t launch_pages_free(const PagesShape& s, const PagesBook& b, const int
                               cudaStream_t stream);
 cudaError_t launch_pages_write(const PagesShape& s, const PagesBook& b, const void* k, const void* v, int n_src,
                                const int* idx, int n_idx, int units_per_idx, const int* counts, const int* seqs,
-                               int n, void* k_pages, void* v_pages, cudaStream_t stream);
+                               int n, void* k_pages, void* v_pages, const int* reserved, cudaStream_t stream);
 cudaError_t launch_pages_compact(const PagesShape& s, const PagesBook& b, void* k_pages, void* v_pages,
                                  const int* src, const int* dst, int n, const int* idx, int n_idx,
                                  int units_per_idx, int* result, void* ws, cudaStream_t stream);

@@ -504,18 +504,19 @@ __global__ void __launch_bounds__(256)
 // Block: kCopyRows of the rows (i, layer, KV head, t), in that order.  Row
 // t < counts[i] goes to row lens[seq] - counts[i] + t of sequence seqs[i].  A
 // page that other sequences hold too is not written, nor a sequence that an
-// earlier entry names.  (A 16K prompt, 32 layers x 8 KV heads, 4.3 GB read and
+// earlier entry names, nor anything where room was missing (*reserved).  (A 16K prompt, 32 layers x 8 KV heads, 4.3 GB read and
 // written: 631 us, 6.8 TB/s.)
 __global__ void __launch_bounds__(256)
     write_kernel(PagesShape s, PagesBook b, const uint4* __restrict__ k, const uint4* __restrict__ v, int n_src,
                  const int* __restrict__ idx, int n_idx, int units_per_idx, const int* __restrict__ counts,
-                 const int* __restrict__ seqs, int n, uint4* __restrict__ kp, uint4* __restrict__ vp) {
+                 const int* __restrict__ seqs, int n, uint4* __restrict__ kp, uint4* __restrict__ vp, const int* __restrict__ reserved) {
   __shared__ long long from_s[kCopyRows], to_s[kCopyRows];
   const int lh_all = s.layers * s.hkv;
   const long long all = static_cast<long long>(n) * lh_all * n_idx;
   const long long f0 = static_cast<long long>(blockIdx.x) * kCopyRows;
   const int rows = static_cast<int>(min(static_cast<long long>(kCopyRows), all - f0));
   const long long per = static_cast<long long>(lh_all) * n_idx;      // rows of an entry
+  const bool room = reserved == nullptr || *reserved == 0;
   long long from = -1, to = -1;
   int mine = -1;
   if (threadIdx.x < rows) {
@@ -533,11 +534,12 @@ __global__ void __launch_bounds__(256)
       if (ok) {
         from = (u * n_src + src) * s.row_vecs;
         to = pool_row(s, static_cast<int>(u - static_cast<long long>(i) * lh_all), page, pos % s.page_rows);
-      } else {
+      } else if (room) {
         record_error(SPK_DEVERR_INDEX, static_cast<int>(u));
       }
     }
   }
+  if (!room) return;
   for (int i = static_cast<int>(f0 / per); i <= static_cast<int>((f0 + rows - 1) / per); ++i) {
     bool twice = false;
     for (int j = threadIdx.x; j < i; j += blockDim.x) twice |= __ldg(seqs + j) == __ldg(seqs + i);
@@ -632,12 +634,12 @@ cudaError_t launch_pages_compact(const PagesShape& s, const PagesBook& b, void* 
 
 cudaError_t launch_pages_write(const PagesShape& s, const PagesBook& b, const void* k, const void* v, int n_src,
                                const int* idx, int n_idx, int units_per_idx, const int* counts, const int* seqs,
-                               int n, void* k_pages, void* v_pages, cudaStream_t stream) {
+                               int n, void* k_pages, void* v_pages, const int* reserved, cudaStream_t stream) {
   const long long rows = static_cast<long long>(n) * s.layers * s.hkv * n_idx;
   if (rows == 0) return cudaSuccess;
   write_kernel<<<static_cast<unsigned>((rows + kCopyRows - 1) / kCopyRows), 256, 0, stream>>>(
       s, b, static_cast<const uint4*>(k), static_cast<const uint4*>(v), n_src, idx, n_idx, units_per_idx, counts, seqs, n,
-      static_cast<uint4*>(k_pages), static_cast<uint4*>(v_pages));
+      static_cast<uint4*>(k_pages), static_cast<uint4*>(v_pages), reserved);
   return cudaGetLastError();
 }
 

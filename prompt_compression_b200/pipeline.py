@@ -129,8 +129,14 @@ def speckv_compress_pages(q, k, v, n_window: int, c_max: int, cache: PagedCache,
                           scale: float = 1.0, stream=None, pool_mode: int = B.SPK_POOL_MAX):
     """SpecKV on every unit, with the kept rows written into the pages of
     sequences seqs int32 [B] (behind what they hold): returns (scores, idx,
-    result); result as kv_pages_reserve's."""
-    Bsz, L, hkv, n_in, _ = k.shape
+    result); result as kv_pages_reserve's: unless it is 0 the cache is as it was."""
+    Bsz, L, hkv, n_in, d = k.shape
+    pages = cache.k_pages
+    if v.shape != k.shape or (L, hkv, d) != (pages.shape[0], pages.shape[2], pages.shape[4]) or k.dtype != pages.dtype:
+        raise ValueError(f"k and v are [B, L, Hkv, n_in, d] with the cache's L, Hkv, d and type, not {tuple(k.shape)}, "
+                         f"{tuple(v.shape)}")
+    if seqs.numel() != Bsz:
+        raise ValueError(f"seqs names {seqs.numel()} sequences for a batch of {Bsz}")
     n_pre = n_in - n_window
     keep = min(c_max, n_pre) + n_window
     units = Bsz * L * hkv
@@ -138,6 +144,8 @@ def speckv_compress_pages(q, k, v, n_window: int, c_max: int, cache: PagedCache,
     idx = torch.empty((units, keep), dtype=torch.int32, device=q.device)
     B.speckv_score(q, k, n_window, scores, None, None, scale, stream)
     B.topk_select(scores, c_max, n_window, idx, pool, None, None, stream, pool_mode)
-    result = cache.reserve(seqs, torch.full_like(seqs, keep), stream=stream)
-    cache.write(k, v, seqs, idx=idx, stream=stream)
+    with torch.cuda.stream(B._stream_object(stream, q.device)):
+        n_new = torch.full_like(seqs, keep)
+    result = cache.reserve(seqs, n_new, stream=stream)
+    cache.write(k, v, seqs, idx=idx, reserved=result, stream=stream)
     return scores, idx, result

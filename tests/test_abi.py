@@ -174,7 +174,7 @@ def test_pages_shape_errors(lib, change, n, status, needle):
     s = _pages(**change)
     assert lib.kv_pages_reserve(ctypes.byref(s), 16, 16, 16, 16, 16, 16, 16, n, 16, 16, 1 << 30, None) == status
     assert needle in lib.spk_last_error().decode()
-    assert lib.kv_pages_write(ctypes.byref(s), 16, 16, 4, None, 4, 1, None, 16, 16, 16, 16, n, 16, 16, None) == status
+    assert lib.kv_pages_write(ctypes.byref(s), 16, 16, 4, None, 4, 1, None, 16, 16, 16, 16, n, 16, 16, None, None) == status
     assert lib.kv_pages_compact(ctypes.byref(s), 16, 16, 16, 16, 16, 16, 16, n, 16, 3, 1, 16, 16, 1 << 30, None) == status
 
 
@@ -195,7 +195,7 @@ def test_pages_pointer_and_workspace_errors(lib):
     assert lib.kv_pages_free(s, 16, 16, 16, None, None, 2, None) == B.SPK_ERR_ARG
     assert lib.kv_pages_free(s, 16, 16, 16, None, None, 0, None) == B.SPK_OK                             # nothing to do
     w = lambda **k: lib.kv_pages_write(s, k.get("k", 16), 16, k.get("n_src", 4), k.get("idx"), k.get("n_idx", 4),  # noqa: E731
-                                       k.get("per", 1), None, 16, 16, 16, 16, 2, 16, 16, None)
+                                       k.get("per", 1), None, 16, 16, 16, 16, 2, 16, 16, None, None)
     assert w(per=3) == B.SPK_ERR_ARG and w(per=0) == B.SPK_ERR_ARG and w(n_idx=5) == B.SPK_ERR_ARG
     assert w(k=None) == B.SPK_ERR_ARG and w(k=8) == B.SPK_ERR_ARG and w(n_src=-1) == B.SPK_ERR_ARG
     assert w(n_idx=0) == B.SPK_OK

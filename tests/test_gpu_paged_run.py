@@ -169,3 +169,34 @@ def test_two_graphs_of_a_step(P):
         kr, _ = _rows(cache, s)
         assert torch.equal(kr[:, :, :70], k[s]) and torch.equal(kr[:, :, 70:], kts[s][0][:, :, :1].expand(-1, -1, 5, -1))
     assert P.spk_device_error() == (0, 0)
+
+
+def test_rows_without_room_leave_the_cache_as_it_was(P):
+    # a prompt whose kept rows find too few pages, and a list that names a sequence twice:
+    # what the sequences hold is not written over; on a stream of its own too
+    import torch
+    L, hq, hkv, d, page, n_in, window = 2, 4, 2, 64, 16, 300, 16
+    q, k, v = _randn((2, L, hq, 20, d), 1), _randn((2, L, hkv, n_in, d), 2), _randn((2, L, hkv, n_in, d), 3)
+    kw = dict(n_window=window, c_max=32, scale=0.125)
+    cache = P.PagedCache(L, 14, hkv, page, d, n_seqs=3, max_pages=12)
+    both, side = _i32([0, 2]), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    _, idx, result = P.speckv_compress_pages(q, k, v, cache=cache, seqs=both, stream=side, **kw)
+    side.synchronize()
+    assert result.item() == 0 and cache.seq_lens.tolist() == [48, 0, 48]       # 6 of the 14 pages
+    assert P.speckv_compress_pages(q, k, v, cache=cache, seqs=_i32([0, 2]), **kw)[2].item() == 0
+    held = [x.clone() for x in cache.tensors]
+    for seqs, want in (([0, 2], 4), ([0, 0], -1), ([0, 1], 4)):
+        assert P.speckv_compress_pages(q, k, v, cache=cache, seqs=_i32(seqs), **kw)[2].item() == want
+        for a, b in zip(cache.tensors[2:], held[2:]):
+            assert torch.equal(a, b)
+        for a, b in zip(cache.tensors[:2], held[:2]):
+            assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+        assert P.spk_device_error(clear=True)[0] == (0 if want > 0 else P.binding.SPK_ERR_ARG)
+    assert torch.equal(_rows(cache, 0)[0][:, :, :48],
+                       k[0].gather(2, idx.view(2, L, hkv, 48, 1)[0].long().expand(L, hkv, 48, d)))
+    with pytest.raises(ValueError):
+        P.speckv_compress_pages(q, k, v[:, :1], cache=cache, seqs=_i32([0, 1]), **kw)
+    with pytest.raises(ValueError):
+        P.speckv_compress_pages(q, k, v, cache=cache, seqs=_i32([0]), **kw)
+    assert cache.seq_lens.tolist() == [96, 0, 96]
