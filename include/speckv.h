@@ -361,7 +361,8 @@ spk_status decode_attention(int batch, int layers, int hq, int hkv, int head_dim
  * count out of range, a destination listed twice), recorded as SPK_ERR_ARG in
  * the device error word too.  Unless it is 0 the call changed nothing.  Free
  * pages are taken lowest number first, for the sequences in the list's order.
- * page_table, seq_lens and page_refs need 4-byte alignment, the pages 16.
+ * page_table, seq_lens, page_refs and the lists need 4-byte alignment, the
+ * pages 16.
  * Calls that change the same cache must not overlap on different streams.
  *
  * Supported: head_dim * elem_bytes a multiple of 16; max_pages * page_rows,

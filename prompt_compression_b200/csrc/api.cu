@@ -4,6 +4,7 @@
 // tensor maps, picks the persistent grid and enqueues the kernels on the
 // caller's stream.  No allocation, no host synchronisation on the compute
 // paths.
+#include <initializer_list>
 #include <atomic>
 #include <chrono>
 #include <cmath>
@@ -666,6 +667,12 @@ static spk_status check_book(const int32_t* refs, const int32_t* table, const in
   return SPK_OK;
 }
 
+static spk_status check_lists(std::initializer_list<const int32_t*> lists) {
+  for (const int32_t* p : lists)
+    if (!aligned4(p)) return fail(SPK_ERR_ARG, "lists and result must be 4-byte aligned");
+  return SPK_OK;
+}
+
 static spk_status check_pool(const void* k, const void* v) {
   if (k == nullptr || v == nullptr) return fail(SPK_ERR_ARG, "k_pages and v_pages must be non-NULL device pointers");
   if (!aligned16(k) || !aligned16(v)) return fail(SPK_ERR_ARG, "k_pages and v_pages must be 16-byte aligned");
@@ -693,6 +700,7 @@ spk_status kv_pages_reserve(const spk_pages_shape* s, void* k_pages, void* v_pag
   if (st != SPK_OK) return st;
   if (result == nullptr || (n > 0 && (seqs == nullptr || n_new == nullptr)))
     return fail(SPK_ERR_ARG, "seqs, n_new and result must be non-NULL device pointers");
+  if ((st = check_lists({seqs, n_new, result})) != SPK_OK) return st;
   if ((st = check_pages_ws(ws, ws_bytes, pages_ws_bytes(n, s->max_pages))) != SPK_OK) return st;
   cudaError_t e = launch_pages_reserve(pages_shape(s), {refs, table, lens}, k_pages, v_pages, seqs, n_new, n, result,
                                        ws, static_cast<cudaStream_t>(stream));
@@ -717,6 +725,7 @@ spk_status kv_pages_write(const spk_pages_shape* s, const void* k, const void* v
   if (k == nullptr || v == nullptr || seqs == nullptr)
     return fail(SPK_ERR_ARG, "k, v and seqs must be non-NULL device pointers");
   if (!aligned16(k) || !aligned16(v)) return fail(SPK_ERR_ARG, "k and v must be 16-byte aligned");
+  if ((st = check_lists({idx, counts, seqs, reserved})) != SPK_OK) return st;
   if (idx == nullptr && n_idx > n_src) return fail(SPK_ERR_ARG, "without idx, n_idx (%d) is at most n_src (%d)", n_idx, n_src);
   cudaError_t e = launch_pages_write(pages_shape(s), {const_cast<int*>(refs), const_cast<int*>(table), const_cast<int*>(lens)},
                                      k, v, n_src, idx, n_idx, units_per_idx, counts, seqs, n, k_pages, v_pages, reserved,
@@ -740,6 +749,7 @@ spk_status kv_pages_compact(const spk_pages_shape* s, void* k_pages, void* v_pag
     return fail(SPK_ERR_ARG, "n * layers * hkv (%lld) must be a multiple of units_per_idx (%d)", units, units_per_idx);
   if (result == nullptr || (n > 0 && (src == nullptr || dst == nullptr || (n_idx > 0 && idx == nullptr))))
     return fail(SPK_ERR_ARG, "src, dst, idx and result must be non-NULL device pointers");
+  if ((st = check_lists({src, dst, idx, result})) != SPK_OK) return st;
   if ((st = check_pages_ws(ws, ws_bytes, pages_ws_bytes(n, s->max_pages))) != SPK_OK) return st;
   cudaError_t e = launch_pages_compact(pages_shape(s), {refs, table, lens}, k_pages, v_pages, src, dst, n, idx, n_idx,
                                        units_per_idx, result, ws, static_cast<cudaStream_t>(stream));
@@ -754,6 +764,7 @@ spk_status kv_pages_fork(const spk_pages_shape* s, int32_t* refs, int32_t* table
   if (st != SPK_OK) return st;
   if (result == nullptr || (n > 0 && (src == nullptr || dst == nullptr)))
     return fail(SPK_ERR_ARG, "src, dst and result must be non-NULL device pointers");
+  if ((st = check_lists({src, dst, n_rows, result})) != SPK_OK) return st;
   if ((st = check_pages_ws(ws, ws_bytes, pages_ws_bytes(n, s->max_pages))) != SPK_OK) return st;
   PagesShape g{1, s->n_pages, 1, s->page_rows, 1, s->n_seqs, s->max_pages};
   cudaError_t e = launch_pages_fork(g, {refs, table, lens}, src, dst, n_rows, n, result, ws,
@@ -768,6 +779,7 @@ spk_status kv_pages_free(const spk_pages_shape* s, int32_t* refs, int32_t* table
   if (st != SPK_OK) return st;
   if (n == 0) return ok();
   if (seqs == nullptr) return fail(SPK_ERR_ARG, "seqs must be a non-NULL device pointer");
+  if ((st = check_lists({seqs, keep_rows})) != SPK_OK) return st;
   PagesShape g{1, s->n_pages, 1, s->page_rows, 1, s->n_seqs, s->max_pages};
   cudaError_t e = launch_pages_free(g, {refs, table, lens}, seqs, keep_rows, n, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ok() : cuda_fail(e, "kv_pages_free launch");

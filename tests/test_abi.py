@@ -194,6 +194,14 @@ def test_pages_pointer_and_workspace_errors(lib):
     assert lib.kv_pages_free(s, 16, None, 16, 16, None, 2, None) == B.SPK_ERR_ARG
     assert lib.kv_pages_free(s, 16, 16, 16, None, None, 2, None) == B.SPK_ERR_ARG
     assert lib.kv_pages_free(s, 16, 16, 16, None, None, 0, None) == B.SPK_OK                             # nothing to do
+    book = (16, 16, 16)
+    for bad in ((18, 16, 16), (16, 18, 16), (16, 16, 18)):            # a list or *result off its alignment
+        assert lib.kv_pages_reserve(s, 16, 16, *book, bad[0], bad[1], 2, bad[2], 16, 1 << 20, None) == B.SPK_ERR_ARG
+        assert lib.kv_pages_fork(s, *book, bad[0], 16, bad[1], 2, bad[2], 16, 1 << 20, None) == B.SPK_ERR_ARG
+        assert lib.kv_pages_compact(s, 16, 16, *book, bad[0], 16, 2, bad[1], 3, 1, bad[2], 16, 1 << 20, None) == B.SPK_ERR_ARG
+        assert lib.kv_pages_write(s, 16, 16, 4, bad[0], 4, 1, bad[1], *book, 16, 2, 16, 16, bad[2], None) == B.SPK_ERR_ARG
+    assert lib.kv_pages_free(s, *book, 18, None, 2, None) == B.SPK_ERR_ARG
+    assert lib.kv_pages_free(s, *book, 16, 18, 2, None) == B.SPK_ERR_ARG
     w = lambda **k: lib.kv_pages_write(s, k.get("k", 16), 16, k.get("n_src", 4), k.get("idx"), k.get("n_idx", 4),  # noqa: E731
                                        k.get("per", 1), None, 16, 16, 16, 16, 2, 16, 16, None, None)
     assert w(per=3) == B.SPK_ERR_ARG and w(per=0) == B.SPK_ERR_ARG and w(n_idx=5) == B.SPK_ERR_ARG
