@@ -15,7 +15,7 @@
 // then in two shares at most) the share that arrives last does it; otherwise
 // tree_join_kernel, which spreads the many shares of an item over the GPU.
 // (16 nodes over 320 rows, 512 KV heads: 33 us the one way, 37 the other; one
-// node over 16K rows, 8 KV heads in 37 shares each: 37 and 22 us.)
+// node over 16K rows, 8 KV heads in 37 shares each: 37 and 20 us.)
 #include <type_traits>
 
 #include "common.cuh"
@@ -503,27 +503,32 @@ __global__ void __launch_bounds__(kThreads, 2)
 // A row's shares are added in their order:
 //   M = max m_c,  out = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c.
 // A block has eight rows of one item at a time; a thread has four columns of a
-// row, and adds them over the shares, four shares' loads in flight together.  MANY (an
-// item has many shares): four groups of such threads, each with every fourth
-// share, joined through shared memory in the groups' order.
+// row, and adds them over the shares, four shares' loads in flight together.
+// MANY (an item has many shares): a block has 16 columns, and eight groups of
+// such threads, each with every eighth share and eight loads in flight, joined
+// through shared memory in the groups' order; blocks of 256 threads, so that
+// they are resident beside the main kernel's.  (One node over 16K rows, 8 KV
+// heads in 37 shares each: 19.7 us; blocks of 1024 threads with all columns
+// and four groups, which start only when the main kernel's end: 22.0 us.)
 // by_border: the item that the border between shares c and c + 1 cuts, if this
 // is the first border inside it; otherwise item c of the call.  The blocks
 // start while the main kernel still runs and find their item (the line does
 // not depend on it), and wait before they read; every block waits, so the
 // join ends after the main kernel.
 constexpr int kJoinRows = 8;
-constexpr int kJoinGroups = 4;                  // MANY
+constexpr int kJoinGroups = 8;                  // MANY
+constexpr int kJoinCols = 4;                    // MANY: columns of a block, in fours (part blockIdx.z of them)
 
 template <typename T, int D, int KEYS, bool PAIRS, bool MANY>
-__global__ void __launch_bounds__(kJoinRows * (D / 4) * (MANY ? kJoinGroups : 1))
+__global__ void __launch_bounds__(kJoinRows *(MANY ? kJoinCols * kJoinGroups : D / 4))
     tree_join_kernel(const __grid_constant__ TreeParams p, int item_rows, bool by_border) {
-  constexpr int kGroup = kJoinRows * (D / 4);   // threads that hold eight rows
+  constexpr int kGroup = kJoinRows * (MANY ? kJoinCols : D / 4);   // threads that hold eight rows
   constexpr int G = MANY ? kJoinGroups : 1;
   __shared__ float4 acc_s[MANY ? kGroup * (G - 1) : 1];
   __shared__ float2 ml_s[MANY ? kGroup * (G - 1) : 1];
   const int lane = threadIdx.x & 31;
   const int group = threadIdx.x / kGroup, me = threadIdx.x % kGroup;
-  const int col4 = me / kJoinRows;
+  const int col4 = (MANY ? blockIdx.z * kJoinCols : 0) + me / kJoinRows;
   TreeStart s = tree_start<KEYS>(p, by_border ? blockIdx.x + 1 : 0, false);
   int x = s.begin;
   if (!by_border) {                             // every unit has the same number of items
@@ -565,11 +570,12 @@ __global__ void __launch_bounds__(kJoinRows * (D / 4) * (MANY ? kJoinGroups : 1)
       m = M;
     };
     if (on) {
-      for (int i0 = c0 + group; i0 <= c1; i0 += 4 * G) {
-        float2 ml[4];
-        float4 o[4];
+      constexpr int U = MANY ? 8 : 4;
+      for (int i0 = c0 + group; i0 <= c1; i0 += U * G) {
+        float2 ml[U];
+        float4 o[U];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < U; ++u) {
           const int i = i0 + u * G;
           int t0 = 0, t1 = 0, slot = 0;
           if (i <= c1) tree_part(item, s.e.tiles, i * s.share, (i + 1) * s.share, t0, t1, slot);
@@ -582,7 +588,7 @@ __global__ void __launch_bounds__(kJoinRows * (D / 4) * (MANY ? kJoinGroups : 1)
           }
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) add(ml[u], o[u]);
+        for (int u = 0; u < U; ++u) add(ml[u], o[u]);
       }
     }
     if (MANY) {
@@ -614,9 +620,10 @@ cudaError_t launch_join(const TreeParams& p, const TreePlan& plan, cudaStream_t 
   cudaLaunchConfig_t cfg = {};
   // blocks that are resident together, beside the main kernel's: six an SM
   const unsigned x = by_border ? plan.ctas - 1 : static_cast<unsigned>(items);
-  const unsigned most = ((many ? 1u : 6u) * p.sms + x - 1) / x, want = (rows + kJoinRows - 1) / kJoinRows;
-  cfg.gridDim = dim3(x, want < most ? want : most);
-  cfg.blockDim = dim3(kJoinRows * (D / 4) * (many ? kJoinGroups : 1));
+  const unsigned z = many ? D / 4 / kJoinCols : 1;
+  const unsigned most = (6u * p.sms + x * z - 1) / (x * z), want = (rows + kJoinRows - 1) / kJoinRows;
+  cfg.gridDim = dim3(x, want < most ? want : most, z);
+  cfg.blockDim = dim3(kJoinRows * (many ? kJoinCols * kJoinGroups : D / 4));
   cfg.stream = stream;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
