@@ -807,7 +807,7 @@ static spk_status check_tree(const spk_tree_shape* s) {
     return fail(SPK_ERR_UNSUPPORTED, "too many units, rows or pages");
   // jobs of all units: 32-bit on the device
   const TreePlan plan = tree_plan(static_cast<int>(rows), s->head_dim, num_sms());
-  const double tiles = static_cast<double>(most / plan.keys + 1 + s->n_nodes / plan.keys + 1);
+  const double tiles = static_cast<double>(most / plan.keys + 1 + s->n_nodes / plan.keys + 1 + kTreeItemJobs);
   if (static_cast<double>(s->batch) * units * plan.row_tiles * tiles > 2.0e9)
     return fail(SPK_ERR_UNSUPPORTED, "too many key tiles over all units");
   return SPK_OK;
@@ -878,6 +878,7 @@ spk_status tree_attention(const spk_tree_shape* s, const void* q, const void* k_
   p.rows = g * s->n_nodes;
   p.tile_rows = plan.tile_rows;
   p.row_tiles = plan.row_tiles;
+  p.items = plan.items;
   p.item_rows = plan.item_rows;
   p.has_tree = k_tree != nullptr;
   p.n_seqs = s->n_seqs; p.max_pages = s->max_pages; p.n_pages = s->n_pages; p.page_rows = s->page_rows;

@@ -48,6 +48,7 @@ cudaError_t device_errors_pages(int* code, int* site, bool clear);
 // ---------------------------------------------------- tree.cu, tree_umma.cu
 constexpr int kTreeMaxBatch = 1024;
 constexpr int kTreeMaxNodes = 1024;
+constexpr int kTreeItemJobs = 4;   // what starting an item costs, in jobs (tcgen05 kernel)
 
 struct TreeParams {
   const void* q;           // [batch][layers][hq][T][d]
@@ -64,6 +65,7 @@ struct TreeParams {
   int rows;                // query rows per unit = g * T, ordered [query head][node]
   int tile_rows;           // query rows of a row tile (wide kernel: 128)
   int row_tiles;           // row tiles per unit
+  int items;               // items per unit
   int item_rows;           // rows of an item, in the partial results
   int has_tree;            // k_tree and v_tree are given
   int n_seqs, max_pages, n_pages, page_rows;

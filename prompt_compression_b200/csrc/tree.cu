@@ -532,21 +532,23 @@ __global__ void __launch_bounds__(kJoinRows *(MANY ? kJoinCols * kJoinGroups : D
   TreeStart s = tree_start<KEYS>(p, by_border ? blockIdx.x + 1 : 0, false);
   int x = s.begin;
   if (!by_border) {                             // every unit has the same number of items
-    const int per = PAIRS ? (p.row_tiles + 1) / 2 : p.row_tiles;
+    const int per = p.items;
     const int unit = blockIdx.x / per, k = blockIdx.x - unit * per, of_b = p.layers * p.hkv;
     s.b = unit / of_b;
     int before = 0;
-    for (int b = lane; b < s.b; b += 32) before += tree_jobs(p, tree_element<KEYS>(p, b, false));
+    for (int b = lane; b < s.b; b += 32) before += tree_jobs(p, tree_element<KEYS>(p, b, false), s.extra);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
     s.base = before;
     s.e = tree_element<KEYS>(p, s.b, false);
-    x = s.e.tiles == 0 ? s.total : before + (unit - s.b * of_b) * s.e.tiles * p.row_tiles + k * s.e.tiles * (PAIRS ? 2 : 1);
+    x = s.e.tiles == 0 ? s.total
+                       : before + (unit - s.b * of_b) * tree_unit_jobs(p, s.e.tiles, s.extra) +
+                             k * (s.e.tiles * (PAIRS ? 2 : 1) + s.extra);
   }
   TreeItem item{};
   int c0 = 0, c1 = 0;
   if (x < s.total) {
-    item = tree_item<PAIRS>(p, s.e, s.b, s.base, x);
+    item = tree_item<PAIRS>(p, s.e, s.b, s.base, x, s.extra);
     const bool mine = !by_border || (item.first != x && item.first / s.share == static_cast<int>(blockIdx.x));
     if (mine) tree_spread(item, s.e.tiles, s.share, c0, c1);
   }

@@ -102,12 +102,17 @@ __device__ __forceinline__ uint32_t tree_word(const TreeParams& p, int b, const 
   return w | v;
 }
 
-__device__ __forceinline__ int tree_jobs(const TreeParams& p, const TreeElement& e) {
-  return e.tiles * p.row_tiles * p.layers * p.hkv;
+// Jobs of one unit of an element, and of all its units.
+__device__ __forceinline__ int tree_unit_jobs(const TreeParams& p, int tiles, int extra) {
+  return tiles == 0 ? 0 : tiles * p.row_tiles + extra * p.items;
+}
+__device__ __forceinline__ int tree_jobs(const TreeParams& p, const TreeElement& e, int extra) {
+  return tree_unit_jobs(p, e.tiles, extra) * p.layers * p.hkv;
 }
 
 struct TreeStart {
   int total, share;
+  int extra;               // jobs in front of an item's tiles
   int begin, end;          // the CTA's jobs
   int b, base;             // the batch element that holds `begin`, and the jobs before it
   TreeElement e;           // that element
@@ -120,17 +125,27 @@ __device__ __forceinline__ TreeStart tree_start(const TreeParams& p, int cta, bo
   TreeStart s;
   TreeElement first = {0, 0, 0, 0};
   if (lane < p.batch) first = tree_element<KEYS>(p, lane, record);
-  int jobs = tree_jobs(p, first);
-  for (int b = lane + 32; b < p.batch; b += 32) jobs += tree_jobs(p, tree_element<KEYS>(p, b, record));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) jobs += __shfl_xor_sync(0xffffffffu, jobs, o);
+  int jobs = tree_jobs(p, first, 0), full = first.tiles > 0;     // tiles; elements with any
+  for (int b = lane + 32; b < p.batch; b += 32) {
+    const TreeElement e = tree_element<KEYS>(p, b, record);
+    jobs += tree_jobs(p, e, 0);
+    full += e.tiles > 0;
+  }
+  jobs = __reduce_add_sync(0xffffffffu, jobs);
+  // What starting an item costs (Q, the first loads, the outputs: 4 to 5 us against
+  // 1.1 us a job) goes into the line as jobs in front of its tiles, where shares
+  // are long enough: otherwise the CTAs whose share falls on many short sequences
+  // end last.  (16 ragged sequences of up to 8192 rows, 24 nodes: 70.6 us without,
+  // 58.5 us with; 61.4 and 59.5 us for 2 and 6 jobs.)
+  s.extra = KEYS == 128 && jobs / p.ctas >= 2 * kTreeItemJobs ? kTreeItemJobs : 0;
   s.total = jobs;
+  if (s.extra > 0) s.total += __reduce_add_sync(0xffffffffu, full) * s.extra * p.items * p.layers * p.hkv;
   // (two jobs at least where items are pairs: no share inside an item is then without a tile)
   s.share = max(p.row_tiles > 1 ? 2 : 1, (s.total + p.ctas - 1) / p.ctas);
   // whole units where that costs few jobs more: no unit is then cut and joined
-  const int unit = p.row_tiles * __shfl_sync(0xffffffffu, first.tiles, 0);
+  const int tiles = __shfl_sync(0xffffffffu, first.tiles, 0), unit = tree_unit_jobs(p, tiles, s.extra);
   bool same = unit > 0;
-  for (int b = lane; b < p.batch; b += 32) same = same && (b < 32 ? first : tree_element<KEYS>(p, b, false)).tiles * p.row_tiles == unit;
+  for (int b = lane; b < p.batch; b += 32) same = same && (b < 32 ? first : tree_element<KEYS>(p, b, false)).tiles == tiles;
   if (__all_sync(0xffffffffu, same)) {
     const int whole = (s.share + unit - 1) / unit * unit;
     if (whole - s.share <= kJoinJobs) s.share = whole;
@@ -145,7 +160,7 @@ __device__ __forceinline__ TreeStart tree_start(const TreeParams& p, int cta, bo
     const int b = b0 + lane;
     TreeElement e = {0, 0, 0, 0};
     if (b0 == 0) e = first; else if (b < p.batch) e = tree_element<KEYS>(p, b, false);
-    const int x = tree_jobs(p, e);
+    const int x = tree_jobs(p, e, s.extra);
     int sum = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -169,35 +184,29 @@ __device__ __forceinline__ TreeStart tree_start(const TreeParams& p, int cta, bo
   return s;                                                    // no jobs: begin == end == total
 }
 
-// An item as the line holds it: jobs [first, first + jobs).
+// An item as the line holds it: jobs [first, first + jobs), `extra` of them
+// before its tiles.
 struct TreeItem {
   int unit, row0;          // unit = (b * layers + l) * hkv + h
   bool pair;
-  int first, jobs;
+  int first, jobs, extra;
 };
 
 // The item that holds job x of batch element b, whose jobs begin at base.
 template <bool PAIRS>
-__device__ __forceinline__ TreeItem tree_item(const TreeParams& p, const TreeElement& e, int b, int base, int x) {
+__device__ __forceinline__ TreeItem tree_item(const TreeParams& p, const TreeElement& e, int b, int base, int x, int extra) {
   TreeItem i;
-  const int per = e.tiles * p.row_tiles;                       // jobs of a unit
+  const int per = tree_unit_jobs(p, e.tiles, extra);           // jobs of a unit
   const int y = x - base;
   const int lh = y / per;
   const int z = y - lh * per;
   i.unit = b * p.layers * p.hkv + lh;
-  if (PAIRS) {
-    const int k = z / (2 * e.tiles);
-    i.pair = 2 * k + 1 < p.row_tiles;
-    i.row0 = k * 256;
-    i.first = base + lh * per + k * 2 * e.tiles;
-    i.jobs = i.pair ? 2 * e.tiles : e.tiles;
-  } else {
-    const int k = z / e.tiles;
-    i.pair = false;
-    i.row0 = k * p.tile_rows;
-    i.first = base + lh * per + k * e.tiles;
-    i.jobs = e.tiles;
-  }
+  i.extra = extra;
+  const int jobs = (PAIRS ? 2 : 1) * e.tiles + extra, k = z / jobs;
+  i.first = base + lh * per + k * jobs;
+  i.pair = PAIRS && 2 * k + 1 < p.row_tiles;
+  i.row0 = k * (PAIRS ? 256 : p.tile_rows);
+  i.jobs = PAIRS && !i.pair ? e.tiles + extra : jobs;
   return i;
 }
 
@@ -205,14 +214,16 @@ __device__ __forceinline__ TreeItem tree_item(const TreeParams& p, const TreeEle
 // they are its slot 1 (the item starts behind the share's first job) or 0 of
 // the share's two places for partial results.
 __device__ __forceinline__ void tree_part(const TreeItem& i, int tiles, int begin, int end, int& t0, int& t1, int& slot) {
-  const int lo = max(begin, i.first) - i.first, hi = min(end, i.first + i.jobs) - i.first;
+  const int last = i.jobs - i.extra;
+  const int lo = max(0, max(begin, i.first) - i.first - i.extra), hi = max(0, min(end, i.first + i.jobs) - i.first - i.extra);
   t0 = i.pair ? lo >> 1 : lo;
-  t1 = hi == i.jobs ? tiles : (i.pair ? hi >> 1 : hi);
+  t1 = hi == last ? tiles : (i.pair ? hi >> 1 : hi);
   slot = i.first > begin ? 1 : 0;
 }
 
-// The shares [from, to] that hold tiles of an item (a pair's border inside its
-// first tile leaves the share before it without one, and so for the last).
+// The shares [from, to] that hold tiles of an item (a border before or, of a
+// pair, inside its first tile leaves the share before it without one, and so
+// for the last; a share is longer than that part).
 __device__ __forceinline__ void tree_spread(const TreeItem& i, int tiles, int share, int& from, int& to) {
   int t0, t1, slot;
   from = i.first / share;
@@ -235,19 +246,19 @@ struct TreeRun {           // a part of an item that a CTA works on
 
 template <int KEYS, bool PAIRS>
 struct TreeWalker {
-  int begin, end, x, b, base, share;
+  int begin, end, x, b, base, share, extra;
   TreeElement e;
   __device__ __forceinline__ explicit TreeWalker(const TreeStart& s)
-      : begin(s.begin), end(s.end), x(s.begin), b(s.b), base(s.base), share(s.share), e(s.e) {}
+      : begin(s.begin), end(s.end), x(s.begin), b(s.b), base(s.base), share(s.share), extra(s.extra), e(s.e) {}
   __device__ __forceinline__ bool next(const TreeParams& p, TreeRun& r) {
     while (x < end) {
-      int jobs = tree_jobs(p, e);
+      int jobs = tree_jobs(p, e, extra);
       while (x >= base + jobs) {
         base += jobs;
         e = tree_element<KEYS>(p, ++b, false);
-        jobs = tree_jobs(p, e);
+        jobs = tree_jobs(p, e, extra);
       }
-      const TreeItem i = tree_item<PAIRS>(p, e, b, base, x);
+      const TreeItem i = tree_item<PAIRS>(p, e, b, base, x, extra);
       tree_part(i, e.tiles, begin, end, r.t0, r.t1, r.slot);
       r.b = b;
       r.unit = i.unit;
