@@ -48,7 +48,7 @@ cudaError_t device_errors_pages(int* code, int* site, bool clear);
 // ---------------------------------------------------- tree.cu, tree_umma.cu
 constexpr int kTreeMaxBatch = 1024;
 constexpr int kTreeMaxNodes = 1024;
-constexpr int kTreeItemJobs = 4;   // what starting an item costs, in jobs (tcgen05 kernel)
+constexpr int kTreeItemJobs = 4;   // what starting an item costs, in jobs
 
 struct TreeParams {
   const void* q;           // [batch][layers][hq][T][d]
