@@ -14,7 +14,7 @@
 // timing.  Where there are at least twice as many items as CTAs (an item is
 // then in two shares at most) the share that arrives last does it; otherwise
 // tree_join_kernel, which spreads the many shares of an item over the GPU.
-// (16 nodes over 320 rows, 512 KV heads: 33 us the one way, 37 the other; one
+// (16 nodes over 320 rows, 512 KV heads: 38 us the one way, 43 the other; one
 // node over 16K rows, 8 KV heads in 37 shares each: 37 and 20 us.)
 #include <type_traits>
 
