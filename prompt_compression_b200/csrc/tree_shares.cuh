@@ -137,8 +137,11 @@ __device__ __forceinline__ TreeStart tree_start(const TreeParams& p, int cta, bo
   // are long enough: otherwise the CTAs whose share falls on many short sequences
   // end last.  (16 ragged sequences of up to 8192 rows, 24 nodes: 70.6 us without,
   // 58.5 us with; 61.4 and 59.5 us for 2 and 6 jobs.  Narrow kernel, 64 sequences
-  // of up to 2048 rows, 8 nodes: 93.8 us without, 68.2 us with; 71.4 us for 6 jobs.)
-  s.extra = jobs / p.ctas >= 2 * kTreeItemJobs ? kTreeItemJobs : 0;
+  // of up to 2048 rows, 8 nodes: 93.8 us without, 68.2 us with; 71.4 us for 6 jobs.
+  // Below four jobs a share the start of an item could fill a share.  From four on
+  // against from eight on: 24 sequences of up to 1000 rows, 24 nodes: 32.6 and 45.9
+  // us; two of 6000 rows each, 24 nodes: 29.6 and 29.1 us.)
+  s.extra = jobs / p.ctas >= kTreeItemJobs ? kTreeItemJobs : 0;
   s.total = jobs;
   if (s.extra > 0) s.total += __reduce_add_sync(0xffffffffu, full) * s.extra * p.items * p.layers * p.hkv;
   // (two jobs at least where items are pairs: no share inside an item is then without a tile)

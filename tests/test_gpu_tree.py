@@ -312,6 +312,26 @@ def test_many_runs_of_one_query_tile_that_end_in_ragged_tiles(P):
         assert torch.equal(o, out) and torch.equal(l, lse2)
 
 
+@pytest.mark.parametrize("case", [
+    # seed, B, hq, hkv, d, T, page, most: shares of a few jobs more than an item's start
+    # counts for, so that borders fall before an item's first tile
+    (60, 24, 32, 8, 128, 24, 32, 900),           # tcgen05, one query tile
+    (61, 10, 32, 8, 64, 40, 24, 1100),           # pairs of query tiles
+    (62, 40, 16, 8, 128, 3, 16, 800),            # 320 units of six rows
+])
+def test_borders_before_the_first_tile_of_an_item(P, case):
+    import torch
+    seed, B, hq, hkv, d, T, page, most = case
+    rng = np.random.default_rng(seed)
+    lens = [0 if b % 7 == 3 else int(x) for b, x in enumerate(rng.integers(1, most, B))]
+    live = [0 if b % 11 == 5 else int(x) for b, x in enumerate(rng.integers(1, T + 1, B))]
+    t, h = build_case(seed, torch.bfloat16, B, 1, hq, hkv, d, T, page, lens, live, "tree")
+    out, lse2 = check(P, t, h, torch.bfloat16)
+    o, l = torch.full_like(out, 7.0), torch.full_like(lse2, 7.0)
+    P.tree_attention(**t, out=o, lse2=l)
+    assert torch.equal(o, out) and torch.equal(l, lse2)
+
+
 def test_long_rows_of_two_query_tiles_and_more(P):
     import torch
     t, h = build_case(50, torch.bfloat16, 1, 1, 10, 2, 64, 64, 64, [6000], None, "tree")      # 320 rows, 47 tiles
