@@ -43,6 +43,9 @@ __host__ __device__ __forceinline__ int* ws_words(void* ws, int n, int max_pages
 }
 
 // The rows' kernel starts while the bookkeeping's runs, and waits for its end.
+// What the bookkeeping leaves for it (words, old) comes by plain pointers:
+// `const __restrict__` says that nobody writes the data while the kernel runs,
+// and lets the compiler load it from the non-coherent cache or above the wait.
 __device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
@@ -258,7 +261,7 @@ __global__ void __launch_bounds__(kBookThreads)
 // Block (i, y): rows 0 .. rows-1 of the copied page of sequence i, for the
 // (layer, KV head) blocks y, y + gridDim.y, ... of K and V.
 __global__ void __launch_bounds__(256)
-    copy_tail_kernel(PagesShape s, const int* __restrict__ words, uint4* __restrict__ k, uint4* __restrict__ v) {
+    copy_tail_kernel(PagesShape s, const int* words, uint4* __restrict__ k, uint4* __restrict__ v) {
   wait_for_previous();
   const int from = words[4 * blockIdx.x], to = words[4 * blockIdx.x + 1];
   if (to < 0) return;
@@ -474,7 +477,7 @@ __device__ __forceinline__ long long pool_row(const PagesShape& s, int lh, int p
 // that src[i] had (`old`).
 __global__ void __launch_bounds__(256)
     compact_rows_kernel(PagesShape s, PagesBook b, const int* __restrict__ dst, int n_idx, const int* __restrict__ idx,
-                        int units_per_idx, const int* __restrict__ old, const int* __restrict__ words, uint4* k, uint4* v) {
+                        int units_per_idx, const int* old, const int* words, uint4* k, uint4* v) {
   __shared__ long long from_s[kCopyRows], to_s[kCopyRows];
   const int chunks = (n_idx + kCopyRows - 1) / kCopyRows;
   const int lh_all = s.layers * s.hkv;
