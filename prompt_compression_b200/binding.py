@@ -522,6 +522,13 @@ def _new_on(stream, t: torch.Tensor, shape, dtype) -> torch.Tensor:
     return out
 
 
+def _output_on(stream, t: torch.Tensor, shape, dtype) -> torch.Tensor:
+    """An output on t's device of a call on `stream` (None: the current one)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=t.device)
+    return _new_on(stream, t, shape, dtype)
+
+
 def _pages_scratch(workspace, shape: "PagesShape", n: int, stream, t: torch.Tensor):
     return workspace if workspace is not None else _workspace(None, kv_pages_workspace_size(shape, n), t.device, stream)
 

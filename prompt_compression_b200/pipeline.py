@@ -140,8 +140,8 @@ def speckv_compress_pages(q, k, v, n_window: int, c_max: int, cache: PagedCache,
     n_pre = n_in - n_window
     keep = min(c_max, n_pre) + n_window
     units = Bsz * L * hkv
-    scores = torch.empty((units, n_pre), dtype=torch.float32, device=q.device)
-    idx = torch.empty((units, keep), dtype=torch.int32, device=q.device)
+    scores = B._output_on(stream, q, (units, n_pre), torch.float32)
+    idx = B._output_on(stream, q, (units, keep), torch.int32)
     B.speckv_score(q, k, n_window, scores, None, None, scale, stream)
     B.topk_select(scores, c_max, n_window, idx, pool, None, None, stream, pool_mode)
     with torch.cuda.stream(B._stream_object(stream, q.device)):

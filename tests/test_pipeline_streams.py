@@ -1,0 +1,84 @@
+"""The pipelines on a stream that is not the caller's: what they allocate must
+be known to both streams, so that the allocator does not hand its memory to
+either while the other still uses it."""
+import contextlib
+
+import pytest
+import torch
+
+from prompt_compression_b200 import binding as B
+from prompt_compression_b200 import pipeline
+
+
+@pytest.fixture
+def recorded(monkeypatch):
+    """Operators replaced by recorders; the tensors that _new_on hands out."""
+    made, used = [], []
+
+    def new_on(stream, t, shape, dtype):
+        assert stream == 1234
+        made.append(torch.empty(shape, dtype=dtype))
+        return made[-1]
+
+    monkeypatch.setattr(B, "_new_on", new_on)
+    monkeypatch.setattr(B, "_stream_object", lambda stream, device: stream)
+    monkeypatch.setattr(B.torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    for name, outs in (("speckv_score", (3,)), ("specpc_score", (3,)), ("topk_select", (0, 3)), ("kv_compact", (2, 3, 4))):
+        monkeypatch.setattr(B, name, lambda *a, _o=outs, **k: used.extend(a[x] for x in _o if x < len(a)))
+    return made, used
+
+
+class _Cache:
+    k_pages = torch.zeros((2, 9, 2, 16, 64), dtype=torch.bfloat16)
+
+    def reserve(self, seqs, n_new, stream=None):
+        return torch.zeros(1, dtype=torch.int32)
+
+    def write(self, k, v, seqs, **kw):
+        self.wrote = kw
+
+
+def _inputs():
+    q = torch.zeros((1, 2, 4, 20, 64), dtype=torch.bfloat16)
+    k = torch.zeros((1, 2, 2, 300, 64), dtype=torch.bfloat16)
+    return q, k, torch.zeros_like(k)
+
+
+def test_scores_and_rows_of_speckv_compress_pages_belong_to_both_streams(recorded):
+    made, used = recorded
+    cache, seqs = _Cache(), torch.zeros(1, dtype=torch.int32)
+    scores, idx, _ = pipeline.speckv_compress_pages(*_inputs(), 16, 32, cache, seqs, stream=1234)
+    known = {id(t) for t in made}
+    assert id(scores) in known and id(idx) in known and id(cache.wrote["idx"]) in known
+    assert {id(t) for t in used} <= known
+
+
+@pytest.mark.gpu
+def test_speckv_compress_pages_whose_results_are_dropped():
+    # the side stream is kept busy, the call's outputs are dropped and their sizes allocated and
+    # filled again on the caller's stream before the side stream comes to the call
+    from prompt_compression_b200 import build
+    build.build_library()
+    import prompt_compression_b200 as P
+    P.spk_device_error(clear=True)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q, k, v = (torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)
+               for s in ((1, 2, 4, 20, 64), (1, 2, 2, 300, 64), (1, 2, 2, 300, 64)))
+    seqs, caches = torch.zeros(1, dtype=torch.int32, device="cuda"), []
+    side = torch.cuda.Stream()
+    for stream in (None, side):
+        cache = P.PagedCache(2, 8, 2, 16, 64, n_seqs=1, max_pages=8)
+        cache.k_pages.zero_(), cache.v_pages.zero_()
+        torch.cuda.synchronize()
+        if stream is not None:
+            with torch.cuda.stream(side):
+                torch.cuda._sleep(200_000_000)                      # about 0.1 s
+        P.speckv_compress_pages(q, k, v, 16, 32, cache, seqs, stream=stream)
+        again = [torch.full(s, 7, dtype=t, device="cuda")
+                 for s, t in (((4, 284), torch.float32), ((4, 48), torch.int32)) for _ in range(8)]
+        torch.cuda.synchronize()
+        assert all(bool((x == 7).all()) for x in again)
+        caches.append(cache)
+    for a, b in zip(caches[0].tensors, caches[1].tensors):
+        assert torch.equal(a, b)
+    assert P.spk_device_error() == (0, 0)
