@@ -146,6 +146,8 @@ def _stream_object(stream, device):
         return torch.cuda.current_stream(device)
     if isinstance(stream, torch.cuda.Stream):
         return stream
+    if int(stream) == 0:                       # (an ExternalStream of handle 0 is a stream of torch's pool)
+        return torch.cuda.default_stream(device)
     return torch.cuda.ExternalStream(int(stream), device=device)
 
 

@@ -82,3 +82,51 @@ def test_speckv_compress_pages_whose_results_are_dropped():
     for a, b in zip(caches[0].tensors, caches[1].tensors):
         assert torch.equal(a, b)
     assert P.spk_device_error() == (0, 0)
+
+
+def test_handle_0_is_the_default_stream(monkeypatch):
+    monkeypatch.setattr(B.torch.cuda, "default_stream", lambda device: ("default", device))
+    monkeypatch.setattr(B.torch.cuda, "ExternalStream", lambda handle, device: ("external", handle, device))
+    assert B._stream_object(0, "cuda:1") == ("default", "cuda:1")
+    assert B._stream_object(5, "cuda:1") == ("external", 5, "cuda:1")
+
+
+@pytest.mark.gpu
+def test_the_default_streams_handle_names_that_stream():
+    default = torch.cuda.default_stream()
+    assert default.cuda_stream == 0
+    assert B._stream_object(0, torch.device("cuda", 0)).cuda_stream == 0
+    side = torch.cuda.Stream()
+    assert B._stream_object(side.cuda_stream, torch.device("cuda", 0)).cuda_stream == side.cuda_stream
+
+
+@pytest.mark.gpu
+def test_speckv_compress_pages_on_handle_0():
+    # from a stream that is not the default one: the fill of the new lengths, the workspaces and the kernels
+    # all go to the default stream, behind what keeps it busy
+    from prompt_compression_b200 import build
+    build.build_library()
+    import prompt_compression_b200 as P
+    P.spk_device_error(clear=True)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    q, k, v = (torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)
+               for s in ((2, 2, 4, 20, 64), (2, 2, 2, 300, 64), (2, 2, 2, 300, 64)))
+    seqs, caches, got = torch.tensor([1, 0], dtype=torch.int32, device="cuda"), [], []
+    side = torch.cuda.Stream()
+    for handle in (None, 0):
+        cache = P.PagedCache(2, 8, 2, 16, 64, n_seqs=2, max_pages=8)
+        cache.k_pages.zero_(), cache.v_pages.zero_()
+        torch.cuda.synchronize()
+        if handle is None:
+            out = P.speckv_compress_pages(q, k, v, 16, 32, cache, seqs)
+        else:
+            torch.cuda._sleep(100_000_000)
+            with torch.cuda.stream(side):
+                out = P.speckv_compress_pages(q, k, v, 16, 32, cache, seqs, stream=handle)
+        torch.cuda.synchronize()
+        assert out[2].item() == 0
+        caches.append(cache)
+        got.append(out[:2])
+    for a, b in zip(caches[0].tensors + got[0], caches[1].tensors + got[1]):
+        assert torch.equal(a, b)
+    assert P.spk_device_error() == (0, 0)
