@@ -20,28 +20,30 @@ from . import binding as B
 
 
 class SpeckvBuffers:
-    """Preallocated outputs and scratch for repeated speckv_compress calls."""
+    """Preallocated outputs and scratch for repeated speckv_compress calls (on
+    `stream`, if they are not to run on the current one)."""
 
     def __init__(self, q, k, v, n_window: int, c_max: int, window_mass: bool = False,
-                 with_pooled: bool = False):
+                 with_pooled: bool = False, stream=None):
         Bsz, L, hq, R, d = q.shape
         _, _, hkv, n_in, _ = k.shape
         units = Bsz * L * hkv
         n_pre = n_in - n_window
         keep = min(c_max, n_pre) + n_window
-        dev = q.device
         shape = B.speckv_shape(q, k, n_window)
+
+        def empty(size, dtype):
+            return B._output_on(stream, q, size, dtype)
+
         self.units, self.n_pre, self.keep = units, n_pre, keep
-        self.scores = torch.empty((units, n_pre), dtype=torch.float32, device=dev)
-        self.window_mass = (torch.empty((units, n_window), dtype=torch.float32, device=dev)
-                            if window_mass else None)
-        self.pooled = torch.empty_like(self.scores) if with_pooled else None
-        self.idx = torch.empty((units, keep), dtype=torch.int32, device=dev)
-        self.k_out = torch.empty((Bsz, L, hkv, keep, d), dtype=k.dtype, device=dev)
-        self.v_out = torch.empty((Bsz, L, hkv, keep, d), dtype=v.dtype, device=dev) if v is not None else None
-        self.ws_score = torch.empty(max(B.speckv_workspace_size(shape), 256), dtype=torch.uint8, device=dev)
-        self.ws_topk = torch.empty(max(B.topk_workspace_size(units, n_pre), 256), dtype=torch.uint8,
-                                   device=dev)
+        self.scores = empty((units, n_pre), torch.float32)
+        self.window_mass = empty((units, n_window), torch.float32) if window_mass else None
+        self.pooled = empty((units, n_pre), torch.float32) if with_pooled else None
+        self.idx = empty((units, keep), torch.int32)
+        self.k_out = empty((Bsz, L, hkv, keep, d), k.dtype)
+        self.v_out = empty((Bsz, L, hkv, keep, d), v.dtype) if v is not None else None
+        self.ws_score = empty(max(B.speckv_workspace_size(shape), 256), torch.uint8)
+        self.ws_topk = empty(max(B.topk_workspace_size(units, n_pre), 256), torch.uint8)
 
 
 def speckv_compress(q, k, v, n_window: int, c_max: int, pool: int = 7, scale: float = 1.0,
@@ -49,7 +51,7 @@ def speckv_compress(q, k, v, n_window: int, c_max: int, pool: int = 7, scale: fl
                     pool_mode: int = B.SPK_POOL_MAX):
     """SpecKV on every unit: returns the buffers object (scores, idx, k_out, v_out).
     pool_mode: B.SPK_POOL_MAX (the workloads' max pool) or B.SPK_POOL_AVG."""
-    buf = buffers or SpeckvBuffers(q, k, v, n_window, c_max, window_mass=window_mass)
+    buf = buffers or SpeckvBuffers(q, k, v, n_window, c_max, window_mass=window_mass, stream=stream)
     B.speckv_score(q, k, n_window, buf.scores, buf.window_mass, buf.ws_score, scale, stream)
     B.topk_select(buf.scores, c_max, n_window, buf.idx, pool, buf.pooled, buf.ws_topk, stream, pool_mode)
     B.kv_compact(k, v, buf.idx, buf.k_out, buf.v_out, 1, stream)
@@ -62,9 +64,9 @@ def specpc_select(q, k, row_weights, l_skip: int, keep: int, pool: int = 7, n_lo
     Bsz = q.shape[0]
     n_in = k.shape[3]
     if scores is None:
-        scores = torch.empty((Bsz, n_in), dtype=torch.float32, device=q.device)
+        scores = B._output_on(stream, q, (Bsz, n_in), torch.float32)
     if idx is None:
-        idx = torch.empty((Bsz, min(keep, n_in)), dtype=torch.int32, device=q.device)
+        idx = B._output_on(stream, q, (Bsz, min(keep, n_in)), torch.int32)
     B.specpc_score(q, k, row_weights, scores, l_skip, n_lookahead, None, scale, stream)
     B.topk_select(scores, keep, 0, idx, pool, None, None, stream, pool_mode)
     return scores, idx
@@ -78,8 +80,8 @@ def cascade_compress(draft_q, draft_k, row_weights, l_skip: int, keep: int, targ
     Bsz, L, hkv, n_full, d = target_k.shape
     pc_scores, pc_idx = specpc_select(draft_q, draft_k, row_weights, l_skip, keep, pool, stream=stream)
     n_keep = pc_idx.shape[1]
-    k_g = torch.empty((Bsz, L, hkv, n_keep, d), dtype=target_k.dtype, device=target_k.device)
-    v_g = torch.empty_like(k_g)
+    k_g = B._output_on(stream, target_k, (Bsz, L, hkv, n_keep, d), target_k.dtype)
+    v_g = B._output_on(stream, target_k, k_g.shape, target_k.dtype)
     B.kv_compact(target_k, target_v, pc_idx, k_g, v_g, L * hkv, stream)
     out = speckv_compress(target_q, k_g, v_g, n_window, c_max, pool, stream=stream)
     return pc_scores, pc_idx, k_g, v_g, out

@@ -53,6 +53,20 @@ def test_scores_and_rows_of_speckv_compress_pages_belong_to_both_streams(recorde
     assert {id(t) for t in used} <= known
 
 
+def test_what_the_other_pipelines_allocate_belongs_to_both_streams(recorded, monkeypatch):
+    made, used = recorded
+    monkeypatch.setattr(B, "speckv_workspace_size", lambda shape: 1000)
+    monkeypatch.setattr(B, "topk_workspace_size", lambda units, n: 1000)
+    q, k, v = _inputs()
+    buf = pipeline.speckv_compress(q, k, v, 16, 32, stream=1234)
+    assert {id(x) for x in vars(buf).values() if torch.is_tensor(x)} <= {id(t) for t in made}
+    scores, idx = pipeline.specpc_select(q, k, torch.ones(4), 0, 40, stream=1234)
+    pc_scores, pc_idx, k_g, v_g, buf = pipeline.cascade_compress(q, k, torch.ones(4), 0, 200, q, k, v, 16, 32, stream=1234)
+    known = {id(t) for t in made}
+    assert {id(t) for t in (scores, idx, pc_scores, pc_idx, k_g, v_g, buf.scores, buf.ws_score)} <= known
+    assert {id(t) for t in used if t is not None} <= known
+
+
 @pytest.mark.gpu
 def test_speckv_compress_pages_whose_results_are_dropped():
     # the side stream is kept busy, the call's outputs are dropped and their sizes allocated and
