@@ -281,7 +281,7 @@ def speckv_prefill_attention(q, k, v, k_look, v_look, n_window: int, out=None, l
     else:
         k_look = v_look = None
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        out = _output_on(stream, q, q.shape, torch.bfloat16)
     _numel(out, "out", q.numel())
     _numel(lse2, "lse2", units * rows, required=False)
     ws_bytes = 0
@@ -428,7 +428,7 @@ def decode_attention(q, k, v, out=None, scale: float = 1.0, stream=None):
     if tuple(k.shape) != (Bsz, L, hkv, n_kv, d) or tuple(v.shape) != tuple(k.shape):
         raise ValueError("k and v must be [B, L, Hkv, n_kv, d] with q's B, L and d")
     if out is None:
-        out = torch.empty((Bsz, L, hq, d), dtype=torch.float32, device=q.device)
+        out = _output_on(stream, q, (Bsz, L, hq, d), torch.float32)
     _numel(out, "out", Bsz * L * hq * d)
     _check(lib.decode_attention(Bsz, L, hq, hkv, d, n_kv, float(scale), _dev(q, "q", torch.bfloat16),
                                 _dev(k, "k", torch.bfloat16), _dev(v, "v", torch.bfloat16),
@@ -468,7 +468,7 @@ def vs_sparse_attention(q, k, v, vertical, slash, out=None, lse2=None, workspace
     _numel(vertical, "vertical", units * n_v)
     _numel(slash, "slash", units * n_s)
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        out = _output_on(stream, q, q.shape, torch.bfloat16)
     _numel(out, "out", q.numel())
     _numel(lse2, "lse2", shape.batch * shape.layers * shape.hq * shape.n_q, required=False)
     ws = None

@@ -67,6 +67,23 @@ def test_what_the_other_pipelines_allocate_belongs_to_both_streams(recorded, mon
     assert {id(t) for t in used if t is not None} <= known
 
 
+def test_outputs_that_the_binding_makes_belong_to_both_streams(recorded, monkeypatch):
+    made, _ = recorded
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *a: 0
+
+    monkeypatch.setattr(B, "load_library", Library)
+    monkeypatch.setattr(B, "_dev", lambda t, *a: 0)
+    q, k, v = _inputs()
+    rows = torch.zeros((4, 3), dtype=torch.int32)
+    outs = [B.decode_attention(q[:, :, :, 0].contiguous(), k, v, stream=1234),
+            B.vs_sparse_attention(q, k, v, rows, rows, workspace=torch.zeros(8), stream=1234),
+            B.speckv_prefill_attention(q, k, v, k[:, :, :, :4], v[:, :, :, :4], 16, stream=1234)]
+    assert {id(t) for t in outs} <= {id(t) for t in made}
+
+
 @pytest.mark.gpu
 def test_speckv_compress_pages_whose_results_are_dropped():
     # the side stream is kept busy, the call's outputs are dropped and their sizes allocated and
