@@ -357,8 +357,8 @@ spk_status decode_attention(int batch, int layers, int hq, int hkv, int head_dim
  *
  * Lists of sequences (seqs, src, dst) are int32 device arrays of n <= 1024
  * entries.  *result (int32, device) tells what became of a call: 0 done; > 0
- * that many free pages were missing; -1 an argument was wrong (a sequence or a
- * count out of range, a destination listed twice), recorded as SPK_ERR_ARG in
+ * that many free pages were missing; -1 an argument was wrong (a sequence, its
+ * length or a count out of range, a destination listed twice), recorded as SPK_ERR_ARG in
  * the device error word too.  Unless it is 0 the call changed nothing.  Free
  * pages are taken lowest number first, for the sequences in the list's order.
  * page_table, seq_lens, page_refs and the lists need 4-byte alignment, the

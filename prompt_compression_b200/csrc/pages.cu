@@ -378,6 +378,11 @@ __global__ void __launch_bounds__(kBookThreads)
   }
   __syncthreads();
   bool bad = bad_list(src_s, n, s.n_seqs, false) | bad_list(dst_s, n, s.n_seqs, true);
+  for (int i = threadIdx.x; i < n; i += kBookThreads) {
+    if (src_s[i] < 0 || src_s[i] >= s.n_seqs) continue;
+    const int len = b.lens[src_s[i]];           // the rows' kernel finds pages by it
+    bad |= len < 0 || len > static_cast<long long>(s.max_pages) * s.page_rows;
+  }
   const bool first_cta = book_rank<CTAS>() == 0;
   if (__syncthreads_or(bad)) {
     refuse<CTAS>(result);

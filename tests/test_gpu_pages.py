@@ -408,3 +408,19 @@ def test_the_binding_refuses_what_does_not_fit(P):
         assert e.value.status == status
     c.check()
     c.no_error()
+
+
+@pytest.mark.parametrize("length", [-1, 81, 1 << 30])
+def test_a_length_beyond_the_table_is_refused(P, length):
+    c = Cache(P, 1, 20, 1, 16, 64, 4, 5, seed=14)
+    assert c.reserve([0, 1], [20, 20]) == 0
+    c.write([0, 1], 20)
+    c.lens[1] = length                                              # not a length that five pages of 16 rows can have
+    c.book.lens[1] = length
+    for call in (lambda: P.kv_pages_compact(*c.all, c.i32([0, 1]), c.i32([2, 3]), c.i32([[0, 19], [100, 19]])),
+                 lambda: P.kv_pages_compact(*c.all, c.i32([1]), c.i32([1]), c.i32([[max(length - 1, 0)]])),
+                 lambda: P.kv_pages_fork(*c.all[2:], c.i32([1]), c.i32([2]), page_rows=16),
+                 lambda: P.kv_pages_reserve(*c.all, c.i32([1]), c.i32([1]))):
+        assert call().item() == -1
+        assert P.spk_device_error(clear=True)[0] == P.binding.SPK_ERR_ARG
+        c.check()
