@@ -466,7 +466,9 @@ spk_status kv_pages_free(const spk_pages_shape* shape, int32_t* page_refs, int32
  *                   share.  It needs no clearing.
  * q, pages, tree and out are bf16 or fp16 (dtype).  Rows behind a sequence's
  * length or among the nodes that do not count are never read into a result,
- * whatever they hold.  An element whose sequence, length or node count is out
+ * whatever they hold.  What is not finite in the V of a node that a row sees
+ * adds to that row however small its weight (inf stays inf, inf - inf is NaN);
+ * in the V of a cached row it leaves the column inf, -inf or NaN.  An element whose sequence, length or node count is out
  * of range keeps its output rows and is recorded as SPK_ERR_ARG in the device
  * error word; a page number out of range is recorded and its rows are read as
  * zeros.  Weights enter the V product rounded to dtype (fp32 accumulation);

@@ -476,11 +476,13 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int c = run.from; c <= run.to; ++c) {
               const size_t at = tree_place(run, c);
               const float2 s = __ldcg(ml + at * C::kRows);
-              const float4 o = __ldcg(po + at * (D / 4) * C::kRows);
+              float4 o = __ldcg(po + at * (D / 4) * C::kRows);
               const float mx = fmaxf(M, s.x), ref = mx == -INFINITY ? 0.f : mx;
-              const float f0 = ex2_approx(M - ref), f = ex2_approx(s.x - ref);
+              float f0 = ex2_approx(M - ref), f = ex2_approx(s.x - ref);
               M = mx;
               L = fmaf(s.y, f, L * f0);
+              tree_weight(f0, acc);
+              tree_weight(f, o);
               acc = make_float4(fmaf(o.x, f, acc.x * f0), fmaf(o.y, f, acc.y * f0), fmaf(o.z, f, acc.z * f0),
                                 fmaf(o.w, f, acc.w * f0));
             }
@@ -563,8 +565,10 @@ __global__ void __launch_bounds__(kJoinRows *(MANY ? kJoinCols * kJoinGroups : D
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     auto add = [&](float2 ml, float4 o) {
       const float M = fmaxf(m, ml.x), ref = M == -INFINITY ? 0.f : M;
-      const float a = ex2_approx(m - ref), f = ex2_approx(ml.x - ref);
+      float a = ex2_approx(m - ref), f = ex2_approx(ml.x - ref);
       l = fmaf(l, a, ml.y * f);
+      tree_weight(a, acc);
+      tree_weight(f, o);
       acc.x = fmaf(acc.x, a, o.x * f);
       acc.y = fmaf(acc.y, a, o.y * f);
       acc.z = fmaf(acc.z, a, o.z * f);

@@ -327,8 +327,20 @@ __device__ __forceinline__ bool tree_wild(const TreeParams& p, int unit, int lo,
   return __any_sync(0xffffffffu, any);
 }
 
-// A row's output (or partial result) where a V row of nodes [lo, hi) that node i
-// sees is not finite: the sum of those values, whatever the finite ones give.
+// The nodes [lo, hi) that lie in key tiles [t0, t1) of an element.
+template <int KEYS>
+__device__ __forceinline__ void tree_nodes(const TreeParams& p, const TreeElement& e, int t0, int t1, int& lo, int& hi) {
+  lo = hi = 0;
+  if (!p.has_tree || t1 * KEYS <= e.len) return;
+  const int cached = (e.len + KEYS - 1) / KEYS;
+  const bool fused = tree_fused<KEYS>(p, e.len);               // all of them lie with the last rows
+  lo = fused ? 0 : max(0, t0 - cached) * KEYS;
+  hi = fused ? e.live : min(e.live, (t1 - cached) * KEYS);
+}
+
+// What is not finite among the V values of nodes [lo, hi) that node i sees, added
+// to the row's output (or partial result) of the others: an infinity stays one, a
+// NaN of the logits or of another row stays NaN.
 // Columns d0, d0 + step, .. below d1; column d lies at
 // out[(d / run) * stride + d % run].
 template <typename V, typename O>
@@ -343,8 +355,23 @@ __device__ __noinline__ void tree_patch(const TreeParams& p, int b, int unit, in
       const float v = static_cast<float>(static_cast<const V*>(p.v_tree)[(static_cast<size_t>(unit) * p.T + j) * D + d]);
       if (!isfinite(v)) sum += v;
     }
-    if (sum != 0.f) out[(d / run) * stride + d % run] = static_cast<O>(sum);   // (true for NaN too)
+    if (sum != 0.f) {                                          // (true for NaN too)
+      O& at = out[(d / run) * stride + d % run];
+      at = static_cast<O>(static_cast<float>(at) + sum);
+    }
   }
+}
+
+// Before partial results are multiplied by their share's weight: where that weight
+// underflowed to 0, what is finite counts for nothing and what is not stays as it
+// is (0 * inf would make NaN of it, in a row that one share holds whole it is inf).
+__device__ __forceinline__ void tree_weight(float& f, float4& o) {
+  if (f != 0.f) return;
+  f = 1.f;
+  o.x = isfinite(o.x) ? 0.f : o.x;
+  o.y = isfinite(o.y) ? 0.f : o.y;
+  o.z = isfinite(o.z) ? 0.f : o.z;
+  o.w = isfinite(o.w) ? 0.f : o.w;
 }
 
 // Where the partial results of share c of an item lie.

@@ -305,11 +305,8 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         go = walk.next(p, r);
         if (!go) r.t0 = -1;
         go = bar_wait(&sh.run_empty[s], ((k / kRunSlots) & 1) ^ 1, abort_v, umma_site(5, 1)) && go;
-        if (go && p.has_tree && r.t1 * kKeys > r.e.len) {      // (the nodes of these tiles, or all where they lie with rows)
-          const int cached = (r.e.len + kKeys - 1) / kKeys;
-          const bool fused = tree_fused<kKeys>(p, r.e.len);
-          lo = fused ? 0 : max(0, r.t0 - cached) * kKeys;
-          hi = fused ? r.e.live : min(r.e.live, (r.t1 - cached) * kKeys);
+        if (go) {
+          tree_nodes<kKeys>(p, r.e, r.t0, r.t1, lo, hi);
           unit = r.unit;
         }
         sh.run[s] = r;
@@ -807,11 +804,13 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       if (wild) {
         __syncwarp();                                          // (the row's outputs are other lanes' stores)
         const int d0 = alone ? x * (D / 2) : 0;
+        int lo, hi;
+        tree_nodes<kKeys>(p, run.e, run.t0, run.t1, lo, hi);
         if (live && whole)
-          tree_patch<T>(p, run.b, run.unit, node, 0, run.e.live, d0, c_end, 1, D,
+          tree_patch<T>(p, run.b, run.unit, node, lo, hi, d0, c_end, 1, D,
                         static_cast<T*>(p.out) + (static_cast<size_t>(run.unit) * p.rows + row) * D, D, size_t(0));
         else if (live)
-          tree_patch<T>(p, run.b, run.unit, node, 0, run.e.live, d0, c_end, 1, D,
+          tree_patch<T>(p, run.b, run.unit, node, lo, hi, d0, c_end, 1, D,
                         p.part_o + (place * (D / 4) * p.item_rows + part_row) * 4, 4, static_cast<size_t>(p.item_rows) * 4);
       }
       if (live && (!alone || x == 0)) {
@@ -861,8 +860,16 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
 #pragma unroll
                 for (int k = 0; k < 8; ++k) o[k] = __ldcg(src + k * p.item_rows);
               }
-              const float f = ex2_approx(s.x - ref);
+              float f = ex2_approx(s.x - ref);
               L = fmaf(s.y, f, L);
+              if (f == 0.f) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  float w = f;
+                  tree_weight(w, o[k]);
+                }
+                f = 1.f;
+              }
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
                 a[4 * k] = fmaf(o[k].x, f, a[4 * k]);

@@ -279,6 +279,63 @@ def test_nodes_that_a_row_does_not_see_may_hold_anything(P, T, hq, lens, dt):
     assert P.spk_device_error() == (0, 0)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("T,hq,lens", [(6, 4, [40]), (6, 4, [3000]), (40, 4, [40]), (40, 4, [3000]), (40, 16, [60]),
+                                       (40, 16, [3000, 50]), (150, 8, [2500])],
+                         ids=["narrow", "narrow-cut", "wide", "wide-cut", "pair", "pair-cut", "nodes-cut"])
+def test_what_is_not_finite_adds_up_whole_or_cut(P, T, hq, lens, dt):
+    # in one share or in many: NaN logits beside an infinite V, infinities of both signs,
+    # an infinite V whose weight is too small for 32 bits
+    import torch
+    dtype = torch.bfloat16 if dt == "bf16" else torch.float16
+    B = len(lens)
+    t, h = build_case(70 + T, dtype, B, 1, hq, 2, 64, T, 32, lens, mask="random")
+    t["q"] = t["q"].abs()
+    t["mask"][:, :, 0] &= ~4                                         # odd nodes see node 2, even ones do not
+    t["mask"][:, 1::2, 0] |= 4
+    seen = np.broadcast_to(np.arange(T) % 2 == 1, (B, T))
+    names = ("k_tree", "v_tree", "v_pages")
+
+    def call(**change):
+        a = dict(t, **change)
+        out, lse2 = torch.full_like(t["q"], 7.0), torch.full(t["q"].shape[:-1], 7.0, device="cuda")
+        P.tree_attention(**a, out=out, lse2=lse2)
+        torch.cuda.synchronize()
+        return out.float().cpu().numpy(), lse2.cpu().numpy()
+
+    ref, ref_lse = call()
+    clean = {x: t[x].clone() for x in names}
+
+    k, v = clean["k_tree"].clone(), clean["v_tree"].clone()          # a NaN logit: the row is NaN, infinite V or not
+    k[:, :, :, 2], v[:, :, :, 2, 0] = float("nan"), float("inf")
+    out, lse2 = call(k_tree=k, v_tree=v)
+    for b in range(B):
+        assert np.isnan(out[b][:, :, seen[b]]).all() and np.isnan(lse2[b][:, :, seen[b]]).all()
+        assert np.array_equal(out[b][:, :, ~seen[b]], ref[b][:, :, ~seen[b]])
+        assert np.array_equal(lse2[b][:, :, ~seen[b]], ref_lse[b][:, :, ~seen[b]])
+
+    v, pages = clean["v_tree"].clone(), clean["v_pages"].clone()     # -inf in the cache, +inf in the node: NaN for who sees both
+    v[:, :, :, 2, 1] = float("inf")
+    for b in range(B):
+        pages[:, h["table"][b][0], :, 3, 1] = float("-inf")
+    out, lse2 = call(v_tree=v, v_pages=pages)
+    assert np.array_equal(lse2, ref_lse)
+    for b in range(B):
+        assert np.isnan(out[b][:, :, seen[b], 1]).all()
+        assert np.isneginf(out[b][:, :, ~seen[b], 1]).all()
+        rest = [x for x in range(64) if x != 1]
+        assert np.array_equal(out[b][..., rest], ref[b][..., rest])
+
+    k, v = clean["k_tree"].clone(), clean["v_tree"].clone()          # a weight below 2^-1000: infinity all the same
+    k[:, :, :, 2], v[:, :, :, 2, 0] = -1000.0, float("inf")
+    out, lse2 = call(k_tree=k, v_tree=v)
+    for b in range(B):
+        assert np.isposinf(out[b][:, :, seen[b], 0]).all()
+        assert np.isfinite(out[b][:, :, seen[b], 1:]).all() and np.isfinite(lse2[b]).all()
+        assert np.array_equal(out[b][:, :, ~seen[b]], ref[b][:, :, ~seen[b]])
+    assert P.spk_device_error() == (0, 0)
+
+
 @pytest.mark.parametrize("case", [
     # seed, B, L, hq, hkv, d, T, page, lens: many units, ragged, so that shares cut them in two
     (40, 40, 2, 16, 8, 64, 1, 16, 300),          # 640 units of 2 rows
