@@ -468,11 +468,12 @@ spk_status kv_pages_free(const spk_pages_shape* shape, int32_t* page_refs, int32
  * length or among the nodes that do not count are never read into a result,
  * whatever they hold.  What is not finite in the V of a node that a row sees
  * adds to that row however small its weight (inf stays inf, inf - inf is NaN);
- * in the V of a cached row it leaves the column inf, -inf or NaN.  An element whose sequence, length or node count is out
- * of range keeps its output rows and is recorded as SPK_ERR_ARG in the device
- * error word; a page number out of range is recorded and its rows are read as
- * zeros.  Weights enter the V product rounded to dtype (fp32 accumulation);
- * the normaliser and lse2 are formed from the fp32 weights.
+ * in the V of a cached row it leaves the column inf, -inf or NaN.  An element
+ * whose sequence, length or node count is out of range keeps its output rows and
+ * is recorded as SPK_ERR_ARG in the device error word; a page number out of range
+ * is recorded and its rows are read as zeros.  Weights enter the V product
+ * rounded to dtype (fp32 accumulation); the normaliser and lse2 are formed from
+ * the fp32 weights.
  * Supported: head_dim in {64, 128}; hq % hkv == 0; T <= 1024; batch <= 1024;
  * page_rows a multiple of 8; layers * n_pages * hkv and the key tiles (of 64)
  * of all units < 2^31; scale > 0 and finite.

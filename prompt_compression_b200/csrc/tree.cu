@@ -476,16 +476,16 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int c = run.from; c <= run.to; ++c) {
               const size_t at = tree_place(run, c);
               const float2 s = __ldcg(ml + at * C::kRows);
-              float4 o = __ldcg(po + at * (D / 4) * C::kRows);
+              const float4 o = __ldcg(po + at * (D / 4) * C::kRows);
               const float mx = fmaxf(M, s.x), ref = mx == -INFINITY ? 0.f : mx;
-              float f0 = ex2_approx(M - ref), f = ex2_approx(s.x - ref);
+              const float f0 = ex2_approx(M - ref), f = ex2_approx(s.x - ref);
               M = mx;
               L = fmaf(s.y, f, L * f0);
-              tree_weight(f0, acc);
-              tree_weight(f, o);
               acc = make_float4(fmaf(o.x, f, acc.x * f0), fmaf(o.y, f, acc.y * f0), fmaf(o.z, f, acc.z * f0),
                                 fmaf(o.w, f, acc.w * f0));
             }
+            if (isnan(acc.x + acc.y + acc.z + acc.w))
+              acc = tree_join_again(p, run.from, run.to, run.c0, run.slot0, row, col4, D / 4, acc);
             const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
             const size_t at = static_cast<size_t>(run.unit) * p.rows + r;
             reinterpret_cast<uint2*>(p.out)[at * (D / 4) + col4] =
@@ -565,10 +565,8 @@ __global__ void __launch_bounds__(kJoinRows *(MANY ? kJoinCols * kJoinGroups : D
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     auto add = [&](float2 ml, float4 o) {
       const float M = fmaxf(m, ml.x), ref = M == -INFINITY ? 0.f : M;
-      float a = ex2_approx(m - ref), f = ex2_approx(ml.x - ref);
+      const float a = ex2_approx(m - ref), f = ex2_approx(ml.x - ref);
       l = fmaf(l, a, ml.y * f);
-      tree_weight(a, acc);
-      tree_weight(f, o);
       acc.x = fmaf(acc.x, a, o.x * f);
       acc.y = fmaf(acc.y, a, o.y * f);
       acc.z = fmaf(acc.z, a, o.z * f);
@@ -608,6 +606,10 @@ __global__ void __launch_bounds__(kJoinRows *(MANY ? kJoinCols * kJoinGroups : D
       __syncthreads();
     }
     if (!on || group > 0) continue;
+    if (isnan(acc.x + acc.y + acc.z + acc.w)) {
+      const int first = item.first / s.share;
+      acc = tree_join_again(p, c0, c1, first, item.first > first * s.share ? 1 : 0, row, col4, D / 4, acc);
+    }
     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
     const size_t at = static_cast<size_t>(item.unit) * p.rows + r;
     reinterpret_cast<uint2*>(p.out)[at * (D / 4) + col4] =

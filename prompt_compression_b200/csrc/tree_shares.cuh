@@ -362,21 +362,37 @@ __device__ __noinline__ void tree_patch(const TreeParams& p, int b, int unit, in
   }
 }
 
-// Before partial results are multiplied by their share's weight: where that weight
-// underflowed to 0, what is finite counts for nothing and what is not stays as it
-// is (0 * inf would make NaN of it, in a row that one share holds whole it is inf).
-__device__ __forceinline__ void tree_weight(float& f, float4& o) {
-  if (f != 0.f) return;
-  f = 1.f;
-  o.x = isfinite(o.x) ? 0.f : o.x;
-  o.y = isfinite(o.y) ? 0.f : o.y;
-  o.z = isfinite(o.z) ? 0.f : o.z;
-  o.w = isfinite(o.w) ? 0.f : o.w;
-}
-
 // Where the partial results of share c of an item lie.
 __device__ __forceinline__ size_t tree_place(const TreeRun& r, int c) {
   return static_cast<size_t>(c) * 2 + (c == r.c0 ? r.slot0 : 0);
+}
+
+// Four columns of a row of a cut item, `sum`, from its shares [from, to] again
+// where adding them gave NaN: where a share's weight underflows to 0, what is
+// finite counts for nothing and what is not stays as it is (0 * inf made NaN of
+// it; in an item that one share holds whole it is inf). c0, slot0: see TreeRun.
+static __device__ __noinline__ float4 tree_join_again(const TreeParams& p, int from, int to, int c0, int slot0, int row,
+                                                      int col4, int cols4, float4 sum) {
+  TreeRun r;
+  r.c0 = c0;
+  r.slot0 = slot0;
+  float m = -INFINITY;
+#pragma unroll 1
+  for (int c = from; c <= to; ++c) m = fmaxf(m, __ldcg(p.part_ml + (tree_place(r, c) * p.item_rows + row) * 2));
+  const float ref = m == -INFINITY ? 0.f : m;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int c = from; c <= to; ++c) {
+    const size_t at = tree_place(r, c);
+    const float f = ex2_approx(__ldcg(p.part_ml + (at * p.item_rows + row) * 2) - ref);
+    const float4 o = __ldcg(reinterpret_cast<const float4*>(p.part_o) + (at * cols4 + col4) * p.item_rows + row);
+    acc.x += f != 0.f ? o.x * f : isfinite(o.x) ? 0.f : o.x;
+    acc.y += f != 0.f ? o.y * f : isfinite(o.y) ? 0.f : o.y;
+    acc.z += f != 0.f ? o.z * f : isfinite(o.z) ? 0.f : o.z;
+    acc.w += f != 0.f ? o.w * f : isfinite(o.w) ? 0.f : o.w;
+  }
+  return make_float4(isnan(sum.x) ? acc.x : sum.x, isnan(sum.y) ? acc.y : sum.y, isnan(sum.z) ? acc.z : sum.z,
+                     isnan(sum.w) ? acc.w : sum.w);
 }
 
 // One more share of a cut item has left its results; true for the last one,

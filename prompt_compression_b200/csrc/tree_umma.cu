@@ -860,16 +860,8 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
 #pragma unroll
                 for (int k = 0; k < 8; ++k) o[k] = __ldcg(src + k * p.item_rows);
               }
-              float f = ex2_approx(s.x - ref);
+              const float f = ex2_approx(s.x - ref);
               L = fmaf(s.y, f, L);
-              if (f == 0.f) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  float w = f;
-                  tree_weight(w, o[k]);
-                }
-                f = 1.f;
-              }
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
                 a[4 * k] = fmaf(o[k].x, f, a[4 * k]);
@@ -879,6 +871,20 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
               }
             }
             const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+            bool again = false;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) again |= isnan(a[k]);
+            if (again && live) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float4 o = tree_join_again(p, run.from, run.to, run.c0, run.slot0, part_row, c / 4 + k, D / 4,
+                                                 make_float4(a[4 * k], a[4 * k + 1], a[4 * k + 2], a[4 * k + 3]));
+                a[4 * k] = o.x;
+                a[4 * k + 1] = o.y;
+                a[4 * k + 2] = o.z;
+                a[4 * k + 3] = o.w;
+              }
+            }
             uint32_t o[32];
 #pragma unroll
             for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(a[k] * inv);
