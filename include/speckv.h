@@ -447,7 +447,8 @@ spk_status kv_pages_free(const spk_pages_shape* shape, int32_t* page_refs, int32
  * with bit j % 32 of mask[b][i][j / 32] set:
  *   out[b][l][qh][i]  = softmax(scale * q . k) . v over those keys
  *   lse2[b][l][qh][i] = log2 sum 2^(scale * log2(e) * q . k)   (optional)
- * A node that sees no key gets out = 0 and lse2 = -inf.  Rows of nodes
+ * A node that sees no key, or whose logits are all -inf, gets out = 0 and
+ * lse2 = -inf.  Rows of nodes
  * i >= n_live[b] are left as they were.  T = 1 is single-token decoding.
  *
  *   q               [batch][layers][hq][T][head_dim]

@@ -669,7 +669,8 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
           const float mx = max32(b, max32(a, -INFINITY));
           tmem_ld_wait2(c, d);
           rescale(max32(d, max32(c, mx)) * p.c2);
-          const float2 nm = f2(-m, -m);
+          const float ref = m == -INFINITY ? 0.f : m;          // (every logit so far -inf: the weights are 2^-inf = 0)
+          const float2 nm = f2(-ref, -ref);
           tmem_ld32(mine + 32, b);
           exp32(d, nm, 3);
           exp32(c, nm, 2);

@@ -336,6 +336,25 @@ def test_what_is_not_finite_adds_up_whole_or_cut(P, T, hq, lens, dt):
     assert P.spk_device_error() == (0, 0)
 
 
+@pytest.mark.parametrize("T,hq", [(6, 4), (40, 4), (40, 16)], ids=["narrow", "wide", "pair"])
+@pytest.mark.parametrize("lens", [[500], [4000]], ids=["few-tiles", "cut"])
+def test_a_tile_of_keys_whose_logits_are_all_minus_infinity(P, T, hq, lens):
+    # the first 128 rows have infinite K against the queries' sign: their weights are 0, the others as without them
+    import torch
+    t, h = build_case(90 + T, torch.bfloat16, 1, 1, hq, 2, 64, T, 32, lens)
+    t["q"] = t["q"].abs() + 0.25
+    h["q"] = t["q"].double().cpu().numpy()
+    pages = h["table"][0][:4]
+    t["k_pages"][:, pages.tolist()] = float("-inf")
+    out, lse2 = torch.full_like(t["q"], 7.0), torch.full(t["q"].shape[:-1], 7.0, device="cuda")
+    P.tree_attention(**t, out=out, lse2=lse2)
+    torch.cuda.synchronize()
+    assert P.spk_device_error() == (0, 0)
+    h["table"] = h["table"][:, 4:]
+    h["lens"] = [lens[0] - 128]
+    compare(out, lse2, h, torch.bfloat16)
+
+
 @pytest.mark.parametrize("case", [
     # seed, B, L, hq, hkv, d, T, page, lens: many units, ragged, so that shares cut them in two
     (40, 40, 2, 16, 8, 64, 1, 16, 300),          # 640 units of 2 rows
