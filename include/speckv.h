@@ -550,6 +550,17 @@ spk_status spk_exp2_fma(const float* t, float* y, int n, void* stream);
  * returns; read it with spk_device_error().  No GPU state is left behind. */
 spk_status spk_selftest_wait_timeout(long long limit_ns, void* stream);
 
+/* Self-test of the waits of tree_attention: the call, and in front of it one
+ * more run of its main kernel in which two CTAs lose part of their work, as a
+ * copy or a warp that never arrives would.  Their waits run out (2 s), record
+ * SPK_ERR_TIMEOUT at a site of 600 and more, and the CTAs end; the call behind
+ * it, on the same workspace, gives its results.  bf16, head_dim 64, hq / hkv *
+ * n_nodes up to 8 or 33 to 128. */
+spk_status spk_selftest_tree_give_up(const spk_tree_shape* shape, const void* q, const void* k_pages, const void* v_pages,
+                                     const int32_t* page_table, const int32_t* seq_lens, const int32_t* seqs,
+                                     const void* k_tree, const void* v_tree, const uint32_t* mask, const int32_t* n_live,
+                                     void* out, float* lse2, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -20,7 +20,7 @@ from .binding import (  # noqa: F401
     speckv_workspace_size, speckv_score, speckv_row_lse, speckv_row_offsets, speckv_colsum,
     speckv_prefill_attention, specpc_workspace_size, specpc_score, specpc_row_offsets, specpc_colsum,
     topk_workspace_size, topk_select, kv_compact, decode_attention,
-    spk_device_error, spk_selftest_wait_timeout, spk_exp2_fma, mapped_host_pointer,
+    spk_device_error, spk_selftest_wait_timeout, spk_selftest_tree_give_up, spk_exp2_fma, mapped_host_pointer,
     SPK_POOL_MAX, SPK_POOL_AVG, vs_workspace_size, vs_sparse_attention,
     pages_shape, kv_pages_workspace_size, kv_pages_reserve, kv_pages_write, kv_pages_compact, kv_pages_fork,
     kv_pages_free, tree_shape, tree_attention_workspace_size, tree_attention, tree_mask,
@@ -34,7 +34,7 @@ __all__ = [
     "speckv_workspace_size", "speckv_score", "speckv_row_lse", "speckv_row_offsets", "speckv_colsum",
     "speckv_prefill_attention", "specpc_workspace_size", "specpc_score", "specpc_row_offsets", "specpc_colsum",
     "topk_workspace_size", "topk_select", "kv_compact", "decode_attention",
-    "spk_device_error", "spk_selftest_wait_timeout", "spk_exp2_fma", "mapped_host_pointer",
+    "spk_device_error", "spk_selftest_wait_timeout", "spk_selftest_tree_give_up", "spk_exp2_fma", "mapped_host_pointer",
     "SPK_POOL_MAX", "SPK_POOL_AVG", "vs_workspace_size", "vs_sparse_attention",
     "pages_shape", "kv_pages_workspace_size", "kv_pages_reserve", "kv_pages_write", "kv_pages_compact",
     "kv_pages_fork", "kv_pages_free", "tree_shape", "tree_attention_workspace_size", "tree_attention", "tree_mask",

@@ -114,6 +114,7 @@ def load_library():
         "tree_attention_workspace_size": (sz, [tr]),
         "tree_attention": (I, [tr, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
         "tree_mask": (I, [I, I, vp, vp, vp, vp, vp]),
+        "spk_selftest_tree_give_up": (I, [tr, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -673,6 +674,20 @@ def spk_device_error(clear: bool = True):
 
 def spk_selftest_wait_timeout(limit_ns: int, stream=None):
     _check(load_library().spk_selftest_wait_timeout(int(limit_ns), _stream(stream)))
+
+
+def spk_selftest_tree_give_up(q, k_pages, v_pages, page_table, seq_lens, k_tree, v_tree, mask, n_live, seqs, out, lse2,
+                              workspace, scale: float, stream=None):
+    """tree_attention behind a run of its kernel whose waits give up (see the header)."""
+    shape = tree_shape(q, k_pages, page_table, scale)
+    half, i32 = torch.bfloat16, torch.int32
+    _check(load_library().spk_selftest_tree_give_up(
+        ctypes.byref(shape), _dev(q, "q", half), _dev(k_pages, "k_pages", half), _dev(v_pages, "v_pages", half),
+        _dev(page_table, "page_table", i32), _dev(seq_lens, "seq_lens", i32), _dev(seqs, "seqs", i32),
+        _dev(k_tree, "k_tree", half), _dev(v_tree, "v_tree", half), _dev(mask, "mask", i32), _dev(n_live, "n_live", i32),
+        _dev(out, "out", half), _dev(lse2, "lse2", torch.float32), _dev(workspace, "workspace"),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
+    return out
 
 
 def spk_exp2_fma(t, y, stream=None):

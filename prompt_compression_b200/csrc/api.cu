@@ -850,10 +850,11 @@ size_t tree_attention_workspace_size(const spk_tree_shape* s) {
   return round_up(tree_ws_bytes(tree_plan(s->hq / s->hkv * s->n_nodes, s->head_dim, num_sms()), s->head_dim), 256);
 }
 
-spk_status tree_attention(const spk_tree_shape* s, const void* q, const void* k_pages, const void* v_pages,
-                          const int32_t* table, const int32_t* lens, const int32_t* seqs, const void* k_tree,
-                          const void* v_tree, const uint32_t* mask, const int32_t* n_live, void* out, float* lse2,
-                          void* ws, size_t ws_bytes, void* stream) {
+// loses: the main kernel with CTAs that lose work is enqueued in front of the call.
+static spk_status tree_call(const spk_tree_shape* s, const void* q, const void* k_pages, const void* v_pages,
+                            const int32_t* table, const int32_t* lens, const int32_t* seqs, const void* k_tree,
+                            const void* v_tree, const uint32_t* mask, const int32_t* n_live, void* out, float* lse2,
+                            void* ws, size_t ws_bytes, void* stream, bool loses) {
   spk_status st = check_tree(s);
   if (st != SPK_OK) return st;
   if (q == nullptr || k_pages == nullptr || v_pages == nullptr || out == nullptr || table == nullptr || lens == nullptr)
@@ -909,8 +910,30 @@ spk_status tree_attention(const spk_tree_shape* s, const void* q, const void* k_
   if (st == SPK_OK) st = make_map16(&maps[6], fp16, v_pages, s->head_dim, s->page_rows, pool, 8);
   if (st == SPK_OK && plan.wide) st = make_map16(&maps[4], fp16, q, s->head_dim, p.rows, units, 128);
   if (st != SPK_OK) return st;
-  cudaError_t e = launch_tree_attention(fp16, s->head_dim, maps, p, plan, static_cast<cudaStream_t>(stream));
+  cudaError_t e = loses ? launch_tree_loses(maps, p, plan, static_cast<cudaStream_t>(stream)) : cudaSuccess;
+  if (e == cudaSuccess) e = launch_tree_attention(fp16, s->head_dim, maps, p, plan, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ok() : cuda_fail(e, "tree attention launch");
+}
+
+spk_status tree_attention(const spk_tree_shape* s, const void* q, const void* k_pages, const void* v_pages,
+                          const int32_t* table, const int32_t* lens, const int32_t* seqs, const void* k_tree,
+                          const void* v_tree, const uint32_t* mask, const int32_t* n_live, void* out, float* lse2,
+                          void* ws, size_t ws_bytes, void* stream) {
+  return tree_call(s, q, k_pages, v_pages, table, lens, seqs, k_tree, v_tree, mask, n_live, out, lse2, ws, ws_bytes, stream,
+                   false);
+}
+
+spk_status spk_selftest_tree_give_up(const spk_tree_shape* s, const void* q, const void* k_pages, const void* v_pages,
+                                     const int32_t* table, const int32_t* lens, const int32_t* seqs, const void* k_tree,
+                                     const void* v_tree, const uint32_t* mask, const int32_t* n_live, void* out,
+                                     float* lse2, void* ws, size_t ws_bytes, void* stream) {
+  spk_status st = check_tree(s);
+  if (st != SPK_OK) return st;
+  const int rows = s->hq / s->hkv * s->n_nodes;
+  if (s->dtype != SPK_BF16 || s->head_dim != 64 || (rows > 8 && rows <= 32) || rows > 128)
+    return fail(SPK_ERR_UNSUPPORTED, "the self-test is for bf16, head_dim 64 and up to 8 or 33 to 128 query rows a unit");
+  return tree_call(s, q, k_pages, v_pages, table, lens, seqs, k_tree, v_tree, mask, n_live, out, lse2, ws, ws_bytes, stream,
+                   true);
 }
 
 spk_status tree_mask(int batch, int n_nodes, const int32_t* parents, const int32_t* n_live, uint32_t* mask,

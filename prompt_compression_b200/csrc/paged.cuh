@@ -100,6 +100,10 @@ cudaError_t launch_tree_attention(bool fp16, int head_dim, const CUtensorMap (&m
                                   const TreePlan& plan, cudaStream_t stream);
 cudaError_t launch_tree_umma(bool fp16, int head_dim, const CUtensorMap (&maps)[7], const TreeParams& p,
                              cudaStream_t stream);
+// The main kernel alone, for bf16, head_dim 64 and units of up to 8 or 33 .. 128
+// rows, with CTAs that lose work (spk_selftest_tree_give_up).
+cudaError_t launch_tree_loses(const CUtensorMap (&maps)[7], const TreeParams& p, const TreePlan& plan, cudaStream_t stream);
+cudaError_t launch_tree_umma_loses(const CUtensorMap (&maps)[7], const TreeParams& p, cudaStream_t stream);
 cudaError_t launch_tree_mask(const int* parents, const int* n_live, int batch, int T, uint32_t* mask, int* depth,
                              cudaStream_t stream);
 cudaError_t device_errors_tree(int* code, int* site, bool clear);

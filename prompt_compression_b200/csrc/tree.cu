@@ -64,7 +64,8 @@ __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, 128
 // type for the product (the largest weight is 1 exactly, the others are off by
 // half a step at most, and the errors average over the keys); the sum is
 // formed from the fp32 values, so lse2 keeps 32 bits.
-template <typename T, int D, int NT>
+// LOSES: a self-test of the waits. The second tile of CTA 0 never comes.
+template <typename T, int D, int NT, bool LOSES>
 __global__ void __launch_bounds__(kThreads, 2)
     tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                 const __grid_constant__ CUtensorMap ktmap, const __grid_constant__ CUtensorMap vtmap,
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             unit = run.pool + page * p.hkv;
           }
         }
-        ok = mbar_wait(&empty[st], ph ^ 1, abort_v, site(0));
+        ok = !(LOSES && blockIdx.x == 0 && count == 1) && mbar_wait(&empty[st], ph ^ 1, abort_v, site(0));
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const int bytes = (boxes * part_rows + (tile.nodes > 0 ? p.node_rows : 0)) * 128 * 2 * C::kAtoms;
@@ -642,7 +643,7 @@ cudaError_t launch_join(const TreeParams& p, const TreePlan& plan, cudaStream_t 
               : cudaLaunchKernelEx(&cfg, tree_join_kernel<T, D, KEYS, PAIRS, false>, p, plan.item_rows, by_border);
 }
 
-template <typename T, int D, int NT>
+template <typename T, int D, int NT, bool LOSES = false>
 cudaError_t launch_nt(const CUtensorMap (&maps)[7], const TreeParams& p, const TreePlan& plan, cudaStream_t stream) {
   using C = TreeCfg<D, NT>;
   static thread_local int configured_device = -1;
@@ -650,11 +651,12 @@ cudaError_t launch_nt(const CUtensorMap (&maps)[7], const TreeParams& p, const T
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (configured_device != dev) {
-    e = cudaFuncSetAttribute(tree_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    e = cudaFuncSetAttribute(tree_kernel<T, D, NT, LOSES>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
-  tree_kernel<T, D, NT><<<plan.ctas, kThreads, C::kSmemBytes, stream>>>(maps[0], maps[1], maps[2], maps[3], maps[5], maps[6], p);
+  tree_kernel<T, D, NT, LOSES><<<plan.ctas, kThreads, C::kSmemBytes, stream>>>(maps[0], maps[1], maps[2], maps[3], maps[5],
+                                                                              maps[6], p);
   return cudaGetLastError();
 }
 
@@ -750,6 +752,10 @@ cudaError_t launch_tree_attention(bool fp16, int head_dim, const CUtensorMap (&m
   if (head_dim == 64)
     return fp16 ? launch_d<__half, 64>(maps, p, plan, stream) : launch_d<__nv_bfloat16, 64>(maps, p, plan, stream);
   return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_tree_loses(const CUtensorMap (&maps)[7], const TreeParams& p, const TreePlan& plan, cudaStream_t stream) {
+  return plan.wide ? launch_tree_umma_loses(maps, p, stream) : launch_nt<__nv_bfloat16, 64, 1, true>(maps, p, plan, stream);
 }
 
 cudaError_t launch_tree_mask(const int* parents, const int* n_live, int batch, int T, uint32_t* mask, int* depth,

@@ -51,10 +51,20 @@ constexpr float kRescaleLog2 = 8.f;      // O and the sum are rescaled when the 
 
 __device__ __forceinline__ int umma_site(int role, int which) { return 620 + role * 10 + which; }
 
-// Bounded wait with little code: the hardware suspends the thread for a while
-// at each try.  (Items are short, so this kernel's speed hangs on how
+// Bounded wait with little code: the hardware suspends the thread for a while at
+// each try; from the 4097th on each is followed by a millisecond by the timer, up
+// to the library's limit.  (Items are short, so this kernel's speed hangs on how
 // much of its code stays in the instruction cache; mbar_wait, inlined at every
-// wait, is several times as long.)
+// wait, is several times as long.  16 nodes over 320 rows, 512 KV heads; 24 nodes,
+// 16 ragged sequences; 64 nodes over 64K rows: 39.3, 59.4 and 216 us; with the
+// timer read in the loop 39.4, 59.7 and 216; with a function that takes the wait
+// over 39.4, 60.2 and 222; without a limit in time 38.8, 59.1 and 219.)
+constexpr int kShortTries = 4096;
+constexpr uint32_t kPauseNs = 1000000;
+__device__ __noinline__ void pause() {
+  const uint64_t t0 = global_timer_ns();
+  while (global_timer_ns() - t0 < kPauseNs) __nanosleep(1000);
+}
 __device__ __noinline__ bool give_up(volatile int* abort_flag, int site) {
   if (*abort_flag == 0) {
     record_error(SPK_DEVERR_TIMEOUT, site);
@@ -63,18 +73,11 @@ __device__ __noinline__ bool give_up(volatile int* abort_flag, int site) {
   return false;
 }
 __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int site) {
-  uint32_t ok = 0;
 #pragma unroll 1
-  for (int tries = 0; tries < 20000000; ++tries) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    if (ok) return true;
+  for (int tries = 0; tries < kShortTries + static_cast<int>(SPK_WAIT_LIMIT_NS / kPauseNs); ++tries) {
+    if (mbar_try_wait(bar, parity)) return true;
     if (*abort_flag) return false;
+    if (tries >= kShortTries) pause();
   }
   return give_up(abort_flag, site);
 }
@@ -219,7 +222,9 @@ __device__ __forceinline__ void transpose4(uint4 (&v)[4], int lane) {
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // --------------------------------------------------------------------------
-template <typename T, int D, int QT>
+// LOSES: a self-test of the waits. CTA c (0 or 1) publishes only its first c runs;
+// what the others wait for never comes.
+template <typename T, int D, int QT, bool LOSES>
 __global__ void __launch_bounds__(kUmmaThreads, 1)
     tree_umma_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap ktmap,
@@ -297,6 +302,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     int lo = 0, hi = 0, unit = 0;
     bool go = true;
     for (uint32_t k = 0; go; ++k) {
+      if (LOSES && blockIdx.x < 2 && k == blockIdx.x) break;
       const uint32_t s = k % kRunSlots;
       const int old_lo = lo, old_hi = hi, old_unit = unit;
       lo = hi = unit = 0;
@@ -911,7 +917,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
   }
 }
 
-template <typename T, int D, int QT>
+template <typename T, int D, int QT, bool LOSES>
 cudaError_t launch_qt(const CUtensorMap (&maps)[7], const TreeParams& p, cudaStream_t stream) {
   using C = UmmaCfg<D, QT>;
   static thread_local int configured_device = -1;
@@ -919,18 +925,18 @@ cudaError_t launch_qt(const CUtensorMap (&maps)[7], const TreeParams& p, cudaStr
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (configured_device != dev) {
-    e = cudaFuncSetAttribute(tree_umma_kernel<T, D, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    e = cudaFuncSetAttribute(tree_umma_kernel<T, D, QT, LOSES>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
-  tree_umma_kernel<T, D, QT><<<p.ctas, kUmmaThreads, C::kSmemBytes, stream>>>(maps[4], maps[0], maps[1], maps[2], maps[3],
-                                                                             maps[5], maps[6], p);
+  tree_umma_kernel<T, D, QT, LOSES><<<p.ctas, kUmmaThreads, C::kSmemBytes, stream>>>(maps[4], maps[0], maps[1], maps[2],
+                                                                                    maps[3], maps[5], maps[6], p);
   return cudaGetLastError();
 }
 
 template <typename T, int D>
 cudaError_t launch_d(const CUtensorMap (&maps)[7], const TreeParams& p, cudaStream_t stream) {
-  return p.rows > 128 ? launch_qt<T, D, 2>(maps, p, stream) : launch_qt<T, D, 1>(maps, p, stream);
+  return p.rows > 128 ? launch_qt<T, D, 2, false>(maps, p, stream) : launch_qt<T, D, 1, false>(maps, p, stream);
 }
 
 }  // namespace
@@ -940,6 +946,10 @@ cudaError_t launch_tree_umma(bool fp16, int head_dim, const CUtensorMap (&maps)[
   if (head_dim == 128) return fp16 ? launch_d<__half, 128>(maps, p, stream) : launch_d<__nv_bfloat16, 128>(maps, p, stream);
   if (head_dim == 64) return fp16 ? launch_d<__half, 64>(maps, p, stream) : launch_d<__nv_bfloat16, 64>(maps, p, stream);
   return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_tree_umma_loses(const CUtensorMap (&maps)[7], const TreeParams& p, cudaStream_t stream) {
+  return launch_qt<__nv_bfloat16, 64, 1, true>(maps, p, stream);
 }
 
 }  // namespace spk

@@ -267,3 +267,14 @@ def test_tree_pointer_and_workspace_errors(lib):
     assert lib.tree_mask(65536, 4, 16, None, 16, None, None) == B.SPK_ERR_UNSUPPORTED
     assert lib.tree_mask(1, 4, None, None, 16, None, None) == B.SPK_ERR_ARG
     assert lib.tree_mask(1, 4, 16, None, 18, None, None) == B.SPK_ERR_ARG
+
+
+def test_the_tree_self_test_refuses_what_it_has_no_kernel_for(lib):
+    from prompt_compression_b200 import binding as B
+    for change in (dict(), dict(head_dim=64, dtype=1), dict(head_dim=64, n_nodes=5), dict(head_dim=64, n_nodes=33)):
+        s = _tree(**change)
+        assert lib.spk_selftest_tree_give_up(ctypes.byref(s), 16, 16, 16, 16, 16, None, 16, 16, None, None, 16, None, 16,
+                                             1 << 40, None) == B.SPK_ERR_UNSUPPORTED
+    s = _tree(head_dim=64, n_nodes=2)
+    assert lib.spk_selftest_tree_give_up(ctypes.byref(s), None, 16, 16, 16, 16, None, 16, 16, None, None, 16, None, 16,
+                                         1 << 40, None) == B.SPK_ERR_ARG

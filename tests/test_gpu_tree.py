@@ -487,3 +487,35 @@ def test_tree_mask_of_wrong_parents(P):
     st, _ = P.spk_device_error(clear=True)
     assert st == P.binding.SPK_ERR_ARG
     assert mask[0, :, 0].tolist() == [1, 2, 5, 8, 16] and depth[0].tolist() == [0, 0, 1, 0, 0]
+
+
+GIVE_UP = [
+    # seed, B, L, hq, hkv, T, page, most, sites: shares that cut items; both ways of joining them
+    (80, 20, 2, 32, 8, 10, 16, 700, range(620, 690)),     # tcgen05, 320 items, joined inside
+    (81, 2, 1, 32, 8, 10, 16, 6000, range(620, 690)),     # tcgen05, 16 items
+    (82, 40, 2, 16, 8, 3, 16, 700, range(600, 620)),      # mma.sync, 640 items, joined inside
+    (83, 1, 1, 16, 8, 3, 16, 6000, range(600, 620)),      # mma.sync, 8 items
+]
+
+
+@pytest.mark.parametrize("case", GIVE_UP, ids=["wide-inside", "wide", "narrow-inside", "narrow"])
+def test_waits_that_run_out_end_the_kernel(P, case):
+    # two CTAs lose work: their waits give up after 2 s and say so
+    import time
+
+    import torch
+    seed, B, L, hq, hkv, T, page, most, sites = case
+    rng = np.random.default_rng(seed)
+    lens = [int(x) for x in rng.integers(most // 2, most, B)]
+    t, h = build_case(seed, torch.bfloat16, B, L, hq, hkv, 64, T, page, lens)
+    shape = P.tree_shape(t["q"], t["k_pages"], t["page_table"], t["scale"])
+    ws = torch.full((P.tree_attention_workspace_size(shape),), 255, dtype=torch.uint8, device="cuda")
+    out, lse2 = torch.full_like(t["q"], 7.0), torch.full(t["q"].shape[:-1], 7.0, device="cuda")
+    torch.cuda.synchronize()
+    t0 = time.monotonic()
+    P.spk_selftest_tree_give_up(**t, out=out, lse2=lse2, workspace=ws)
+    torch.cuda.synchronize()
+    assert 1.5 < time.monotonic() - t0 < 10.0
+    status, where = P.spk_device_error(clear=True)
+    assert status == P.binding.SPK_ERR_TIMEOUT and where in sites
+    assert P.spk_device_error() == (0, 0)
