@@ -92,6 +92,7 @@ struct UmmaShared {
   float2 ml[2][128];          // both groups' row states, for the other
   uint32_t tmem_holder;
   int abort_flag, last;
+  int arrived;                // cut items of which this CTA's share has been counted (tree_arrive)
   int wild[kRunSlots];        // of each run: whether V of its nodes holds something that is not finite
 };
 
@@ -221,6 +222,18 @@ __device__ __forceinline__ void transpose4(uint4 (&v)[4], int lane) {
 
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// A CTA that gave up counts its shares of the cut items that it did not come to,
+// so that the counts end at 0: a replay of the call has its number, and would
+// take what is left in the workspace for shares of its own.  (By a warp.)
+__device__ __noinline__ void count_the_rest(const TreeParams& p, int arrived) {
+  const TreeStart start = tree_start<kKeys>(p, blockIdx.x, false);
+  if ((threadIdx.x & 31) != 0) return;
+  TreeWalker<kKeys, true> walk(start);
+  TreeRun r;
+  while (walk.next(p, r))
+    if (r.from != r.to && --arrived < 0) tree_arrive(p, r);
+}
+
 // --------------------------------------------------------------------------
 // LOSES: a self-test of the waits. CTA c (0 or 1) publishes only its first c runs;
 // what the others wait for never comes.
@@ -260,6 +273,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
       mbar_init(&sh.wild_full[s], 1);
     }
     sh.abort_flag = 0;
+    sh.arrived = 0;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -838,6 +852,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
         if (threadIdx.x == 0) {
           ok = bar_wait(&sh.parts_in, cut_runs & 1, abort_v, umma_site(2, 4));
           sh.last = ok && tree_arrive(p, run);
+          sh.arrived += ok;
           mbar_arrive(&sh.joined);
         }
         __syncwarp();
@@ -915,6 +930,7 @@ __global__ void __launch_bounds__(kUmmaThreads, 1)
     tc_fence_after();
     tmem_dealloc(sh.tmem_holder, 512);
   }
+  if (warp == kRunWarp && p.join_inside && sh.abort_flag != 0) count_the_rest(p, sh.arrived);
 }
 
 template <typename T, int D, int QT, bool LOSES>

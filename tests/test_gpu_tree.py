@@ -500,7 +500,7 @@ GIVE_UP = [
 
 @pytest.mark.parametrize("case", GIVE_UP, ids=["wide-inside", "wide", "narrow-inside", "narrow"])
 def test_waits_that_run_out_end_the_kernel(P, case):
-    # two CTAs lose work: their waits give up after 2 s and say so
+    # two CTAs lose work: their waits give up after 2 s and say so, and the same call behind it is right
     import time
 
     import torch
@@ -518,4 +518,11 @@ def test_waits_that_run_out_end_the_kernel(P, case):
     assert 1.5 < time.monotonic() - t0 < 10.0
     status, where = P.spk_device_error(clear=True)
     assert status == P.binding.SPK_ERR_TIMEOUT and where in sites
+    compare(out, lse2, h, torch.bfloat16)
+    # the words that count a cut item's shares lie behind the partial results: none is left in between
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    ctas, item_rows = (sms, 128) if hq // hkv * T > 32 else (2 * sms, 8)
+    counts = ws[ctas * 2 * item_rows * (64 + 2) * 4:][:ctas * 8].view(torch.int64)
+    used = counts != -1
+    assert bool(used.any()) == (B * L * hkv >= 2 * ctas) and not (counts[used] & 0xffff).any()
     assert P.spk_device_error() == (0, 0)
