@@ -1,5 +1,5 @@
 // mma.cuh -- warp-level matrix fragments (mma.sync m16n8k16, ldmatrix,
-// stmatrix) for the kernels whose query side is narrow: 8 to 64 rows.
+// stmatrix) for the kernels whose query side is narrow: 8 to 32 rows.
 //
 // Fragment layout of one warp (lane = 4 gr + gc): the 16 x 8 accumulator holds
 // rows gr (c0, c1) and gr + 8 (c2, c3) at columns 2 gc, 2 gc + 1; the B operand

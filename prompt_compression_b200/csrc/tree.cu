@@ -6,16 +6,21 @@
 //   out  = sum_j 2^(c2 s_j - m) v_j / sum_j 2^(c2 s_j - m),  lse2 = m + log2 sum,
 // in one pass with the running maximum m and sum (log2 domain, fp32).
 //
-// This kernel has the units of few query rows (row tiles of 8 to 64, on
+// This kernel has the units of few query rows (row tiles of 8, 16 or 32, on
 // mma.sync); tree_umma.cu has the others.  How the work is shared out:
 // tree_shares.cuh.  An item inside one share is finished there; the others
 // leave (m, sum, unnormalised output) of each share in the workspace, to be
 // added in the order of the shares, so that the results do not depend on
-// timing.  Where there are at least twice as many items as CTAs (an item is
-// then in two shares at most) the share that arrives last does it; otherwise
-// tree_join_kernel, which spreads the many shares of an item over the GPU.
+// timing.  Where there are at least twice as many items as CTAs the share that
+// arrives last does it, one share after the other: with items of like lengths
+// an item is then in two shares at most; one long sequence among short ones is
+// in many, which costs time but is right.  Otherwise tree_join_kernel does it,
+// which spreads the many shares of an item over the GPU.
 // (16 nodes over 320 rows, 512 KV heads: 38 us the one way, 43 the other; one
-// node over 16K rows, 8 KV heads in 37 shares each: 37 and 20 us.)
+// node over 16K rows, 8 KV heads in 37 shares each: 37 and 20 us.  One sequence
+// of 65,536 rows among 79 of 300, 8 KV heads, one node, 22 shares a long item,
+// joined inside: 76 us; the long one by itself 49, the others 30.  One of 16K
+// rows beside 73 elements without a live node, 32 shares: 37 us, by itself 20.)
 #include <type_traits>
 
 #include "common.cuh"

@@ -22,7 +22,8 @@
 //   warp 11         the runs (tree_shares.cuh), ahead of the others, which read
 //                   them from shared memory
 // TMEM (512 columns): group x's S at 256 x, its O at 256 x + 128.
-// No atomics: the result is deterministic.
+// The one atomic counts a cut item's shares (tree_arrive); which of them is the
+// last does not change a result.
 #include <cuda_bf16.h>
 
 #include <type_traits>

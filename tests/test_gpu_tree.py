@@ -526,3 +526,26 @@ def test_waits_that_run_out_end_the_kernel(P, case):
     used = counts != -1
     assert bool(used.any()) == (B * L * hkv >= 2 * ctas) and not (counts[used] & 0xffff).any()
     assert P.spk_device_error() == (0, 0)
+
+
+@pytest.mark.parametrize("case", [
+    # seed, B, hq, T, long, short, dead: twice as many items as CTAs, and one sequence whose items lie in tens of shares
+    (100, 74, 16, 1, 16384, 40, True),           # mma.sync, one element with a live node
+    (101, 80, 16, 3, 9000, 200, False),
+    (102, 37, 32, 10, 16384, 40, True),          # tcgen05
+    (103, 40, 32, 10, 12000, 200, False),
+    (104, 40, 64, 20, 8000, 100, False),         # pairs of query tiles: 160 rows
+], ids=["narrow-dead", "narrow", "wide-dead", "wide", "pair"])
+def test_one_long_sequence_among_many_short_ones(P, case):
+    import torch
+    seed, B, hq, T, most, short, dead = case
+    rng = np.random.default_rng(seed)
+    lens = [int(x) for x in rng.integers(1, short, B)]
+    live = [0 if dead else int(x) for x in rng.integers(0, T + 1, B)]
+    lens[B // 3], live[B // 3] = most, T
+    t, h = build_case(seed, torch.bfloat16, B, 1, hq, 8, 64, T, 64, lens, live)
+    out, lse2 = check(P, t, h, torch.bfloat16)
+    for _ in range(5):
+        o, l = torch.full_like(out, 7.0), torch.full_like(lse2, 7.0)
+        P.tree_attention(**t, out=o, lse2=l)
+        assert torch.equal(o, out) and torch.equal(l, lse2)
