@@ -424,3 +424,65 @@ def test_a_length_beyond_the_table_is_refused(P, length):
         assert call().item() == -1
         assert P.spk_device_error(clear=True)[0] == P.binding.SPK_ERR_ARG
         c.check()
+
+
+def _sorted_rows(rng, n, keep, lists):
+    return [sorted(rng.choice(n, keep, replace=False).tolist()) for _ in range(lists)]
+
+
+def test_compaction_of_hundreds_of_sequences(P):
+    # tables large enough for the bookkeeping in a cluster of CTAs: into others, in place,
+    # a source twice, too few free pages, refused lists
+    c = Cache(P, 1, 2000, 1, 2, 16, 700, 12, seed=15)
+    rng = np.random.default_rng(15)
+    seqs = rng.permutation(700).tolist()
+    a, b = seqs[:300], seqs[300:600]
+    assert c.reserve(a, [int(x) for x in rng.integers(5, 9, 300)]) == 0
+    c.check()
+    assert c.compact(a, b, _sorted_rows(rng, 5, 3, 300), 1) == 0
+    c.check()
+    assert c.compact(a[:200], a[:200], _sorted_rows(rng, 5, 4, 200), 1) == 38    # in place: the new pages come first
+    c.check()
+    # a source a hundred times
+    assert c.compact([a[0]] * 100 + a[100:200], b[200:300] + b[:100], _sorted_rows(rng, 4, 2, 200), 1) == 0
+    c.check()
+    assert c.compact(b[100:300], a[100:300], _sorted_rows(rng, 2, 1, 200), 1) == 0
+    c.check()
+    c.fork(a[:250], seqs[440:690])                                               # shared pages
+    c.check()
+    assert c.compact(a[:250], a[:250], _sorted_rows(rng, 1, 1, 250), 1) == 0     # in place, the others keep the pages
+    c.check()
+    c.no_error()
+    E = P.binding.SPK_ERR_ARG
+    i32, rows = c.i32, c.i32([[0]] * 250)
+    dup = a[1:250] + [a[1]]
+    for call in (lambda: P.kv_pages_compact(*c.all, i32(a[:250]), i32(dup), rows),
+                 lambda: P.kv_pages_compact(*c.all, i32(a[:249] + [700]), i32(b[:250]), rows),
+                 lambda: P.kv_pages_fork(*c.all[2:], i32(a[:250]), i32(dup), page_rows=2),
+                 lambda: P.kv_pages_fork(*c.all[2:], i32(a[:249] + [-1]), i32(b[:250]), page_rows=2)):
+        assert call().item() == -1
+        assert P.spk_device_error(clear=True)[0] == E
+        c.check()
+
+
+def test_refusals_with_a_pool_of_many_pages(P):
+    c = Cache(P, 1, 9001, 1, 1, 16, 64, 300, seed=16)
+    assert c.reserve(list(range(30)), [300] * 30) == 0                           # 9000 of 9001 pages
+    c.check()
+    assert c.reserve([30, 31], [1, 1]) == 1
+    c.check()
+    assert c.compact([0, 1], [32, 33], [[0, 5, 7]] * 2, 1) == 5
+    c.check()
+    assert c.compact([0, 1], [0, 1], [[0, 5, 7]] * 2, 1) == 5                    # in place: the new pages come first
+    c.check()
+    assert c.compact([0, 1], [2, 3], [[0, 5, 299]] * 2, 1) == 0                  # what 2 and 3 held is enough
+    c.check()
+    c.no_error()
+    E = P.binding.SPK_ERR_ARG
+    for call in (lambda: P.kv_pages_reserve(*c.all, c.i32([5, 5]), c.i32([0, 0])),
+                 lambda: P.kv_pages_reserve(*c.all, c.i32([64]), c.i32([1])),
+                 lambda: P.kv_pages_compact(*c.all, c.i32([0, 1]), c.i32([4, 4]), c.i32([[0], [0]])),
+                 lambda: P.kv_pages_fork(*c.all[2:], c.i32([0, 1]), c.i32([4, 4]), page_rows=1)):
+        assert call().item() == -1
+        assert P.spk_device_error(clear=True)[0] == E
+        c.check()

@@ -549,3 +549,54 @@ def test_one_long_sequence_among_many_short_ones(P, case):
         o, l = torch.full_like(out, 7.0), torch.full_like(lse2, 7.0)
         P.tree_attention(**t, out=o, lse2=l)
         assert torch.equal(o, out) and torch.equal(l, lse2)
+
+
+@pytest.mark.parametrize("case", [
+    # seed, dtype, B, hq, hkv, d, T, page, lens, live, mask: forms that the cases above leave out
+    (110, "fp16", 2, 8, 2, 128, 1, 16, [700, 1], None, "tree"),           # one token in fp16
+    (111, "fp16", 1, 8, 8, 64, 1, 24, [65], None, "chain"),
+    (112, "fp16", 2, 16, 2, 128, 33, 48, [300, 129], [33, 20], "tree"),   # 264 rows, fp16, head size 128
+    (113, "fp16", 1, 4, 1, 128, 40, 64, [5000], None, "random"),          # 160 rows, cut
+    (114, "bf16", 1, 2, 1, 64, 1024, 16, [77], None, "tree"),             # the most nodes: 2048 rows, 8 node tiles
+    (115, "bf16", 2, 1, 1, 128, 700, 8, [0, 333], [700, 513], "random"),
+    (116, "fp16", 1, 1, 1, 64, 257, 32, [96], [256], "chain"),
+], ids=[str(x) for x in range(110, 117)])
+def test_more_forms(P, case):
+    import torch
+    seed, dt, B, hq, hkv, d, T, page, lens, live, mask = case
+    dtype = torch.bfloat16 if dt == "bf16" else torch.float16
+    t, h = build_case(seed, dtype, B, 1, hq, hkv, d, T, page, lens, live, mask)
+    check(P, t, h, dtype)
+
+
+@pytest.mark.parametrize("T,hq", [(3, 4), (12, 16), (40, 16)], ids=["narrow", "wide", "pair"])
+@pytest.mark.parametrize("page", [24, 128])
+def test_pages_out_of_range_are_read_as_zeros_and_recorded(P, T, hq, page):
+    import torch
+    t, h = build_case(120 + T, torch.bfloat16, 2, 1, hq, 2, 64, T, page, [5 * page + 7, 100])
+    n_pages = t["k_pages"].shape[1]
+    zero = np.zeros_like(h["kp"][:, :1])
+    h["kp"], h["vp"] = np.concatenate([h["kp"], zero], 1), np.concatenate([h["vp"], zero], 1)
+    for at, bad in ((0, n_pages), (2, -1), (4, 0x7fffffff), (5, -0x80000000)):
+        t["page_table"][0, at] = bad
+        h["table"][0, at] = n_pages                                  # the zeros
+    out, lse2 = torch.full_like(t["q"], 7.0), torch.full(t["q"].shape[:-1], 7.0, device="cuda")
+    P.tree_attention(**t, out=out, lse2=lse2)
+    torch.cuda.synchronize()
+    assert P.spk_device_error(clear=True)[0] == P.binding.SPK_ERR_ARG
+    compare(out, lse2, h, torch.bfloat16)
+
+
+@pytest.mark.parametrize("T,hq", [(3, 4), (12, 16), (40, 16)], ids=["narrow", "wide", "pair"])
+@pytest.mark.parametrize("length", [-1, -0x80000000, 161, 0x7fffffff])
+def test_lengths_out_of_range_keep_their_rows_and_are_recorded(P, T, hq, length):
+    import torch
+    t, h = build_case(130 + T, torch.bfloat16, 3, 1, hq, 2, 64, T, 16, [140, 100, 9], spare=1)      # ten pages of 16 rows
+    assert t["page_table"].shape[1] == 10
+    t["seq_lens"][1] = length
+    h["live"] = [T, 0, T]                                            # element 1 has no rows
+    out, lse2 = torch.full_like(t["q"], 7.0), torch.full(t["q"].shape[:-1], 7.0, device="cuda")
+    P.tree_attention(**t, out=out, lse2=lse2)
+    torch.cuda.synchronize()
+    assert P.spk_device_error(clear=True)[0] == P.binding.SPK_ERR_ARG
+    compare(out, lse2, h, torch.bfloat16)
