@@ -90,9 +90,11 @@ def cascade_compress(draft_q, draft_k, row_weights, l_skip: int, keep: int, targ
 class PagedCache:
     """A paged KV cache on the device: k_pages, v_pages [L, n_pages, Hkv, page_rows,
     d], page_table int32 [n_seqs, max_pages], seq_lens int32 [n_seqs], page_refs
-    int32 [n_pages].  The methods are the operators of the same names; lists of
-    sequences are int32 tensors.  A layer at a time, tree_attention takes
-    k_pages[l:l+1] and v_pages[l:l+1]."""
+    int32 [n_pages].  The methods are the operators of the same names, and
+    append; lists of sequences are int32 tensors.  write alone takes it that there
+    was room: after a reserve that was refused it would go over rows the sequence
+    holds, unless that reserve's result is given as `reserved`.  A layer at a
+    time, tree_attention takes k_pages[l:l+1] and v_pages[l:l+1]."""
 
     def __init__(self, layers: int, n_pages: int, hkv: int, page_rows: int, head_dim: int, n_seqs: int, max_pages: int,
                  dtype=torch.bfloat16, device="cuda"):
@@ -113,6 +115,14 @@ class PagedCache:
 
     def write(self, k, v, seqs, **kw):
         B.kv_pages_write(k, v, *self.tensors, seqs, **kw)
+
+    def append(self, k, v, seqs, counts, idx=None, units_per_idx: int = 1, stream=None):
+        """Sequences seqs grow by counts int32 [n] rows and get them from k, v
+        (reserve and write as one): returns reserve's result; unless it is 0
+        nothing is changed."""
+        result = self.reserve(seqs, counts, stream=stream)
+        self.write(k, v, seqs, idx=idx, counts=counts, units_per_idx=units_per_idx, reserved=result, stream=stream)
+        return result
 
     def compact(self, src, dst, idx, **kw):
         return B.kv_pages_compact(*self.tensors, src, dst, idx, **kw)
@@ -148,6 +158,4 @@ def speckv_compress_pages(q, k, v, n_window: int, c_max: int, cache: PagedCache,
     B.topk_select(scores, c_max, n_window, idx, pool, None, None, stream, pool_mode)
     with torch.cuda.stream(B._stream_object(stream, q.device)):
         n_new = torch.full_like(seqs, keep)
-    result = cache.reserve(seqs, n_new, stream=stream)
-    cache.write(k, v, seqs, idx=idx, reserved=result, stream=stream)
-    return scores, idx, result
+    return scores, idx, cache.append(k, v, seqs, n_new, idx=idx, stream=stream)

@@ -31,11 +31,9 @@ def recorded(monkeypatch):
 class _Cache:
     k_pages = torch.zeros((2, 9, 2, 16, 64), dtype=torch.bfloat16)
 
-    def reserve(self, seqs, n_new, stream=None):
+    def append(self, k, v, seqs, counts, idx=None, stream=None):
+        self.idx = idx
         return torch.zeros(1, dtype=torch.int32)
-
-    def write(self, k, v, seqs, **kw):
-        self.wrote = kw
 
 
 def _inputs():
@@ -49,7 +47,7 @@ def test_scores_and_rows_of_speckv_compress_pages_belong_to_both_streams(recorde
     cache, seqs = _Cache(), torch.zeros(1, dtype=torch.int32)
     scores, idx, _ = pipeline.speckv_compress_pages(*_inputs(), 16, 32, cache, seqs, stream=1234)
     known = {id(t) for t in made}
-    assert id(scores) in known and id(idx) in known and id(cache.wrote["idx"]) in known
+    assert id(scores) in known and id(idx) in known and id(cache.idx) in known
     assert {id(t) for t in used} <= known
 
 
