@@ -630,7 +630,11 @@ cudaError_t launch_join(const TreeParams& p, const TreePlan& plan, cudaStream_t 
   const long long items = static_cast<long long>(p.batch) * p.layers * p.hkv * plan.items;
   const bool by_border = items > plan.ctas - 1;
   const int rows = p.rows < plan.item_rows ? p.rows : plan.item_rows;
-  const bool many = items * 16 <= plan.ctas;    // many shares an item
+  // Many shares an item.  The join for few shares and the one for many, us: one node
+  // over 16K rows, 2 items 32.5 and 11.1; 8 items 25.8 and 19.5; 16 items 32.1 and
+  // 29.2; over 8K rows, 32 items 32.6 and 30.1, 64 items 51.0 and 53.8; 16 nodes
+  // (148 CTAs), 8 items 30.4 and 29.7, 16 items 29.0 and 33.2, 32 items 38.8 and 49.1.
+  const bool many = items * 16 <= plan.ctas;
   cudaLaunchConfig_t cfg = {};
   // blocks that are resident together, beside the main kernel's: six an SM
   const unsigned x = by_border ? plan.ctas - 1 : static_cast<unsigned>(items);
@@ -733,7 +737,12 @@ __global__ void __launch_bounds__(128) tree_mask_kernel(const int* __restrict__ 
 }  // namespace
 
 // Up to 32 rows a unit fit one narrow tile, which wastes less than a tile of
-// 128 rows; above that the tcgen05 kernel.
+// 128 rows; above that the tcgen05 kernel.  Narrow and wide, us, of 8 KV heads:
+//   rows a unit                        10         16         24         32         33         64
+//   16 sequences of 4096 rows       52,  53    51,  53    66,  54    68,  55   124,  57   126,  58
+//   one of 16,384 rows              21,  26    21,  26    26,  26    27,  26    43,  27    44,  30
+//   64 layers over 320 rows         27,  41    28,  40    39,  40    41,  40    65,  41    69,  39
+// (between 17 and 32 rows the wide kernel gains on long sequences in batches only)
 TreePlan tree_plan(int rows, int head_dim, int sms) {
   TreePlan plan;
   plan.wide = rows > 32;
