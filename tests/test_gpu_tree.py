@@ -284,12 +284,25 @@ def test_nodes_that_a_row_does_not_see_may_hold_anything(P, T, hq, lens, dt):
                                        (40, 16, [3000, 50]), (150, 8, [2500])],
                          ids=["narrow", "narrow-cut", "wide", "wide-cut", "pair", "pair-cut", "nodes-cut"])
 def test_what_is_not_finite_adds_up_whole_or_cut(P, T, hq, lens, dt):
+    import torch
+    dtype = torch.bfloat16 if dt == "bf16" else torch.float16
+    t, h = build_case(70 + T, dtype, len(lens), 1, hq, 2, 64, T, 32, lens, mask="random")
+    not_finite_adds_up(P, t, h)
+
+
+@pytest.mark.parametrize("B,hq,T,most", [(80, 16, 3, 700), (40, 32, 10, 900), (40, 64, 20, 900)], ids=["narrow", "wide", "pair"])
+def test_what_is_not_finite_adds_up_where_the_main_kernel_joins(P, B, hq, T, most):
+    import torch
+    rng = np.random.default_rng(170 + T)
+    t, h = build_case(170 + T, torch.bfloat16, B, 1, hq, 8, 64, T, 32, [int(x) for x in rng.integers(40, most, B)], mask="random")
+    not_finite_adds_up(P, t, h)
+
+
+def not_finite_adds_up(P, t, h):
     # in one share or in many: NaN logits beside an infinite V, infinities of both signs,
     # an infinite V whose weight is too small for 32 bits
     import torch
-    dtype = torch.bfloat16 if dt == "bf16" else torch.float16
-    B = len(lens)
-    t, h = build_case(70 + T, dtype, B, 1, hq, 2, 64, T, 32, lens, mask="random")
+    B, T = t["q"].shape[0], t["q"].shape[3]
     t["q"] = t["q"].abs()
     t["mask"][:, :, 0] &= ~4                                         # odd nodes see node 2, even ones do not
     t["mask"][:, 1::2, 0] |= 4
