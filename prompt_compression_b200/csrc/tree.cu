@@ -16,11 +16,11 @@
 // an item is then in two shares at most; one long sequence among short ones is
 // in many, which costs time but is right.  Otherwise tree_join_kernel does it,
 // which spreads the many shares of an item over the GPU.
-// (16 nodes over 320 rows, 512 KV heads: 38 us the one way, 43 the other; one
-// node over 16K rows, 8 KV heads in 37 shares each: 37 and 20 us.  One sequence
-// of 65,536 rows among 79 of 300, 8 KV heads, one node, 22 shares a long item,
-// joined inside: 76 us; the long one by itself 49, the others 30.  One of 16K
-// rows beside 73 elements without a live node, 32 shares: 37 us, by itself 20.)
+// (The one way and the other, us: 16 nodes over 320 rows, 512 KV heads, 39.5 and
+// 45.2; one node over 16K rows, 8 KV heads in 37 shares each, 41.2 and 20.2; over
+// 80 sequences of 1500 rows 86.3 and 84.8; over 79 sequences of 300 rows and one of
+// 65,536, whose items lie in 22 shares, 75.5 and 68.6.  One of 16K rows beside 73
+// elements without a live node, about 32 shares: 37 joined inside, 20 by itself.)
 #include <type_traits>
 
 #include "common.cuh"

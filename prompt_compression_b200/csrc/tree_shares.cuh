@@ -137,15 +137,14 @@ __device__ __forceinline__ TreeStart tree_start(const TreeParams& p, int cta, bo
     full += e.tiles > 0;
   }
   jobs = __reduce_add_sync(0xffffffffu, jobs);
-  // What starting an item costs (Q, the first loads, the outputs: 4 to 5 us against
-  // 1.1 us a job) goes into the line as jobs in front of its tiles, where shares
-  // are long enough: otherwise the CTAs whose share falls on many short sequences
-  // end last.  (16 ragged sequences of up to 8192 rows, 24 nodes: 70.6 us without,
-  // 58.5 us with; 61.4 and 59.5 us for 2 and 6 jobs.  Narrow kernel, 64 sequences
-  // of up to 2048 rows, 8 nodes: 93.8 us without, 68.2 us with; 71.4 us for 6 jobs.
-  // Below four jobs a share the start of an item could fill a share.  From four on
-  // against from eight on: 24 sequences of up to 1000 rows, 24 nodes: 32.6 and 45.9
-  // us; two of 6000 rows each, 24 nodes: 29.6 and 29.1 us.)
+  // What starting an item costs (Q, the first loads, the outputs: 4 to 5 us) goes
+  // into the line as jobs in front of its tiles, where shares are long enough:
+  // otherwise the CTAs whose share falls on many short sequences end last.  With
+  // 0, 2, 4 and 6 jobs: 16 ragged sequences of up to 8192 rows, 24 nodes, 73.5,
+  // 63.6, 60.2, 60.7 us; narrow kernel, 64 sequences of up to 2048 rows, 8 nodes,
+  // 109.8, 82.9, 76.2, 78.3; 24 sequences of up to 1000 rows, 24 nodes, 51.1, 36.5,
+  // 35.9, 51.3; two of 6000 rows, 24 nodes, 26.6, 27.6, 27.7, 26.8.  (Below as many
+  // jobs a share as an item starts with, the start could fill a share.)
   s.extra = jobs / p.ctas >= kTreeItemJobs ? kTreeItemJobs : 0;
   s.total = jobs;
   if (s.extra > 0) s.total += __reduce_add_sync(0xffffffffu, full) * s.extra * p.items * p.layers * p.hkv;
