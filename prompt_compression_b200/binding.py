@@ -635,7 +635,8 @@ def tree_attention(q, k_pages, v_pages, page_table, seq_lens, k_tree=None, v_tre
     that mask int32 [B, T, ceil(T/32)] lets each see (None: a chain).  seqs
     int32 [B]: the elements' sequences (None: 0 .. B-1); n_live int32 [B]: how
     many of the tokens count (None: T).  Returns out [B, L, Hq, T, d]; fills
-    lse2 fp32 [B, L, Hq, T] when given."""
+    lse2 fp32 [B, L, Hq, T] when given.  The weights enter the product with V
+    rounded to q's type (decode_attention's with 16 bits)."""
     handle = None
     if stream is not None:
         handle = _handle(stream, q)
