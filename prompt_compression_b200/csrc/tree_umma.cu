@@ -4,7 +4,8 @@
 // this kernel takes over where a unit has more query rows than a narrow
 // mma.sync tile holds.  Tiles are 128 query rows by 128 keys:
 //   S = Q K^T   A = Q, B = K from shared memory, S in TMEM (fp32)
-//   O += P V    A = P from TMEM (16-bit, over the second half of S), B = V from
+//   O += P V    A = P from TMEM (in the element type's 16 bits, as tree_kernel's
+//               is, and over the second half of S), B = V from
 //               shared memory as it lies ([key][d], MN-major), O in TMEM
 // with two softmax groups of four warps (thread = query row), so that one
 // group's exponentials run under the other's products.  Rows of a unit are

@@ -613,3 +613,14 @@ def test_lengths_out_of_range_keep_their_rows_and_are_recorded(P, T, hq, length)
     torch.cuda.synchronize()
     assert P.spk_device_error(clear=True)[0] == P.binding.SPK_ERR_ARG
     compare(out, lse2, h, torch.bfloat16)
+
+
+@pytest.mark.parametrize("T,hq", [(3, 4), (12, 16), (40, 16)], ids=["narrow", "wide", "pair"])
+def test_no_keys_at_all(P, T, hq):
+    # an empty sequence beside one with rows, and no nodes to see: zeros, and -inf
+    import torch
+    t, h = build_case(140 + T, torch.bfloat16, 3, 2, hq, 2, 64, T, 16, [0, 140, 0], tree=False)
+    out, lse2 = check(P, t, h, torch.bfloat16)
+    assert (out[0] == 0).all() and torch.isneginf(lse2[0]).all()
+    t, h = build_case(141 + T, torch.float16, 1, 1, hq, 2, 128, T, 16, [0], tree=False)
+    check(P, t, h, torch.float16)
